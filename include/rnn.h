@@ -362,6 +362,105 @@ rnn_status_t rnn_device_status(rnn_handle_t h, void* stream, const void* ws, siz
 rnn_status_t rnn_set_profiling(rnn_handle_t h, int enable);
 rnn_status_t rnn_profile_read(rnn_handle_t h, int kernel, long long* launches, double* total_ms);
 
+/* ------------------------------------------------ language-model operators
+ * Three operators that surround the recurrent layers in a recurrent language
+ * model.  They keep no state on the host and need no handle.  `wtype` is the
+ * element type of the activations and weights they take and write
+ * (RNN_W_F32 or RNN_W_BF16); recurrent states are always fp32, and every sum,
+ * state and activation is computed in fp32.  All tensors are contiguous.
+ * Buffers may have any alignment that their element type allows (workspaces,
+ * reserves and checkpoints: 256 bytes).  Two calls that share a workspace
+ * must not run at the same time.  Every call only enqueues on `stream`, can
+ * be captured into a HIP graph, and gives bitwise the same results for the
+ * same inputs.
+ *
+ * Common errors: INVALID_ARG for an unknown enum value, a negative size or a
+ * NULL pointer to a non-empty required buffer, a misaligned workspace,
+ * reserve or checkpoint; WORKSPACE_TOO_SMALL for a buffer below its queried
+ * size; UNSUPPORTED where a dimension or a product of the sizes does not fit
+ * the kernels' 32-bit indexes (stated at each call); DEVICE for a failed
+ * launch. */
+
+/* Gated linear recurrence over T steps:  h_t = a_t * h_(t-1) + b_t,  with
+ *   RNN_SCAN_GATED   a = sigmoid(p), b = sigmoid(-p) * tanh(q)
+ *   RNN_SCAN_LINEAR  a = p,          b = q
+ * g [T, B, dirs * 2 * H] holds, for each direction, H columns p and H columns
+ * q; y [T, B, dirs * H]; h0, hy [dirs, B, H] fp32.  Direction 1 walks from the
+ * last step to the first.  `lengths` (device, int32 [B], or NULL) as in
+ * rnn_set_sequence_lengths: past a row's length the state is carried, y is 0,
+ * and g is not used (whatever it holds). */
+typedef enum RNN_ENUM_BASE { RNN_SCAN_GATED = 0, RNN_SCAN_LINEAR = 1 } rnn_scan_mode_t;
+
+/* Bytes of the workspace of one forward call and the backward calls that
+ * follow it.  UNSUPPORTED: B * H * dirs >= 2^30. */
+rnn_status_t rnn_scan_workspace_size(int T, int B, int H, int dirs, size_t* bytes);
+
+/* One step of one direction (a generated token): g [B, 2 * H], h [B, H] (NULL:
+ * zeros), y [B, H] in the element type (or NULL), hy [B, H] fp32, which may
+ * be h itself. */
+rnn_status_t rnn_scan_step(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int B, int H, const void* g,
+                           const float* h, void* y, float* hy);
+
+/* All steps.  h0 NULL: zeros; hy NULL: not wanted.  The workspace then holds
+ * what rnn_scan_backward reads.  The time axis is split among workgroups that
+ * pass the state on; a workgroup whose bounded wait for the state expires
+ * sets the workspace's first 32-bit word and carries on with NaN, so that
+ * every workgroup ends. */
+rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
+                              const void* g, const float* h0, const int* lengths, void* y, float* hy, void* ws,
+                              size_t ws_bytes);
+
+/* Gradients of a forward call with the same mode, sizes, g, h0, lengths and
+ * workspace (which may have been followed by other backward calls, but by no
+ * other forward call).  dy [T, B, dirs * H]; dhy [dirs, B, H] fp32 or NULL
+ * (zeros); dg as g; dh0 as h0 or NULL. */
+rnn_status_t rnn_scan_backward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
+                               const void* g, const float* h0, const int* lengths, const void* dy, const float* dhy,
+                               void* dg, float* dh0, void* ws, size_t ws_bytes);
+
+/* Gated feed-forward block over M rows:
+ *   y = (act(x Wg^T) * (x Wu^T)) w_out^T,   w_in = [Wg; Wu]
+ * x, y [M, D]; w_in [2F, D] (F gate rows, then F up rows); w_out [D, F].
+ * RNN_ACT_GELU is the tanh form. */
+typedef enum RNN_ENUM_BASE { RNN_ACT_SIGMOID = 0, RNN_ACT_SILU = 1, RNN_ACT_GELU = 2 } rnn_act_t;
+
+/* What the forward call leaves in the reserve for the backward call:
+ *   RNN_SAVE_NONE   nothing (inference)
+ *   RNN_SAVE_FULL   the projections and the gated product
+ *   RNN_SAVE_INT8   x and the projections as 8-bit checkpoints (the format of
+ *                   rnn_checkpoint_store); backward then needs no x */
+typedef enum RNN_ENUM_BASE { RNN_SAVE_NONE = 0, RNN_SAVE_FULL = 1, RNN_SAVE_INT8 = 2 } rnn_save_t;
+
+/* UNSUPPORTED: D or F >= 2^24, or M >= 2^30. */
+rnn_status_t rnn_ffn_workspace_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
+rnn_status_t rnn_ffn_reserve_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
+
+rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn_save_t save, int M, int D, int F,
+                             const void* x, const void* w_in, const void* w_out, void* y, void* ws, size_t ws_bytes,
+                             void* reserve, size_t reserve_bytes);
+
+/* Gradients; the reserve of a forward call with the same arguments (read
+ * only, so it may be used again).  x may be NULL with RNN_SAVE_INT8 and is
+ * not read then.  dx, dw_in and dw_out as x, w_in and w_out; each may be NULL
+ * (not wanted).  INVALID_ARG for RNN_SAVE_NONE. */
+rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn_save_t save, int M, int D, int F,
+                              const void* x, const void* w_in, const void* w_out, const void* dy, void* dx,
+                              void* dw_in, void* dw_out, void* ws, size_t ws_bytes, const void* reserve,
+                              size_t reserve_bytes);
+
+/* A matrix [rows, cols] kept in 8 bits a value: each group of 32 columns of a
+ * row (the last may be shorter) shares a power of two 2^e, and a value is
+ * held as round(v / 2^e), ties to even, within -127 .. 127.  e is the
+ * exponent that puts the group's largest magnitude into [64, 128) units, at
+ * least -126.  Layout: rows * cols signed bytes, then rows * ceil(cols / 32)
+ * signed exponents.  A group that holds an infinity or a NaN has the exponent
+ * byte -128 and reads back as NaN throughout.  UNSUPPORTED: cols >= 2^30. */
+rnn_status_t rnn_checkpoint_size(int rows, int cols, size_t* bytes);
+rnn_status_t rnn_checkpoint_store(void* stream, rnn_wtype_t wtype, int rows, int cols, const void* x, void* kept,
+                                  size_t kept_bytes);
+rnn_status_t rnn_checkpoint_load(void* stream, rnn_wtype_t wtype, int rows, int cols, const void* kept,
+                                 size_t kept_bytes, void* x);
+
 /* Static text for a status code. */
 const char* rnn_status_string(rnn_status_t s);
 

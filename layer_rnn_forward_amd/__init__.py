@@ -44,6 +44,17 @@ from ._binding import (  # noqa: F401
     rnn_set_profiling,
     rnn_profile_read,
     rnn_status_string,
+    rnn_scan_workspace_size,
+    rnn_scan_step,
+    rnn_scan_forward,
+    rnn_scan_backward,
+    rnn_ffn_workspace_size,
+    rnn_ffn_reserve_size,
+    rnn_ffn_forward,
+    rnn_ffn_backward,
+    rnn_checkpoint_size,
+    rnn_checkpoint_store,
+    rnn_checkpoint_load,
     pack_weights,
     unpack_weights,
     SCHED_AUTO,

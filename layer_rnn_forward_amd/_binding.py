@@ -10,6 +10,9 @@ import torch
 
 MODES = {"rnn_tanh": 0, "lstm": 1, "gru": 2, "gru_tf": 3, "gru_paper": 4}
 WTYPES = {"f32": 0, "bf16": 1}
+SCAN_MODES = {"gated": 0, "linear": 1}
+ACTS = {"sigmoid": 0, "silu": 1, "gelu": 2}
+SAVES = {"none": 0, "full": 1, "int8": 2}
 SCHED_AUTO, SCHED_PERSISTENT, SCHED_STEPPED = 0, 1, 2
 KERNEL_NAMES = ["gemm_input", "recurrent_fwd", "recurrent_bwd", "gemm_dx", "gemm_dw", "fill", "prep",
                 "exchange_probe", "dropout"]
@@ -66,6 +69,17 @@ def load_library():
         "rnn_plan_info": [vp, i, i, i, ctypes.POINTER(ctypes.c_int)],
         "rnn_set_profiling": [vp, i],
         "rnn_profile_read": [vp, i, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(ctypes.c_double)],
+        "rnn_scan_workspace_size": [i, i, i, i, psz],
+        "rnn_scan_step": [vp, i, i, i, i, vp, vp, vp, vp],
+        "rnn_scan_forward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, sz],
+        "rnn_scan_backward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, sz],
+        "rnn_ffn_workspace_size": [i, i, i, i, i, psz],
+        "rnn_ffn_reserve_size": [i, i, i, i, i, psz],
+        "rnn_ffn_forward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, sz, vp, sz],
+        "rnn_ffn_backward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, sz],
+        "rnn_checkpoint_size": [i, i, psz],
+        "rnn_checkpoint_store": [vp, i, i, i, vp, vp, sz],
+        "rnn_checkpoint_load": [vp, i, i, i, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -293,6 +307,196 @@ def rnn_profile_read(h, kernel: int):
     _check(load_library().rnn_profile_read(h.ptr, int(kernel), ctypes.byref(n), ctypes.byref(ms)),
            "rnn_profile_read")
     return n.value, ms.value
+
+
+# ------------------------------------------------- language-model operators
+_WTYPE_OF = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _addr(t, name, dtype, shape, optional=False):
+    """Device address of ``t`` after its checks (None: NULL where optional)."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor" + (" or None" if optional else ""))
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _room(t, name, optional=False):
+    """Address and size in bytes of a workspace, reserve or checkpoint."""
+    if t is None and optional:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _elements(t, name, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _WTYPE_OF:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.dtype, _WTYPE_OF[t.dtype]
+
+
+def _choice(table, key, name):
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {key!r}") from None
+
+
+def rnn_scan_workspace_size(T: int, B: int, H: int, num_dirs: int = 1) -> int:
+    """Bytes of the workspace that one rnn_scan_forward fills and the
+    rnn_scan_backward calls after it read."""
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_scan_workspace_size(T, B, H, num_dirs, ctypes.byref(n)), "rnn_scan_workspace_size")
+    return n.value
+
+
+def rnn_scan_step(mode, g, h, y, hy):
+    """One step of the gated linear recurrence (a generated token):
+    ``g`` [B, 2H]; ``h`` (or None: zeros) and ``hy`` [B, H] float32, which may
+    be the same tensor; ``y`` [B, H] in g's type, or None."""
+    m = _choice(SCAN_MODES, mode, "mode")
+    dt, w = _elements(g, "g", 2)
+    B, H2 = g.shape
+    if H2 % 2:
+        raise ValueError("g must have an even number of columns")
+    bh = (B, H2 // 2)
+    _check(load_library().rnn_scan_step(
+        _stream(), m, w, B, H2 // 2, _addr(g, "g", dt, g.shape), _addr(h, "h", torch.float32, bh, True),
+        _addr(y, "y", dt, bh, True), _addr(hy, "hy", torch.float32, bh)), "rnn_scan_step")
+
+
+def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
+    """The gated linear recurrence h[t] = a[t] h[t-1] + b[t] over ``g``
+    [T, B, dirs*2*H] (for each direction H columns p, then H columns q):
+    "gated" a = sigmoid(p), b = sigmoid(-p) tanh(q); "linear" a = p, b = q.
+    ``y`` [T, B, dirs*H]; ``hy`` [dirs, B, H] float32 (its shape gives dirs
+    and H); ``h0`` as hy, or None (zeros); ``lengths`` int32 [B] or None."""
+    m = _choice(SCAN_MODES, mode, "mode")
+    dt, w = _elements(g, "g", 3)
+    if not isinstance(hy, torch.Tensor) or hy.dim() != 3:
+        raise ValueError("hy must be a tensor [dirs, B, H]")
+    T, B = g.shape[:2]
+    D, H = hy.shape[0], hy.shape[2]
+    st = (D, B, H)
+    wp, wn = _room(ws, "ws")
+    _check(load_library().rnn_scan_forward(
+        _stream(), m, w, T, B, H, D, _addr(g, "g", dt, (T, B, D * 2 * H)),
+        _addr(h0, "h0", torch.float32, st, True), _addr(lengths, "lengths", torch.int32, (B,), True),
+        _addr(y, "y", dt, (T, B, D * H)), _addr(hy, "hy", torch.float32, st), wp, wn), "rnn_scan_forward")
+
+
+def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
+    """Gradients of the rnn_scan_forward call that filled ``ws`` (same mode, g,
+    h0 and lengths): ``dy`` [T, B, dirs*H], ``dhy`` as hy or None (zeros);
+    ``dg`` as g, ``dh0`` [dirs, B, H] float32 (its shape gives dirs and H)."""
+    m = _choice(SCAN_MODES, mode, "mode")
+    dt, w = _elements(g, "g", 3)
+    if not isinstance(dh0, torch.Tensor) or dh0.dim() != 3:
+        raise ValueError("dh0 must be a tensor [dirs, B, H]")
+    T, B = g.shape[:2]
+    D, H = dh0.shape[0], dh0.shape[2]
+    st = (D, B, H)
+    wp, wn = _room(ws, "ws")
+    _check(load_library().rnn_scan_backward(
+        _stream(), m, w, T, B, H, D, _addr(g, "g", dt, (T, B, D * 2 * H)),
+        _addr(h0, "h0", torch.float32, st, True), _addr(lengths, "lengths", torch.int32, (B,), True),
+        _addr(dy, "dy", dt, (T, B, D * H)), _addr(dhy, "dhy", torch.float32, st, True),
+        _addr(dg, "dg", dt, (T, B, D * 2 * H)), _addr(dh0, "dh0", torch.float32, st), wp, wn), "rnn_scan_backward")
+
+
+def rnn_ffn_workspace_size(M: int, D: int, F: int, wtype: str, save: str = "none") -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_ffn_workspace_size(M, D, F, _choice(WTYPES, wtype, "wtype"),
+                                                 _choice(SAVES, save, "save"), ctypes.byref(n)),
+           "rnn_ffn_workspace_size")
+    return n.value
+
+
+def rnn_ffn_reserve_size(M: int, D: int, F: int, wtype: str, save: str = "none") -> int:
+    """Bytes that rnn_ffn_forward keeps for rnn_ffn_backward (0 for "none")."""
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_ffn_reserve_size(M, D, F, _choice(WTYPES, wtype, "wtype"),
+                                               _choice(SAVES, save, "save"), ctypes.byref(n)),
+           "rnn_ffn_reserve_size")
+    return n.value
+
+
+def rnn_ffn_forward(act, x, w_in, w_out, y, ws, save="none", reserve=None):
+    """The gated feed-forward block y = (act(x Wg^T) * (x Wu^T)) w_out^T with
+    w_in = [Wg; Wu]: ``x``, ``y`` [M, D], ``w_in`` [2F, D], ``w_out`` [D, F],
+    all float32 or all bfloat16; act "sigmoid", "silu" or "gelu" (tanh form);
+    save "none", "full" or "int8": what ``reserve`` keeps for backward."""
+    a, sv = _choice(ACTS, act, "act"), _choice(SAVES, save, "save")
+    dt, w = _elements(x, "x", 2)
+    _elements(w_out, "w_out", 2)
+    M, D = x.shape
+    F = w_out.shape[1]
+    wp, wn = _room(ws, "ws")
+    rp, rn = _room(reserve, "reserve", True)
+    _check(load_library().rnn_ffn_forward(
+        _stream(), a, w, sv, M, D, F, _addr(x, "x", dt, (M, D)), _addr(w_in, "w_in", dt, (2 * F, D)),
+        _addr(w_out, "w_out", dt, (D, F)), _addr(y, "y", dt, (M, D)), wp, wn, rp, rn), "rnn_ffn_forward")
+
+
+def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reserve):
+    """Gradients of the rnn_ffn_forward call that filled ``reserve``; ``x`` may
+    be None with save "int8"; each of ``dx``, ``dw_in`` and ``dw_out`` may be
+    None (not wanted)."""
+    a, sv = _choice(ACTS, act, "act"), _choice(SAVES, save, "save")
+    dt, w = _elements(dy, "dy", 2)
+    _elements(w_out, "w_out", 2)
+    M, D = dy.shape
+    F = w_out.shape[1]
+    wp, wn = _room(ws, "ws")
+    rp, rn = _room(reserve, "reserve")
+    _check(load_library().rnn_ffn_backward(
+        _stream(), a, w, sv, M, D, F, _addr(x, "x", dt, (M, D), True), _addr(w_in, "w_in", dt, (2 * F, D)),
+        _addr(w_out, "w_out", dt, (D, F)), _addr(dy, "dy", dt, (M, D)), _addr(dx, "dx", dt, (M, D), True),
+        _addr(dw_in, "dw_in", dt, (2 * F, D), True), _addr(dw_out, "dw_out", dt, (D, F), True), wp, wn, rp, rn),
+        "rnn_ffn_backward")
+
+
+def rnn_checkpoint_size(rows: int, cols: int) -> int:
+    """Bytes of the 8-bit checkpoint of a matrix [rows, cols]."""
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_checkpoint_size(rows, cols, ctypes.byref(n)), "rnn_checkpoint_size")
+    return n.value
+
+
+def rnn_checkpoint_store(x, kept):
+    """Keep ``x`` [rows, cols] in 8 bits a value with one power of two per 32
+    columns of a row, in the buffer ``kept``."""
+    dt, w = _elements(x, "x", 2)
+    kp, kn = _room(kept, "kept")
+    _check(load_library().rnn_checkpoint_store(_stream(), w, x.shape[0], x.shape[1], _addr(x, "x", dt, x.shape),
+                                               kp, kn), "rnn_checkpoint_store")
+
+
+def rnn_checkpoint_load(kept, x):
+    """Read a checkpoint of a matrix of x's shape back into ``x`` [rows, cols]
+    (float32 or bfloat16; both hold its values exactly)."""
+    dt, w = _elements(x, "x", 2)
+    kp, kn = _room(kept, "kept")
+    _check(load_library().rnn_checkpoint_load(_stream(), w, x.shape[0], x.shape[1], kp, kn,
+                                              _addr(x, "x", dt, x.shape)), "rnn_checkpoint_load")
 
 
 # ------------------------------------------------------------ weight packing

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librnn_mi355x.so")
-SOURCES = ["dropout.hip", "gemm.hip", "layout.hip", "recurrent.hip", "recurrent_gru2.hip", "rnn_api.cpp",
+SOURCES = ["checkpoint.hip", "dropout.hip", "ffn.hip", "gemm.hip", "layout.hip", "lm_api.cpp", "recurrent.hip",
+           "recurrent_gru2.hip", "rnn_api.cpp", "scan.hip",
            *[f"recurrent_{m}_{k}.hip" for m in ("tanh", "lstm", "gru") for k in ("fwd", "bwd")]]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -48,8 +49,8 @@ def _run(cmd):
     return out
 
 
-# host-only sanitizers for the C-ABI translation unit (the planner and its
-# workspace carve); device code is built as usual
+# host-only sanitizers for the C-ABI translation units (the planners and their
+# workspace carves); device code is built as usual
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
 SAN_LIB = os.path.join(BUILD, "sanitize", "librnn_mi355x_san.so")
@@ -65,7 +66,7 @@ def _build(out_lib: str, obj_dir: str, sanitize: bool, verbose: bool, defines=()
         obj = os.path.join(obj_dir, src.replace(".", "_") + ".o")
         objs.append(obj)
         extra = ["-x", "hip"] if src.endswith(".cpp") else []
-        san = SANITIZE if (sanitize and src == "rnn_api.cpp") else []
+        san = SANITIZE if (sanitize and src.endswith("_api.cpp")) else []
         cmds.append([HIPCC, *FLAGS, *defines, *EXTRA.get(src, []), *san, *extra, "-c", os.path.join(CSRC, src),
                      "-o", obj])
     with ThreadPoolExecutor(max_workers=min(16, len(cmds))) as ex:
