@@ -431,7 +431,7 @@ typedef enum RNN_ENUM_BASE { RNN_ACT_SIGMOID = 0, RNN_ACT_SILU = 1, RNN_ACT_GELU
  *                   rnn_checkpoint_store); backward then needs no x */
 typedef enum RNN_ENUM_BASE { RNN_SAVE_NONE = 0, RNN_SAVE_FULL = 1, RNN_SAVE_INT8 = 2 } rnn_save_t;
 
-/* UNSUPPORTED: D or F >= 2^24, or M >= 2^30. */
+/* UNSUPPORTED: D or F >= 2^20, or M >= 2^30. */
 rnn_status_t rnn_ffn_workspace_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
 rnn_status_t rnn_ffn_reserve_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
 

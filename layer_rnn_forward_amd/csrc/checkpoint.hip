@@ -37,7 +37,8 @@ __global__ __launch_bounds__(256) void store_kernel(int rows, int cols, const vo
 }
 
 template <bool BF16>
-__global__ __launch_bounds__(256) void load_kernel(int rows, int cols, const int8_t* q, const int8_t* ex, void* xv) {
+__global__ __launch_bounds__(256) void load_kernel(int rows, int cols, const int8_t* q, const int8_t* ex, void* xv,
+                                                   long long ld) {
   const int gpr = (cols + kGroup - 1) / kGroup;
   const long long groups = (long long)rows * gpr;
   const long long step = (long long)gridDim.x * 8;
@@ -48,7 +49,9 @@ __global__ __launch_bounds__(256) void load_kernel(int rows, int cols, const int
     if (c < cols) {
       const float v = e == kNanGroup ? __uint_as_float(0x7fc00000u)
                                      : (float)q[r * cols + c] * __uint_as_float((unsigned)(127 + e) << 23);
-      el_store<BF16>((El<BF16>*)xv + r * cols + c, v);
+      el_store<BF16>((El<BF16>*)xv + r * ld + c, v);
+    } else if (c < ld) {
+      el_store<BF16>((El<BF16>*)xv + r * ld + c, 0.f);
     }
   }
 }
@@ -70,12 +73,12 @@ hipError_t rnn_launch_ckpt_store(int bf16, int rows, int cols, const void* x, vo
   return hipGetLastError();
 }
 
-hipError_t rnn_launch_ckpt_load(int bf16, int rows, int cols, const void* kept, void* x, hipStream_t s) {
+hipError_t rnn_launch_ckpt_load(int bf16, int rows, int cols, const void* kept, void* x, long long ld, hipStream_t s) {
   if (rows == 0 || cols == 0) return hipSuccess;
   const int8_t* q = (const int8_t*)kept;
   const int8_t* ex = q + (long long)rows * cols;
   const dim3 grid(grid_for(rows, cols));
-  if (bf16) hipLaunchKernelGGL(load_kernel<true>, grid, dim3(256), 0, s, rows, cols, q, ex, x);
-  else hipLaunchKernelGGL(load_kernel<false>, grid, dim3(256), 0, s, rows, cols, q, ex, x);
+  if (bf16) hipLaunchKernelGGL(load_kernel<true>, grid, dim3(256), 0, s, rows, cols, q, ex, x, ld);
+  else hipLaunchKernelGGL(load_kernel<false>, grid, dim3(256), 0, s, rows, cols, q, ex, x, ld);
   return hipGetLastError();
 }

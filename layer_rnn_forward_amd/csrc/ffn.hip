@@ -1,102 +1,75 @@
-// Products and activations of the gated feed-forward block (gfx950).
-//
-// mat_kernel: one 64 x 64 tile per workgroup, staged through LDS as fp32;
-// any strides.
+// Launches of the gated feed-forward block's products (ffn_gemm.h), and the
+// copy that pads rows which are not whole 16-byte pieces.
 #include <algorithm>
-#include <type_traits>
 
-#include "lm_math.h"
+#include "ffn_gemm.h"
 
 using namespace rnnk;
 
 namespace {
 
-template <bool AB, bool BB, bool CB>
-__global__ __launch_bounds__(256) void mat_kernel(const MatParams p) {
-  __shared__ float as[16][65], bs[16][65];
-  const El<AB>* A = (const El<AB>*)p.A;
-  const El<BB>* B = (const El<BB>*)p.B;
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int tid = threadIdx.x, tm = tid / 16 * 4, tn = tid % 16 * 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += 16) {
-    for (int i = tid; i < 64 * 16; i += 256) {
-      // the operand's contiguous axis along the lanes
-      const int ra = p.sak == 1 ? i / 16 : i % 64, ka = p.sak == 1 ? i % 16 : i / 64;
-      const int rb = p.sbk == 1 ? i / 16 : i % 64, kb = p.sbk == 1 ? i % 16 : i / 64;
-      as[ka][ra] = m0 + ra < p.M && k0 + ka < p.K ? el_load<AB>(A + (m0 + ra) * p.sam + (k0 + ka) * p.sak) : 0.f;
-      bs[kb][rb] = n0 + rb < p.N && k0 + kb < p.K ? el_load<BB>(B + (n0 + rb) * p.sbn + (k0 + kb) * p.sbk) : 0.f;
-    }
-    __syncthreads();
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][tm + i], bs[k][tn + j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j)
-      if (m0 + tm + i < p.M && n0 + tn + j < p.N)
-        el_store<CB>((El<CB>*)p.C + (m0 + tm + i) * p.ldc + n0 + tn + j, acc[i][j]);
-}
-
-template <bool BF16, int ACT>
-__global__ __launch_bounds__(256) void act_kernel(int M, int F, const float* gu, void* h) {
-  const long long n = (long long)M * F;
+template <bool BF>
+__global__ __launch_bounds__(256) void pad_kernel(const PadJob j) {
+  const int z = blockIdx.z;
+  const El<BF>* src = (const El<BF>*)j.src[z];
+  El<BF>* dst = (El<BF>*)j.dst[z];
+  const int cols = j.cols[z], ld = j.ld[z];
+  const long long n = j.rows[z] * ld;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long m = i / F, f = i - m * F;
-    float a, da;
-    act_pair<ACT>(gu[m * 2 * F + f], a, da);
-    el_store<BF16>((El<BF16>*)h + i, a * gu[m * 2 * F + F + f]);
+    const long long r = i / ld;
+    const int c = (int)(i - r * ld);
+    dst[i] = c < cols ? src[r * cols + c] : (El<BF>)0;
   }
 }
 
-template <bool BF16, int ACT>
-__global__ __launch_bounds__(256) void act_bwd_kernel(int M, int F, const float* gu, const float* dh, void* dgu) {
-  const long long n = (long long)M * F;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long m = i / F, f = i - m * F;
-    float a, da;
-    act_pair<ACT>(gu[m * 2 * F + f], a, da);
-    el_store<BF16>((El<BF16>*)dgu + m * 2 * F + f, dh[i] * gu[m * 2 * F + F + f] * da);
-    el_store<BF16>((El<BF16>*)dgu + m * 2 * F + F + f, dh[i] * a);
-  }
+template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int OCC>
+hipError_t launch(const FfnGemm& p, hipStream_t s) {
+  constexpr int FN = EPI == FFN_GLU ? 32 * NT : 64 * NT;
+  const long long tiles = ((p.M + 64LL * MT - 1) / (64 * MT)) * ((p.N + FN - 1LL) / FN);
+  if (tiles > 0x7ffffff0LL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((ffn_gemm_kernel<BF, AROWS, BROWS, MT, NT, EPI, SAVE, OCC>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                     dim3(256), 0, s, p);
+  return hipGetLastError();
 }
 
-unsigned flat_grid(long long n) { return (unsigned)std::min<long long>((n + 255) / 256, 256LL * 32); }
+// 256 x 256 tiles, one workgroup per CU, where their rounds cost less than
+// those of 128 x 128 tiles at two per CU
+template <bool AROWS, bool BROWS, int EPI, int SAVE>
+hipError_t pick(const FfnGemm& p, int bf16, hipStream_t s) {
+  if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  if (!bf16) return launch<false, AROWS, BROWS, 2, 2, EPI, SAVE, 2>(p, s);
+  const long long cols = EPI == FFN_GLU ? 2LL * p.N : p.N;
+  const long long t256 = ((p.M + 255LL) / 256) * ((cols + 255) / 256), t128 = ((p.M + 127LL) / 128) * ((cols + 127) / 128);
+  if (8 * ((t256 + 255) / 256) <= 5 * ((t128 + 511) / 512)) return launch<true, AROWS, BROWS, 4, 4, EPI, SAVE, 1>(p, s);
+  return launch<true, AROWS, BROWS, 2, 2, EPI, SAVE, 2>(p, s);
+}
 
 }  // namespace
 
-hipError_t rnn_launch_mat(const MatParams& p, int a_bf16, int b_bf16, int c_bf16, hipStream_t s) {
-  if (p.M == 0 || p.N == 0) return hipSuccess;
-  const dim3 grid((p.N + 63) / 64, (p.M + 63) / 64);
-  if (a_bf16 && b_bf16 && c_bf16) hipLaunchKernelGGL((mat_kernel<true, true, true>), grid, dim3(256), 0, s, p);
-  else if (a_bf16 && b_bf16) hipLaunchKernelGGL((mat_kernel<true, true, false>), grid, dim3(256), 0, s, p);
-  else if (!a_bf16 && !b_bf16 && !c_bf16) hipLaunchKernelGGL((mat_kernel<false, false, false>), grid, dim3(256), 0, s, p);
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
+hipError_t rnn_launch_ffn_glu(const FfnGemm& p, int bf16, int save, hipStream_t s) {
+  if (save == SAVE_NONE) return pick<true, true, FFN_GLU, SAVE_NONE>(p, bf16, s);
+  if (save == SAVE_FULL) return pick<true, true, FFN_GLU, SAVE_FULL>(p, bf16, s);
+  return pick<true, true, FFN_GLU, SAVE_INT8>(p, bf16, s);
 }
 
-#define ACT_PICK(KERNEL, ...)                                                                                  \
-  do {                                                                                                         \
-    const dim3 grid(flat_grid((long long)M * F));                                                              \
-    if (M == 0 || F == 0) return hipSuccess;                                                                   \
-    if (bf16 && act == ACT_SIGMOID) hipLaunchKernelGGL((KERNEL<true, ACT_SIGMOID>), grid, dim3(256), 0, s, __VA_ARGS__);  \
-    else if (bf16 && act == ACT_SILU) hipLaunchKernelGGL((KERNEL<true, ACT_SILU>), grid, dim3(256), 0, s, __VA_ARGS__);   \
-    else if (bf16) hipLaunchKernelGGL((KERNEL<true, ACT_GELU>), grid, dim3(256), 0, s, __VA_ARGS__);            \
-    else if (act == ACT_SIGMOID) hipLaunchKernelGGL((KERNEL<false, ACT_SIGMOID>), grid, dim3(256), 0, s, __VA_ARGS__);    \
-    else if (act == ACT_SILU) hipLaunchKernelGGL((KERNEL<false, ACT_SILU>), grid, dim3(256), 0, s, __VA_ARGS__);          \
-    else hipLaunchKernelGGL((KERNEL<false, ACT_GELU>), grid, dim3(256), 0, s, __VA_ARGS__);                     \
-  } while (0)
-
-hipError_t rnn_launch_act(int act, int bf16, int M, int F, const float* gu, void* h, hipStream_t s) {
-  ACT_PICK(act_kernel, M, F, gu, h);
-  return hipGetLastError();
+hipError_t rnn_launch_ffn_dglu(const FfnGemm& p, int bf16, int save, hipStream_t s) {
+  if (save == SAVE_FULL) return pick<true, false, FFN_DGLU, SAVE_FULL>(p, bf16, s);
+  return pick<true, false, FFN_DGLU, SAVE_INT8>(p, bf16, s);
 }
 
-hipError_t rnn_launch_act_bwd(int act, int bf16, int M, int F, const float* gu, const float* dh, void* dgu,
-                              hipStream_t s) {
-  ACT_PICK(act_bwd_kernel, M, F, gu, dh, dgu);
+hipError_t rnn_launch_ffn_store(const FfnGemm& p, int bf16, int layout, hipStream_t s) {
+  if (layout == 0) return pick<true, true, FFN_STORE, SAVE_NONE>(p, bf16, s);
+  if (layout == 1) return pick<true, false, FFN_STORE, SAVE_NONE>(p, bf16, s);
+  return pick<false, false, FFN_STORE, SAVE_NONE>(p, bf16, s);
+}
+
+hipError_t rnn_launch_pad(const PadJob& j, int bf16, hipStream_t s) {
+  if (j.n == 0) return hipSuccess;
+  long long n = 0;
+  for (int i = 0; i < j.n; ++i) n = std::max(n, j.rows[i] * j.ld[i]);
+  if (n == 0) return hipSuccess;
+  const dim3 grid((unsigned)std::min<long long>((n + 255) / 256, 256 * 16), 1, j.n);
+  if (bf16) hipLaunchKernelGGL(pad_kernel<true>, grid, dim3(256), 0, s, j);
+  else hipLaunchKernelGGL(pad_kernel<false>, grid, dim3(256), 0, s, j);
   return hipGetLastError();
 }

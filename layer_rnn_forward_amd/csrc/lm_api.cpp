@@ -48,46 +48,87 @@ size_t scan_bytes(int T, int B, int H, int dirs) {
 rnn_status_t ffn_sizes(int M, int D, int F, int wtype, int save) {
   if (M < 0 || D < 0 || F < 0 || !wtype_ok(wtype)) return RNN_STATUS_INVALID_ARG;
   if (save != RNN_SAVE_NONE && save != RNN_SAVE_FULL && save != RNN_SAVE_INT8) return RNN_STATUS_INVALID_ARG;
-  if (D >= (1 << 24) || F >= (1 << 24) || M >= (1 << 30)) return RNN_STATUS_UNSUPPORTED;
+  if (D >= (1 << 20) || F >= (1 << 20) || M >= (1 << 30)) return RNN_STATUS_UNSUPPORTED;
   return RNN_STATUS_SUCCESS;
 }
 
 size_t ckpt_bytes(size_t rows, size_t cols) { return rows * cols + rows * ((cols + kGroup - 1) / kGroup); }
 
+// Widths as the products see them: rows of x, dy and w_in in whole 16-byte
+// pieces (Dp), rows of w_out likewise (Fo), rows of the library's own
+// [M, F] buffers in whole K steps (Fp).
 struct FfnPlan {
-  // workspace
-  size_t gu = 0, h = 0, x = 0, dh = 0, dgu = 0, ws = 0;
+  int es = 0, Dp = 0, Fo = 0, Fp = 0;
+  // workspace: padded copies (used where rows or addresses are not 16-byte
+  // aligned), the gated product, its gradients
+  size_t x = 0, w_in = 0, w_out = 0, dy = 0, h = 0, dgu = 0, ws = 0;
   // reserve
-  size_t rgu = 0, rh = 0, rx = 0, reserve = 0;
+  size_t s0 = 0, s1 = 0, e0 = 0, e1 = 0, rh = 0, rx = 0, reserve = 0;
 };
 
 FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
-  const size_t es = wtype == RNN_W_BF16 ? 2 : 4, m = M, d = D, f = F;
   FfnPlan p;
+  p.es = wtype == RNN_W_BF16 ? 2 : 4;
+  const int piece = 16 / p.es;
+  p.Dp = (D + piece - 1) / piece * piece;
+  p.Fo = (F + piece - 1) / piece * piece;
+  p.Fp = (F + 63) / 64 * 64;
+  const size_t m = M, es = p.es;
   size_t o = 0;
-  auto take = [](size_t& top, size_t bytes) {
-    const size_t at = top;
-    top += align_up(bytes);
+  auto take = [&o](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
     return at;
   };
-  p.gu = take(o, m * 2 * f * 4);
-  p.h = take(o, m * f * es);
+  p.x = take(m * p.Dp * es);
+  p.w_in = take(2 * (size_t)F * p.Dp * es);
+  p.w_out = take((size_t)D * p.Fo * es);
+  if (save != RNN_SAVE_FULL) p.h = take(m * p.Fp * es);
   if (save != RNN_SAVE_NONE) {
-    p.x = take(o, m * d * es);
-    p.dh = take(o, m * f * 4);
-    p.dgu = take(o, m * 2 * f * es);
+    p.dy = take(m * p.Dp * es);
+    p.dgu = take(m * 2 * p.Fp * es);
   }
   p.ws = std::max(o, kAlign);
   o = 0;
-  if (save == RNN_SAVE_FULL) {
-    p.rgu = take(o, m * 2 * f * 4);
-    p.rh = take(o, m * f * es);
-  } else if (save == RNN_SAVE_INT8) {
-    p.rgu = take(o, ckpt_bytes(2 * m, f));
-    p.rx = take(o, ckpt_bytes(m, d));
+  if (save != RNN_SAVE_NONE) {
+    const size_t vs = save == RNN_SAVE_INT8 ? 1 : wtype == RNN_W_BF16 ? 2 : 4;
+    p.s0 = take(m * p.Fp * vs);
+    p.s1 = take(m * p.Fp * vs);
+    if (vs < 4) {
+      p.e0 = take(m * (p.Fp / kGroup));
+      p.e1 = take(m * (p.Fp / kGroup));
+    }
+    if (save == RNN_SAVE_FULL) p.rh = take(m * p.Fp * es);
+    else p.rx = take(ckpt_bytes(m, D));
   }
   p.reserve = o;
   return p;
+}
+
+// The padded copies that one call needs, made in one launch.
+struct Pads {
+  PadJob j{};
+  const void* add(const void* src, long long rows, int cols, int ld, void* dst) {
+    if (cols == ld && ((uintptr_t)src & 15) == 0) return src;
+    const int i = j.n++;
+    j.src[i] = src;
+    j.dst[i] = dst;
+    j.rows[i] = rows;
+    j.cols[i] = cols;
+    j.ld[i] = ld;
+    return dst;
+  }
+};
+
+int store16(const void* c, long long ld, int es) { return ((uintptr_t)c & 15) == 0 && ld * es % 16 == 0; }
+
+void ffn_saved(FfnGemm& g, const FfnPlan& p, void* reserve) {
+  g.s0 = at<void>(reserve, p.s0);
+  g.s1 = at<void>(reserve, p.s1);
+  g.e0 = at<int8_t>(reserve, p.e0);
+  g.e1 = at<int8_t>(reserve, p.e1);
+  g.lds = p.Fp;
+  g.lde = p.Fp / kGroup;
 }
 
 }  // namespace
@@ -168,15 +209,29 @@ rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn
   if (!x || !y || (F > 0 && (!w_in || !w_out))) return RNN_STATUS_INVALID_ARG;
   const int bf = wtype == RNN_W_BF16;
   const hipStream_t s = hs(stream);
-  float* gu = save == RNN_SAVE_FULL ? at<float>(reserve, p.rgu) : at<float>(ws, p.gu);
+  Pads pads;
+  const void* xp = pads.add(x, M, D, p.Dp, at<void>(ws, p.x));
+  const void* wi = pads.add(w_in, 2LL * F, D, p.Dp, at<void>(ws, p.w_in));
+  const void* wo = pads.add(w_out, D, F, p.Fo, at<void>(ws, p.w_out));
+  LM_TRY(dev(rnn_launch_pad(pads.j, bf, s)));
+  if (save == RNN_SAVE_INT8) LM_TRY(dev(rnn_launch_ckpt_store(bf, M, D, x, at<void>(reserve, p.rx), s)));
   void* h = save == RNN_SAVE_FULL ? at<void>(reserve, p.rh) : at<void>(ws, p.h);
-  LM_TRY(dev(rnn_launch_mat({M, 2 * F, D, x, D, 1, w_in, D, 1, gu, 2LL * F}, bf, bf, 0, s)));
-  if (save == RNN_SAVE_INT8) {
-    LM_TRY(dev(rnn_launch_ckpt_store(bf, M, D, x, at<void>(reserve, p.rx), s)));
-    LM_TRY(dev(rnn_launch_ckpt_store(0, 2 * M, F, gu, at<void>(reserve, p.rgu), s)));
-  }
-  LM_TRY(dev(rnn_launch_act(act, bf, M, F, gu, h, s)));
-  return dev(rnn_launch_mat({M, D, F, h, F, 1, w_out, F, 1, y, D}, bf, bf, bf, s));
+  FfnGemm g{};
+  g.M = M; g.N = F; g.K = D;
+  g.A = xp; g.lda = p.Dp;
+  g.B = wi; g.ldb = p.Dp;
+  g.C = h; g.ldc = p.Fp;
+  g.segs = 1;
+  g.act = act;
+  if (save != RNN_SAVE_NONE) ffn_saved(g, p, reserve);
+  LM_TRY(dev(rnn_launch_ffn_glu(g, bf, save, s)));
+  FfnGemm o{};
+  o.M = M; o.N = D; o.K = F;
+  o.A = h; o.lda = p.Fp;
+  o.B = wo; o.ldb = p.Fo;
+  o.C = y; o.ldc = D; o.cvec = store16(y, D, p.es);
+  o.segs = 1;
+  return dev(rnn_launch_ffn_store(o, bf, 0, s));
 }
 
 rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn_save_t save, int M, int D, int F,
@@ -194,21 +249,63 @@ rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rn
     return RNN_STATUS_INVALID_ARG;
   const int bf = wtype == RNN_W_BF16;
   const hipStream_t s = hs(stream);
-  const float* gu = save == RNN_SAVE_FULL ? at<const float>(reserve, p.rgu) : at<float>(ws, p.gu);
-  const void* h = save == RNN_SAVE_FULL ? at<const void>(reserve, p.rh) : at<void>(ws, p.h);
-  float* dh = at<float>(ws, p.dh);
-  void* dgu = at<void>(ws, p.dgu);
-  if (save == RNN_SAVE_INT8) {
-    LM_TRY(dev(rnn_launch_ckpt_load(0, 2 * M, F, at<const void>(reserve, p.rgu), at<float>(ws, p.gu), s)));
-    LM_TRY(dev(rnn_launch_ckpt_load(bf, M, D, at<const void>(reserve, p.rx), at<void>(ws, p.x), s)));
-    LM_TRY(dev(rnn_launch_act(act, bf, M, F, gu, at<void>(ws, p.h), s)));
-    x = at<void>(ws, p.x);
+  Pads pads;
+  const void* wi = rows && dx ? pads.add(w_in, 2LL * F, D, p.Dp, at<void>(ws, p.w_in)) : nullptr;
+  const void* wo = rows ? pads.add(w_out, D, F, p.Fo, at<void>(ws, p.w_out)) : nullptr;
+  const void* dyp = rows ? pads.add(dy, M, D, p.Dp, at<void>(ws, p.dy)) : nullptr;
+  LM_TRY(dev(rnn_launch_pad(pads.j, bf, s)));
+  const void* xp = nullptr;
+  if (rows && dw_in) {
+    if (save == RNN_SAVE_INT8) {
+      LM_TRY(dev(rnn_launch_ckpt_load(bf, M, D, at<const void>(reserve, p.rx), at<void>(ws, p.x), p.Dp, s)));
+      xp = at<void>(ws, p.x);
+    } else {
+      Pads px;
+      xp = px.add(x, M, D, p.Dp, at<void>(ws, p.x));
+      LM_TRY(dev(rnn_launch_pad(px.j, bf, s)));
+    }
   }
-  LM_TRY(dev(rnn_launch_mat({M, F, D, dy, D, 1, w_out, 1, F, dh, F}, bf, bf, 0, s)));
-  LM_TRY(dev(rnn_launch_act_bwd(act, bf, M, F, gu, dh, dgu, s)));
-  if (dx) LM_TRY(dev(rnn_launch_mat({M, D, 2 * F, dgu, 2LL * F, 1, w_in, 1, D, dx, D}, bf, bf, bf, s)));
-  if (dw_in) LM_TRY(dev(rnn_launch_mat({2 * F, D, M, dgu, 1, 2LL * F, x, 1, D, dw_in, D}, bf, bf, bf, s)));
-  if (dw_out) LM_TRY(dev(rnn_launch_mat({D, F, M, dy, 1, D, h, 1, F, dw_out, F}, bf, bf, bf, s)));
+  void* dgu = at<void>(ws, p.dgu);
+  void* res = const_cast<void*>(reserve);   // read only
+  const void* h = save == RNN_SAVE_FULL ? at<void>(res, p.rh) : at<void>(ws, p.h);
+  FfnGemm g{};
+  g.M = M; g.N = F; g.K = D;
+  g.A = dyp; g.lda = p.Dp;
+  g.B = wo; g.ldb = p.Fo;
+  g.C = dgu; g.ldc = 2LL * p.Fp;
+  g.segs = 1;
+  g.act = act;
+  ffn_saved(g, p, res);
+  g.h = at<void>(ws, p.h); g.ldh = p.Fp;
+  LM_TRY(dev(rnn_launch_ffn_dglu(g, bf, save, s)));
+  if (dx) {
+    FfnGemm o{};
+    o.M = M; o.N = D; o.K = F;
+    o.A = dgu; o.lda = 2LL * p.Fp;
+    o.B = wi; o.ldb = p.Dp;
+    o.C = dx; o.ldc = D; o.cvec = store16(dx, D, p.es);
+    o.segs = 2; o.kseg = p.Fp;
+    LM_TRY(dev(rnn_launch_ffn_store(o, bf, 1, s)));
+  }
+  if (dw_in && F > 0) {
+    FfnGemm o{};
+    o.M = 2 * p.Fp; o.N = D; o.K = M;
+    o.A = dgu; o.lda = 2LL * p.Fp;
+    o.B = xp; o.ldb = p.Dp;
+    o.C = dw_in; o.ldc = D; o.cvec = store16(dw_in, D, p.es);
+    o.segs = 1;
+    o.mseg = p.Fp; o.mreal = F;
+    LM_TRY(dev(rnn_launch_ffn_store(o, bf, 2, s)));
+  }
+  if (dw_out) {
+    FfnGemm o{};
+    o.M = D; o.N = F; o.K = M;
+    o.A = dyp; o.lda = p.Dp;
+    o.B = h; o.ldb = p.Fp;
+    o.C = dw_out; o.ldc = F; o.cvec = store16(dw_out, F, p.es);
+    o.segs = 1;
+    LM_TRY(dev(rnn_launch_ffn_store(o, bf, 2, s)));
+  }
   return RNN_STATUS_SUCCESS;
 }
 
@@ -237,7 +334,7 @@ rnn_status_t rnn_checkpoint_store(void* stream, rnn_wtype_t wtype, int rows, int
 rnn_status_t rnn_checkpoint_load(void* stream, rnn_wtype_t wtype, int rows, int cols, const void* kept,
                                  size_t kept_bytes, void* x) {
   LM_TRY(ckpt_check(wtype, rows, cols, x, kept, kept_bytes));
-  return dev(rnn_launch_ckpt_load(wtype == RNN_W_BF16, rows, cols, kept, x, hs(stream)));
+  return dev(rnn_launch_ckpt_load(wtype == RNN_W_BF16, rows, cols, kept, x, cols, hs(stream)));
 }
 
 }  // extern "C"

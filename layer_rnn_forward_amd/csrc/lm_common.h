@@ -27,15 +27,44 @@ struct ScanParams {
   float* states;         // [D][B][H][T] (workspace): every state, written by the forward pass
 };
 
-// C[m, n] = sum_k A[m*sam + k*sak] * B[n*sbn + k*sbk], fp32 accumulation
-struct MatParams {
-  int M, N, K;
+// One product of the feed-forward block (ffn_gemm.h).  Leading dimensions in
+// elements, multiples of 16 bytes; bases 16-byte aligned.
+struct FfnGemm {
+  int M, N, K;           // N: columns of C (the gated product's: F)
   const void* A;
-  long long sam, sak;
-  const void* B;
-  long long sbn, sbk;
+  long long lda;
+  const void* B;         // FFN_GLU: F gate rows, then F up rows
+  long long ldb;
   void* C;
   long long ldc;
+  int cvec;              // 16-byte stores of C are aligned
+  // K in `segs` (1 or 2) segments: K real values each; the second starts kseg
+  // later in A and K later in B
+  int segs, kseg;
+  // mseg > 0: rows [0, mreal) and [mseg, mseg + mreal) of the product are
+  // rows [0, 2 * mreal) of C
+  int mseg, mreal;
+  int act;
+  // saved for backward, rows of lds values and lde exponents: act(g) and
+  // u act'(g) (RNN_SAVE_FULL; 16 bits with exponents, or fp32), or g and u
+  // (RNN_SAVE_INT8)
+  void* s0;
+  void* s1;
+  int8_t* e0;
+  int8_t* e1;
+  long long lds, lde;
+  void* h;               // FFN_DGLU with RNN_SAVE_INT8: the gated product, again
+  long long ldh;
+};
+
+// Copies of up to three matrices with rows padded by zeros to a multiple of
+// 16 bytes.
+struct PadJob {
+  int n;
+  const void* src[3];
+  void* dst[3];
+  long long rows[3];
+  int cols[3], ld[3];    // ld: columns of dst
 };
 
 }  // namespace rnnk
@@ -45,12 +74,12 @@ hipError_t rnn_launch_scan_step(int mode, int bf16, int B, int H, const void* g,
 hipError_t rnn_launch_scan_fwd(const rnnk::ScanParams& p, int mode, int bf16, hipStream_t s);
 hipError_t rnn_launch_scan_bwd(const rnnk::ScanParams& p, int mode, int bf16, hipStream_t s);
 
-hipError_t rnn_launch_mat(const rnnk::MatParams& p, int a_bf16, int b_bf16, int c_bf16, hipStream_t s);
-// h = act(g) * u from gu [M][2F] fp32
-hipError_t rnn_launch_act(int act, int bf16, int M, int F, const float* gu, void* h, hipStream_t s);
-// dgu [M][2F] (element type) from dh [M][F] and gu [M][2F] fp32
-hipError_t rnn_launch_act_bwd(int act, int bf16, int M, int F, const float* gu, const float* dh, void* dgu,
-                              hipStream_t s);
+// layout: 0 rows x rows, 1 rows x columns, 2 columns x columns (A, B)
+hipError_t rnn_launch_ffn_glu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
+hipError_t rnn_launch_ffn_dglu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
+hipError_t rnn_launch_ffn_store(const rnnk::FfnGemm& p, int bf16, int layout, hipStream_t s);
+hipError_t rnn_launch_pad(const rnnk::PadJob& j, int bf16, hipStream_t s);
 
 hipError_t rnn_launch_ckpt_store(int bf16, int rows, int cols, const void* x, void* kept, hipStream_t s);
-hipError_t rnn_launch_ckpt_load(int bf16, int rows, int cols, const void* kept, void* x, hipStream_t s);
+// ld: elements between the rows of x; columns from cols on are set to zero
+hipError_t rnn_launch_ckpt_load(int bf16, int rows, int cols, const void* kept, void* x, long long ld, hipStream_t s);
