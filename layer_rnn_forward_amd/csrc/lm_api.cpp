@@ -40,8 +40,39 @@ rnn_status_t scan_sizes(int T, int B, int H, int dirs) {
   return RNN_STATUS_SUCCESS;
 }
 
-size_t scan_bytes(int T, int B, int H, int dirs) {
-  return kAlign + align_up((size_t)T * B * H * dirs * 4);
+// Chunks of as many waves as there are pieces, `most` at most.
+void scan_split(int T, int steps, int most, int& waves, int& chunks) {
+  const int pieces = (int)(((long long)T + steps - 1) / steps);
+  waves = std::max(1, std::min(most, pieces));
+  chunks = std::max(1, (pieces + waves - 1) / waves);
+}
+
+struct ScanPlan {
+  int fwaves, fchunks, bwaves, bchunks;
+  size_t maps, starts, bytes;
+};
+ScanPlan scan_plan(int T, int B, int H, int dirs) {
+  ScanPlan p;
+  scan_split(T, kScanFwdSteps, kScanFwdWaves, p.fwaves, p.fchunks);
+  scan_split(T, kScanBwdSteps, kScanBwdWaves, p.bwaves, p.bchunks);
+  const size_t C = (size_t)B * H * dirs;
+  auto words = [](int chunks, int super) { return chunks > 1 ? 2 * (size_t)chunks + chunks / super + 1 : 0; };
+  const size_t most = std::max(words(p.fchunks, kScanFwdSuper), words(p.bchunks, kScanBwdSuper));
+  p.maps = kAlign + (most ? align_up(((size_t)B * H + 63) / 64 * dirs * 64) : 0);
+  p.starts = p.maps + align_up(most * C * 4);
+  p.bytes = p.starts + align_up(((size_t)T + kScanKeep - 1) / kScanKeep * C * 4);
+  return p;
+}
+
+void scan_room(ScanParams& p, bool back, void* ws) {
+  const ScanPlan q = scan_plan(p.T, p.B, p.H, p.D);
+  p.waves = back ? q.bwaves : q.fwaves;
+  p.chunks = back ? q.bchunks : q.fchunks;
+  p.head = at<unsigned>(ws, 0);
+  p.counters = at<unsigned>(ws, kAlign);
+  p.starts = at<float>(ws, q.starts);
+  p.maps = at<unsigned long long>(ws, q.maps);
+  p.state = reinterpret_cast<float*>(p.maps + (size_t)p.chunks * p.B * p.H * p.D);
 }
 
 // -------------------------------------------------------------------- ffn
@@ -138,7 +169,7 @@ extern "C" {
 rnn_status_t rnn_scan_workspace_size(int T, int B, int H, int dirs, size_t* bytes) {
   if (!bytes) return RNN_STATUS_INVALID_ARG;
   LM_TRY(scan_sizes(T, B, H, dirs));
-  *bytes = scan_bytes(T, B, H, dirs);
+  *bytes = scan_plan(T, B, H, dirs).bytes;
   return RNN_STATUS_SUCCESS;
 }
 
@@ -157,13 +188,13 @@ rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wt
   if (!scan_mode_ok(mode) || !wtype_ok(wtype)) return RNN_STATUS_INVALID_ARG;
   LM_TRY(scan_sizes(T, B, H, dirs));
   if (!ws || !aligned(ws)) return RNN_STATUS_INVALID_ARG;
-  if (ws_bytes < scan_bytes(T, B, H, dirs)) return RNN_STATUS_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < scan_plan(T, B, H, dirs).bytes) return RNN_STATUS_WORKSPACE_TOO_SMALL;
   if (B == 0 || H == 0) return RNN_STATUS_SUCCESS;
   if (T > 0 && (!g || !y)) return RNN_STATUS_INVALID_ARG;
   ScanParams p{};
   p.T = T; p.B = B; p.H = H; p.D = dirs;
   p.g = g; p.h0 = h0; p.lengths = lengths; p.y = y; p.hy = hy;
-  p.states = at<float>(ws, kAlign);
+  scan_room(p, false, ws);
   return dev(rnn_launch_scan_fwd(p, mode, wtype == RNN_W_BF16, hs(stream)));
 }
 
@@ -173,13 +204,13 @@ rnn_status_t rnn_scan_backward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t w
   if (!scan_mode_ok(mode) || !wtype_ok(wtype)) return RNN_STATUS_INVALID_ARG;
   LM_TRY(scan_sizes(T, B, H, dirs));
   if (!ws || !aligned(ws)) return RNN_STATUS_INVALID_ARG;
-  if (ws_bytes < scan_bytes(T, B, H, dirs)) return RNN_STATUS_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < scan_plan(T, B, H, dirs).bytes) return RNN_STATUS_WORKSPACE_TOO_SMALL;
   if (B == 0 || H == 0) return RNN_STATUS_SUCCESS;
   if (T > 0 && (!g || !dy || !dg)) return RNN_STATUS_INVALID_ARG;
   ScanParams p{};
   p.T = T; p.B = B; p.H = H; p.D = dirs;
   p.g = g; p.h0 = h0; p.lengths = lengths; p.dy = dy; p.dhy = dhy; p.dg = dg; p.dh0 = dh0;
-  p.states = at<float>(ws, kAlign);
+  scan_room(p, true, ws);
   return dev(rnn_launch_scan_bwd(p, mode, wtype == RNN_W_BF16, hs(stream)));
 }
 

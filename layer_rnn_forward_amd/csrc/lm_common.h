@@ -13,6 +13,13 @@ enum Save { SAVE_NONE = 0, SAVE_FULL = 1, SAVE_INT8 = 2 };
 
 constexpr int kGroup = 32;   // columns that share one exponent in a checkpoint
 
+// Scan: the forward pass keeps the state before every kScanKeep-th step; for
+// each pass the steps of a wave's piece (multiples of kScanKeep), the waves of
+// a workgroup, the chunks between two published states
+constexpr int kScanKeep = 8;
+constexpr int kScanFwdSteps = 16, kScanFwdWaves = 8, kScanFwdSuper = 8, kScanFwdEu = 4;
+constexpr int kScanBwdSteps = 8, kScanBwdWaves = 8, kScanBwdSuper = 4, kScanBwdEu = 4;
+
 struct ScanParams {
   int T, B, H, D;
   const void* g;
@@ -24,7 +31,16 @@ struct ScanParams {
   const float* dhy;      // backward, or null
   void* dg;              // backward
   float* dh0;            // backward, or null
-  float* states;         // [D][B][H][T] (workspace): every state, written by the forward pass
+  int waves, chunks;     // chunks of `waves` pieces
+  // workspace, in this order: [0] a wait expired (256 bytes); started chunks
+  // of each workgroup's channels, 64 bytes apart; the chunks' maps (A, B) and
+  // the states before every group of chunks, contiguous; the state before
+  // every kScanKeep-th step
+  unsigned* head;
+  unsigned* counters;        // [ceil(B * H / 64)][D][16]
+  unsigned long long* maps;  // [chunks][D][B][H]
+  float* state;              // [chunks / group + 1][D][B][H]
+  float* starts;             // [ceil(T / kScanKeep)][D][B][H]
 };
 
 // One product of the feed-forward block (ffn_gemm.h).  Leading dimensions in

@@ -1,25 +1,125 @@
-// Gated linear recurrence h_t = a_t h_(t-1) + b_t (gfx950).
+// Gated linear recurrence h_t = a_t h_(t-1) + b_t (gfx950): one pass over the
+// gates, with the time axis split among workgroups.
 //
-// One thread per (direction, row, unit) walks the steps in order; the forward
-// pass keeps every state in the workspace for the backward pass.
+// The steps s .. e of one channel compose to h_e = A h_(s-1) + B, and two such
+// maps compose to (A2 A1, A2 B1 + B2).  A lane holds VW neighbouring channels
+// over 16 steps (forward) or 8 (backward) in registers, as coefficients in 32
+// bits, so the gates are read once; the waves of a workgroup hold consecutive
+// pieces of one chunk.  Each wave composes its piece, the first wave the
+// chunk; it publishes the chunk's (A, B), waits for what precedes it, and the
+// waves then walk their pieces from the true state.
+//
+// What precedes a chunk is the state before its group of SUPER chunks,
+// followed by the maps of the group's chunks before it.  Every chunk composes
+// those in order, and the last chunk of a group publishes the state that its
+// successors start from: the sequence of roundings never depends on which
+// chunk came first, and a sequence of N chunks waits N / SUPER times in a row
+// instead of N.  A workgroup takes its chunk from its channels' counter, in
+// walking order, so everything a chunk waits for is done or running (one
+// counter for all workgroups cost 20 % of a pass over 2048 steps).
+//
+// Published words are their own flags: a kernel sets them beforehand to a
+// pattern that no published value has (kUnset, a NaN pattern replaced by
+// another NaN when a result has it), so a wait costs one round trip.  Waits
+// are bounded; one that expires sets the workspace's first word and carries on
+// with NaN.
+//
+// The backward pass is the same recurrence walked the other way
+// (D_(t-1) = a_t (dy_t + D_t)).  It composes the states again from the gates
+// and the state before every 8th step, which the forward pass leaves in the
+// workspace: 0.5 bytes a value instead of 4 for the states themselves.
+//
+// Bound: 6 (forward) and 10.5 (backward) bytes a value in bf16 against about
+// 39 and 59 issue slots of vector work (exponentials and reciprocals count
+// four), which is 0.5 to 0.8 of the memory's time; waves that wait for each
+// other leave the two overlapped in part.  65536 steps of 1760 channels in
+// bf16: forward 0.22 ms, backward 0.35 ms (3.3 and 3.5 TB/s); 2048 steps of 8
+// rows of 1024: 0.030 and 0.042 ms.  One thread per channel that walks every
+// step took 96 ms and 2.7 ms for both passes.  Measured against the split
+// used (forward 16 steps x 8 waves in groups of 8, backward 8 x 8 in groups
+// of 4; forward / backward ms of the long case): 4 waves 0.24 / 0.37, 8 steps
+// forward 0.25, 16 steps backward 0.36, groups of 16 0.23 / 0.39, of 32
+// backward 0.48.
+#include <algorithm>
 #include <type_traits>
 
 #include "lm_math.h"
 
 using namespace rnnk;
 
+// sums and products are fused where fmaf says so and nowhere else, so that the
+// variants of one kernel round alike
+#pragma clang fp contract(off)
+
 namespace {
+
+constexpr unsigned kUnset = 0xffffffffu;
+constexpr int kWaitLimit = 1 << 22;
+
+template <bool BF, int VW>
+struct Vec {
+  static_assert(VW == 1 || BF, "");
+  using T = typename std::conditional<BF, typename std::conditional<VW == 2, uint32_t, uint16_t>::type, float>::type;
+  static __device__ __forceinline__ void get(const T& v, float (&o)[VW]) {
+    if constexpr (BF && VW == 2) {
+      o[0] = __uint_as_float(v << 16);
+      o[1] = __uint_as_float(v & 0xffff0000u);
+    } else if constexpr (BF) {
+      o[0] = bf2f(v);
+    } else {
+      o[0] = v;
+    }
+  }
+  static __device__ __forceinline__ T make(const float (&o)[VW]) {
+    if constexpr (BF && VW == 2) return pack2bf(o[0], o[1]);
+    else if constexpr (BF) return f2bf(o[0]);
+    else return o[0];
+  }
+};
+
+// a, 1 - a and the candidate n of a gated step.  1 - a from the same
+// exponential (no cancellation); tanh from one exponential of -2|q|, and from
+// its series q - q^3/3 + 2q^5/15 below 1/16, where 1 - e^(-2|q|) would cancel
+// (both are within 12 units in the last place).
+__device__ __forceinline__ void gate(float p, float q, float& a, float& na, float& n) {
+  const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(p));
+  const float x = fabsf(q), t = __builtin_amdgcn_exp2f(-2.8853900817779268f * x);
+  const float e1 = 1.f + e, t1 = 1.f + t, r = __builtin_amdgcn_rcpf(e1 * t1);
+  const float big = r * t1, small = e * big;
+  a = p >= 0.f ? big : small;
+  na = p >= 0.f ? small : big;
+  const float far = (1.f - t) * (r * e1);
+  const float z = q * q, near = fmaf(x * z, fmaf(z, 2.f / 15.f, -1.f / 3.f), x);
+  n = copysignf(x < 0.0625f ? near : far, q);
+}
 
 template <int MODE>
 __device__ __forceinline__ void coeffs(float p, float q, float& a, float& na, float& n) {
   if constexpr (MODE == SCAN_GATED) {
-    sigmoid_pair(p, a, na);
-    n = tanhf_(q);
+    gate(p, q, a, na, n);
   } else {
     a = p;
     na = 1.f;
     n = q;
   }
+}
+
+// A h + B; a state of exactly zero stays out of the product, so that an A
+// which overflowed (linear steps with |a| > 1) does not turn it into NaN
+__device__ __forceinline__ float apply(float A, float h, float B) { return h == 0.f ? B : fmaf(A, h, B); }
+
+__device__ __forceinline__ unsigned word(float v) {
+  const unsigned u = __float_as_uint(v);
+  return u == kUnset ? 0x7fffffffu : u;
+}
+__device__ __forceinline__ void publish(float* p, float v) { flag_store(reinterpret_cast<unsigned*>(p), word(v)); }
+__device__ __forceinline__ unsigned peek(const float* p) { return flag_load(reinterpret_cast<const unsigned*>(p)); }
+// a map (A, B) is one 8-byte word, A in its lower half
+__device__ __forceinline__ void publish2(unsigned long long* p, float A, float B) {
+  __hip_atomic_store(p, word(A) | (unsigned long long)word(B) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned long long peek2(const unsigned long long* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 template <bool BF16, int MODE>
@@ -35,95 +135,447 @@ __global__ __launch_bounds__(256) void step_kernel(int B, int H, const void* gv,
   hy[i] = v;
 }
 
-template <bool BF16, int MODE>
-__global__ __launch_bounds__(64) void fwd_kernel(const ScanParams p) {
-  const long long C = (long long)p.D * p.B * p.H;
-  const long long c = (long long)blockIdx.x * 64 + threadIdx.x;
-  if (c >= C) return;
-  const int u = (int)(c % p.H), b = (int)(c / p.H % p.B), d = (int)(c / ((long long)p.H * p.B));
-  const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-  const El<BF16>* g = (const El<BF16>*)p.g;
-  El<BF16>* y = (El<BF16>*)p.y;
-  float h = p.h0 ? p.h0[c] : 0.f;
-  for (int i = 0; i < p.T; ++i) {
-    const int t = d ? p.T - 1 - i : i;
-    const long long row = ((long long)t * p.B + b) * p.D + d;
-    float out = 0.f;
-    if (t < len) {
-      float a, na, n;
-      coeffs<MODE>(el_load<BF16>(g + row * 2 * p.H + u), el_load<BF16>(g + row * 2 * p.H + p.H + u), a, na, n);
-      if (p.states) p.states[i * C + c] = h;
-      out = h = fmaf(a, h, na * n);
-    }
-    el_store<BF16>(y + row * p.H + u, out);
+// counters to zero, published words to kUnset, 16 bytes a lane
+__global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long counters, long long all) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) head[0] = 0;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const unsigned v = i < counters ? 0u : kUnset;
+    reinterpret_cast<uint4*>(head + 64)[i] = make_uint4(v, v, v, v);
   }
-  if (p.hy) p.hy[c] = h;
 }
 
-template <bool BF16, int MODE>
-__global__ __launch_bounds__(64) void bwd_kernel(const ScanParams p) {
-  const long long C = (long long)p.D * p.B * p.H;
-  const long long c = (long long)blockIdx.x * 64 + threadIdx.x;
-  if (c >= C) return;
-  const int u = (int)(c % p.H), b = (int)(c / p.H % p.B), d = (int)(c / ((long long)p.H * p.B));
-  const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-  const El<BF16>* g = (const El<BF16>*)p.g;
-  const El<BF16>* dy = (const El<BF16>*)p.dy;
-  El<BF16>* dg = (El<BF16>*)p.dg;
-  float dh = p.dhy ? p.dhy[c] : 0.f;
-  for (int i = p.T - 1; i >= 0; --i) {
-    const int t = d ? p.T - 1 - i : i;
-    const long long row = ((long long)t * p.B + b) * p.D + d;
-    float dp = 0.f, dq = 0.f;
-    if (t < len) {
-      float a, na, n;
-      coeffs<MODE>(el_load<BF16>(g + row * 2 * p.H + u), el_load<BF16>(g + row * 2 * p.H + p.H + u), a, na, n);
-      dh += el_load<BF16>(dy + row * p.H + u);
-      const float before = p.states[i * C + c];
-      if constexpr (MODE == SCAN_GATED) {
-        dp = dh * (before - n) * a * na;
-        dq = dh * na * (1.f - n * n);
-      } else {
-        dp = dh * before;
-        dq = dh;
+// Read `count` words at once, and those again that were unset.
+template <int N, int VW, class Load, class Word>
+__device__ __forceinline__ void wait_words(const ScanParams& p, int count, Word (&v)[N][VW], Load load) {
+  unsigned need = (1u << count) - 1u;
+  for (int spin = 0; need; ++spin) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (need >> j & 1)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) v[j][e] = load(j, e);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (need >> j & 1) {
+        bool ok = true;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) ok &= (unsigned)v[j][e] != kUnset;
+        if (__all(ok)) need &= ~(1u << j);
       }
-      dh *= a;
+    if (!need) break;
+    if (spin == kWaitLimit) {
+      flag_store(p.head, 1u);
+      break;                             // the unset words are NaNs
     }
-    el_store<BF16>(dg + row * 2 * p.H + u, dp);
-    el_store<BF16>(dg + row * 2 * p.H + p.H + u, dq);
+    __builtin_amdgcn_s_sleep(1);
   }
-  if (p.dh0) p.dh0[c] = dh;
+}
+
+// The state that chunk `pos` (in walking order) starts from: the wave's VW
+// channels at `c` of `C`.  h holds the sequence's first state.  The maps since
+// the last published state are composed first, then that state is waited for.
+template <int VW, int SUPER>
+__device__ void wait_state(const ScanParams& p, int pos, long long C, long long c, bool live, float (&h)[VW]) {
+  const int sup = pos / SUPER, n = pos - sup * SUPER;
+  constexpr int N = 4;
+  float A[VW], B[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    A[e] = 1.f;
+    B[e] = 0.f;
+  }
+  for (int j0 = 0; j0 < n; j0 += N) {
+    unsigned long long m[N][VW];
+    const unsigned long long* from = p.maps + (long long)(sup * SUPER + j0) * C + c;
+    const int count = min(N, n - j0);
+    wait_words<N, VW>(p, count, m, [&](int j, int e) { return live ? peek2(from + j * C + e) : 0ull; });
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < count)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) {
+          const float a = __uint_as_float((unsigned)m[j][e]);
+          A[e] *= a;
+          B[e] = apply(a, B[e], __uint_as_float((unsigned)(m[j][e] >> 32)));
+        }
+  }
+  if (sup > 0) {
+    unsigned u[1][VW];
+    wait_words<1, VW>(p, 1, u, [&](int, int e) { return live ? peek(p.state + (long long)sup * C + c + e) : 0u; });
+#pragma unroll
+    for (int e = 0; e < VW; ++e) h[e] = __uint_as_float(u[0][e]);
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) h[e] = apply(A[e], h[e], B[e]);
+}
+
+// The chunk and channels of a workgroup.
+struct Place {
+  int pos;           // chunk, in walking order
+  int d, c0;         // direction, first channel (of B * H)
+};
+__device__ __forceinline__ Place place(const ScanParams& p, int VW, unsigned& shared) {
+  const int per = (p.B * p.H + 64 * VW - 1) / (64 * VW), tile = (int)(blockIdx.x % (unsigned)(per * p.D));
+  Place r;
+  r.pos = 0;
+  if (p.chunks > 1) {
+    if (threadIdx.x == 0) shared = atomicAdd(p.counters + tile * 16LL, 1u);
+    __syncthreads();
+    r.pos = __builtin_amdgcn_readfirstlane(shared);
+  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.head[0] = 0;
+  }
+  r.d = tile / per;
+  r.c0 = (tile - r.d * per) * 64 * VW;
+  return r;
+}
+
+// compose the waves' maps to the chunk's, find the state before the chunk,
+// pass it on; returns the state before this wave's piece
+template <int VW, int SUPER, int MW>
+__device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, long long c, bool live, const float* first,
+                                     int wave, int lane, int W, float (&sA)[MW][64 * VW], float (&sB)[MW][64 * VW],
+                                     float (&sh)[64 * VW], const float (&A)[VW], const float (&B)[VW], float (&h)[VW]) {
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    sA[wave][lane * VW + e] = A[e];
+    sB[wave][lane * VW + e] = B[e];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    float tA[VW], tB[VW];
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      tA[e] = A[e];
+      tB[e] = B[e];
+    }
+    for (int w = 1; w < W; ++w)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const float a = sA[w][lane * VW + e];
+        tA[e] *= a;
+        tB[e] = apply(a, tB[e], sB[w][lane * VW + e]);
+      }
+    const bool ends = pos % SUPER == SUPER - 1, more = pos + 1 < p.chunks;
+    if (more && !ends && live)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) publish2(p.maps + (long long)pos * C + c + e, tA[e], tB[e]);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) h[e] = first && live ? first[c + e] : 0.f;
+    if (pos > 0) wait_state<VW, SUPER>(p, pos, C, c, live, h);
+    if (more && ends && live)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) publish(p.state + (long long)(pos / SUPER + 1) * C + c + e, apply(tA[e], h[e], tB[e]));
+#pragma unroll
+    for (int e = 0; e < VW; ++e) sh[lane * VW + e] = h[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < VW; ++e) h[e] = sh[lane * VW + e];
+  for (int w = 0; w < wave; ++w)
+#pragma unroll
+    for (int e = 0; e < VW; ++e) h[e] = apply(sA[w][lane * VW + e], h[e], sB[w][lane * VW + e]);
+}
+
+// Where a lane's values lie in a step's row: the elements up to the
+// workgroup's first channel are uniform (gbase, ybase), the bytes from there
+// to the lane's p and y fit 32 bits.
+struct Lanes {
+  unsigned g, y;
+  int b;             // batch row
+  bool live;
+};
+template <bool BF, int VW>
+__device__ __forceinline__ void lanes(const ScanParams& p, const Place& at, int lane, long long& gbase, long long& ybase,
+                                      Lanes& l) {
+  constexpr int ES = BF ? 2 : 4;
+  const int BH = p.B * p.H;
+  int c = at.c0 + lane * VW;
+  l.live = c < BH;
+  if (!l.live) c = at.c0;                     // reads what the first lane reads, writes nothing
+  l.b = c / p.H;
+  const int b0 = at.c0 / p.H, u0 = at.c0 - b0 * p.H;
+  ybase = ((long long)b0 * p.D + at.d) * p.H + u0;
+  gbase = ((long long)b0 * p.D + at.d) * 2 * p.H + u0;
+  const long long y = ((long long)l.b * p.D + at.d) * p.H + (c - l.b * p.H);
+  const long long g = ((long long)l.b * p.D + at.d) * 2 * p.H + (c - l.b * p.H);
+  l.y = (unsigned)((y - ybase) * ES);
+  l.g = (unsigned)((g - gbase) * ES);
+}
+
+template <class T>
+__device__ __forceinline__ T ld(const char* row, unsigned off) { return *reinterpret_cast<const T*>(row + off); }
+template <class T>
+__device__ __forceinline__ void st(char* row, unsigned off, T v) { *reinterpret_cast<T*>(row + off) = v; }
+
+template <bool BF, int MODE, int VW>
+__global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(const ScanParams p) {
+  using V = Vec<BF, VW>;
+  using T = typename V::T;
+  constexpr int ES = BF ? 2 : 4, G = kScanFwdSteps;
+  __shared__ float sA[kScanFwdWaves][64 * VW], sB[kScanFwdWaves][64 * VW], sh[64 * VW];
+  __shared__ unsigned shared;
+  const Place at = place(p, VW, shared);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+  const long long C = (long long)p.D * p.B * p.H;
+  long long gbase, ybase;
+  Lanes l;
+  lanes<BF, VW>(p, at, lane, gbase, ybase, l);
+  const long long c = (long long)at.d * p.B * p.H + at.c0 + lane * VW;
+  const long long grow = (long long)p.B * p.D * 2 * p.H * ES, yrow = grow / 2;
+  const char* g = (const char*)p.g + gbase * ES;
+  char* y = (char*)p.y + ybase * ES;
+  const int i0 = (at.pos * W + wave) * G;
+  const long long half = (long long)p.H * ES;
+  const int len = p.lengths ? min(max(p.lengths[l.b], 0), p.T) : p.T;
+  const bool whole = !p.lengths && i0 + G <= p.T;
+
+  T rp[G], rq[G];
+#pragma unroll
+  for (int s = 0; s < G; ++s) {
+    const int i = min(i0 + s, p.T - 1), t = at.d ? p.T - 1 - i : i;
+    const char* row = g + t * grow;
+    rp[s] = ld<T>(row, l.g);
+    rq[s] = ld<T>(row + half, l.g);
+  }
+  float a[G][VW], b[G][VW], A[VW], B[VW], h[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) {
+    A[e] = 1.f;
+    B[e] = 0.f;
+  }
+  // WHOLE: every step of the piece belongs to every row; otherwise steps past
+  // the sequence or the row are a = 1, b = 0 (they read a step that is there)
+  auto compose = [&](auto w) {
+    constexpr bool WHOLE = decltype(w)::value;
+#pragma unroll
+    for (int s = 0; s < G; ++s) {
+      float vp[VW], vq[VW];
+      V::get(rp[s], vp);
+      V::get(rq[s], vq);
+      const int i = i0 + s, t = at.d ? p.T - 1 - i : i;
+      const bool valid = WHOLE || (i < p.T && t < len);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        float na, n;
+        coeffs<MODE>(vp[e], vq[e], a[s][e], na, n);
+        b[s][e] = valid ? na * n : 0.f;
+        if (!valid) a[s][e] = 1.f;
+        A[e] *= a[s][e];
+        B[e] = fmaf(a[s][e], B[e], b[s][e]);
+      }
+    }
+  };
+  if (whole) compose(std::true_type{});
+  else compose(std::false_type{});
+  join<VW, kScanFwdSuper, kScanFwdWaves>(p, at.pos, C, c, l.live, p.h0, wave, lane, W, sA, sB, sh, A, B, h);
+  if (!l.live) return;
+  auto walk = [&](auto w) {
+    constexpr bool WHOLE = decltype(w)::value;
+#pragma unroll
+    for (int s = 0; s < G; ++s) {
+      const int i = i0 + s, t = at.d ? p.T - 1 - i : i;
+      if (s % kScanKeep == 0 && (WHOLE || i < p.T)) {
+        float* kept = p.starts + (long long)(i / kScanKeep) * C + c;
+#pragma unroll
+        for (int e = 0; e < VW; ++e) kept[e] = h[e];
+      }
+      float o[VW];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        h[e] = fmaf(a[s][e], h[e], b[s][e]);
+        o[e] = WHOLE || t < len ? h[e] : 0.f;
+      }
+      if (WHOLE || i < p.T) st<T>(y + t * yrow, l.y, V::make(o));
+    }
+  };
+  if (whole) walk(std::true_type{});
+  else walk(std::false_type{});
+  if (p.hy && at.pos == p.chunks - 1 && wave == W - 1)
+#pragma unroll
+    for (int e = 0; e < VW; ++e) p.hy[c + e] = h[e];
+}
+
+template <bool BF, int MODE, int VW>
+__global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(const ScanParams p) {
+  using V = Vec<BF, VW>;
+  using T = typename V::T;
+  constexpr int ES = BF ? 2 : 4, G = kScanBwdSteps;
+  __shared__ float sA[kScanBwdWaves][64 * VW], sB[kScanBwdWaves][64 * VW], sh[64 * VW];
+  __shared__ unsigned shared;
+  const Place at = place(p, VW, shared);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+  const long long C = (long long)p.D * p.B * p.H;
+  long long gbase, ybase;
+  Lanes l;
+  lanes<BF, VW>(p, at, lane, gbase, ybase, l);
+  const long long c = (long long)at.d * p.B * p.H + at.c0 + lane * VW;
+  const long long grow = (long long)p.B * p.D * 2 * p.H * ES, yrow = grow / 2;
+  const char* g = (const char*)p.g + gbase * ES;
+  const char* dy = (const char*)p.dy + ybase * ES;
+  char* dg = (char*)p.dg + gbase * ES;
+  const long long half = (long long)p.H * ES;
+  const int len = p.lengths ? min(max(p.lengths[l.b], 0), p.T) : p.T;
+  // the first wave of the first chunk has the last steps
+  const int piece = (p.chunks - 1 - at.pos) * W + (W - 1 - wave), i0 = piece * G;
+  const bool whole = !p.lengths && i0 + G <= p.T;
+
+  T rp[G], rq[G], rd[G];
+  float h[VW];
+#pragma unroll
+  for (int e = 0; e < VW; ++e) h[e] = i0 < p.T && l.live ? p.starts[(long long)(i0 / kScanKeep) * C + c + e] : 0.f;
+#pragma unroll
+  for (int s = 0; s < G; ++s) {
+    const int i = min(i0 + s, p.T - 1), t = at.d ? p.T - 1 - i : i;
+    const char* row = g + t * grow;
+    rp[s] = ld<T>(row, l.g);
+    rq[s] = ld<T>(row + half, l.g);
+    rd[s] = ld<T>(dy + t * yrow, l.y);
+  }
+  // a, dp = f (dy + D), dq = f2 (dy + D)
+  float a[G][VW], f[G][VW], f2[G][VW], A[VW], B[VW], D[VW];
+  auto compose = [&](auto w) {
+    constexpr bool WHOLE = decltype(w)::value;
+#pragma unroll
+    for (int s = 0; s < G; ++s) {
+      float vp[VW], vq[VW];
+      V::get(rp[s], vp);
+      V::get(rq[s], vq);
+      const int i = i0 + s, t = at.d ? p.T - 1 - i : i;
+      const bool valid = WHOLE || (i < p.T && t < len);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        float na, n;
+        coeffs<MODE>(vp[e], vq[e], a[s][e], na, n);
+        if constexpr (MODE == SCAN_GATED) {
+          f[s][e] = (h[e] - n) * (a[s][e] * na);
+          f2[s][e] = na * fmaf(-n, n, 1.f);
+        } else {
+          f[s][e] = h[e];
+          f2[s][e] = 1.f;
+        }
+        if (!valid) {
+          a[s][e] = 1.f;
+          f[s][e] = f2[s][e] = 0.f;
+        }
+        h[e] = fmaf(a[s][e], h[e], valid ? na * n : 0.f);
+      }
+      if (!valid) {
+        float zero[VW] = {};
+        rd[s] = V::make(zero);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      A[e] = a[G - 1][e];
+      B[e] = 0.f;
+    }
+    // B: dy + D of the step, D of nothing being 0
+    V::get(rd[G - 1], B);
+#pragma unroll
+    for (int s = G - 2; s >= 0; --s) {
+      float v[VW];
+      V::get(rd[s], v);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        A[e] *= a[s][e];
+        B[e] = fmaf(a[s + 1][e], B[e], v[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VW; ++e) B[e] *= a[0][e];
+  };
+  if (whole) compose(std::true_type{});
+  else compose(std::false_type{});
+  join<VW, kScanBwdSuper, kScanBwdWaves>(p, at.pos, C, c, l.live, p.dhy, wave, lane, W, sA, sB, sh, A, B, D);
+  if (!l.live) return;
+  auto walk = [&](auto w) {
+    constexpr bool WHOLE = decltype(w)::value;
+#pragma unroll
+    for (int s = G - 1; s >= 0; --s) {
+      const int i = i0 + s, t = at.d ? p.T - 1 - i : i;
+      float v[VW], op[VW], oq[VW];
+      V::get(rd[s], v);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        D[e] = s == G - 1 ? D[e] + v[e] : fmaf(a[s == G - 1 ? s : s + 1][e], D[e], v[e]);
+        const bool valid = WHOLE || t < len;
+        op[e] = valid ? D[e] * f[s][e] : 0.f;    // D itself may be infinite or NaN
+        oq[e] = valid ? D[e] * f2[s][e] : 0.f;
+      }
+      if (WHOLE || i < p.T) {
+        char* row = dg + t * grow;
+        st<T>(row, l.g, V::make(op));
+        st<T>(row + half, l.g, V::make(oq));
+      }
+    }
+  };
+  if (whole) walk(std::true_type{});
+  else walk(std::false_type{});
+  if (p.dh0 && at.pos == p.chunks - 1 && wave == W - 1)
+#pragma unroll
+    for (int e = 0; e < VW; ++e) p.dh0[c + e] = a[0][e] * D[e];
+}
+
+// T == 0: the states pass through
+__global__ __launch_bounds__(256) void pass_kernel(long long n, const float* from, float* to) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) to[i] = from ? from[i] : 0.f;
+}
+
+template <bool BACK, bool BF, int MODE>
+void start(const ScanParams& p, bool two, dim3 grid, dim3 block, hipStream_t s) {
+  if constexpr (BACK) {
+    if (BF && two) hipLaunchKernelGGL((bwd_kernel<BF, MODE, BF ? 2 : 1>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((bwd_kernel<BF, MODE, 1>), grid, block, 0, s, p);
+  } else {
+    if (BF && two) hipLaunchKernelGGL((fwd_kernel<BF, MODE, BF ? 2 : 1>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((fwd_kernel<BF, MODE, 1>), grid, block, 0, s, p);
+  }
+}
+
+template <bool BACK>
+hipError_t launch(const ScanParams& p, int mode, int bf16, hipStream_t s) {
+  const long long C = (long long)p.D * p.B * p.H;
+  if (C == 0) return hipSuccess;
+  if (p.T == 0) {
+    float* to = BACK ? p.dh0 : p.hy;
+    if (to) hipLaunchKernelGGL(pass_kernel, dim3((unsigned)((C + 255) / 256)), dim3(256), 0, s, C, BACK ? p.dhy : p.h0, to);
+    return hipGetLastError();
+  }
+  // bf16: two channels (4 bytes) a lane where they never straddle two rows of
+  // the batch and are aligned; fp32 has 4 bytes a lane with one
+  const uintptr_t bases = (uintptr_t)p.g | (BACK ? (uintptr_t)p.dy | (uintptr_t)p.dg : (uintptr_t)p.y);
+  const bool two = bf16 && p.H % 2 == 0 && (bases & 3) == 0;
+  const long long BH = (long long)p.B * p.H, tiles = (BH + (two ? 127 : 63)) / (two ? 128 : 64) * p.D;
+  if (tiles * p.chunks > 0x7fffffffLL) return hipErrorInvalidValue;
+  if (p.chunks > 1) {
+    const long long words = (long long)(p.chunks * 2 + p.chunks / (BACK ? kScanBwdSuper : kScanFwdSuper) + 1) * C;
+    const long long counters = ((char*)p.maps - (char*)p.counters) / 16, all = counters + (words + 3) / 4;
+    const dim3 grid((unsigned)std::min<long long>((all + 255) / 256, 2048));
+    hipLaunchKernelGGL(clear_kernel, grid, dim3(256), 0, s, p.head, counters, all);
+  }
+  const dim3 grid((unsigned)(tiles * p.chunks)), block(64 * p.waves);
+  if (bf16 && mode == SCAN_GATED) start<BACK, true, SCAN_GATED>(p, two, grid, block, s);
+  else if (bf16) start<BACK, true, SCAN_LINEAR>(p, two, grid, block, s);
+  else if (mode == SCAN_GATED) start<BACK, false, SCAN_GATED>(p, two, grid, block, s);
+  else start<BACK, false, SCAN_LINEAR>(p, two, grid, block, s);
+  return hipGetLastError();
 }
 
 }  // namespace
-
-#define SCAN_PICK(KERNEL, GRID, BLOCK, ...)                                                              \
-  do {                                                                                                   \
-    if (bf16 && mode == SCAN_GATED) hipLaunchKernelGGL((KERNEL<true, SCAN_GATED>), GRID, BLOCK, 0, s, __VA_ARGS__); \
-    else if (bf16) hipLaunchKernelGGL((KERNEL<true, SCAN_LINEAR>), GRID, BLOCK, 0, s, __VA_ARGS__);      \
-    else if (mode == SCAN_GATED) hipLaunchKernelGGL((KERNEL<false, SCAN_GATED>), GRID, BLOCK, 0, s, __VA_ARGS__); \
-    else hipLaunchKernelGGL((KERNEL<false, SCAN_LINEAR>), GRID, BLOCK, 0, s, __VA_ARGS__);               \
-  } while (0)
 
 hipError_t rnn_launch_scan_step(int mode, int bf16, int B, int H, const void* g, const float* h, void* y, float* hy,
                                 hipStream_t s) {
   const long long n = (long long)B * H;
   if (n == 0) return hipSuccess;
-  const dim3 grid((unsigned)((n + 255) / 256));
-  SCAN_PICK(step_kernel, grid, dim3(256), B, H, g, h, y, hy);
+  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+  if (bf16 && mode == SCAN_GATED) hipLaunchKernelGGL((step_kernel<true, SCAN_GATED>), grid, block, 0, s, B, H, g, h, y, hy);
+  else if (bf16) hipLaunchKernelGGL((step_kernel<true, SCAN_LINEAR>), grid, block, 0, s, B, H, g, h, y, hy);
+  else if (mode == SCAN_GATED) hipLaunchKernelGGL((step_kernel<false, SCAN_GATED>), grid, block, 0, s, B, H, g, h, y, hy);
+  else hipLaunchKernelGGL((step_kernel<false, SCAN_LINEAR>), grid, block, 0, s, B, H, g, h, y, hy);
   return hipGetLastError();
 }
 
-hipError_t rnn_launch_scan_fwd(const ScanParams& p, int mode, int bf16, hipStream_t s) {
-  const long long C = (long long)p.D * p.B * p.H;
-  if (C == 0) return hipSuccess;
-  SCAN_PICK(fwd_kernel, dim3((unsigned)((C + 63) / 64)), dim3(64), p);
-  return hipGetLastError();
-}
-
-hipError_t rnn_launch_scan_bwd(const ScanParams& p, int mode, int bf16, hipStream_t s) {
-  const long long C = (long long)p.D * p.B * p.H;
-  if (C == 0) return hipSuccess;
-  SCAN_PICK(bwd_kernel, dim3((unsigned)((C + 63) / 64)), dim3(64), p);
-  return hipGetLastError();
-}
+hipError_t rnn_launch_scan_fwd(const ScanParams& p, int mode, int bf16, hipStream_t s) { return launch<false>(p, mode, bf16, s); }
+hipError_t rnn_launch_scan_bwd(const ScanParams& p, int mode, int bf16, hipStream_t s) { return launch<true>(p, mode, bf16, s); }
