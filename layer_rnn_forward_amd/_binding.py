@@ -313,16 +313,15 @@ def rnn_profile_read(h, kernel: int):
 _WTYPE_OF = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _addr(t, name, dtype, shape, optional=False):
-    """Device address of ``t`` after its checks (None: NULL where optional)."""
-    if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name} must be a torch.Tensor")
+def _addr(t, name, dev, dtype, shape, optional=False):
+    """Device address of ``t`` after its checks (None: NULL where optional);
+    ``dev``: index of the device that the call's first tensor is on."""
+    if t is None and optional:
+        return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor" + (" or None" if optional else ""))
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor, on the same device as the others")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -332,25 +331,42 @@ def _addr(t, name, dtype, shape, optional=False):
     return t.data_ptr()
 
 
-def _room(t, name, optional=False):
+def _room(t, name, dev, optional=False):
     """Address and size in bytes of a workspace, reserve or checkpoint."""
     if t is None and optional:
         return None, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous device tensor")
+    if dev < 0 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor, on the same device as the others")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _elements(t, name, dims):
+    """Type, its code and the device index of a tensor of ``dims`` dimensions."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _WTYPE_OF:
         raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    return t.dtype, _WTYPE_OF[t.dtype]
+    _ints(*t.shape)
+    return t.dtype, _WTYPE_OF[t.dtype], t.get_device()
+
+
+def _ints(*sizes):
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            raise ValueError(f"{n} does not fit a C int")
+
+
+def _on(dev):
+    """The current stream, which has to be of the tensors' device."""
+    if dev < 0:
+        raise ValueError("the tensors must be device tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors' device ({dev}) must be the current one")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _choice(table, key, name):
@@ -363,6 +379,7 @@ def _choice(table, key, name):
 def rnn_scan_workspace_size(T: int, B: int, H: int, num_dirs: int = 1) -> int:
     """Bytes of the workspace that one rnn_scan_forward fills and the
     rnn_scan_backward calls after it read."""
+    _ints(T, B, H, num_dirs)
     n = ctypes.c_size_t()
     _check(load_library().rnn_scan_workspace_size(T, B, H, num_dirs, ctypes.byref(n)), "rnn_scan_workspace_size")
     return n.value
@@ -373,14 +390,14 @@ def rnn_scan_step(mode, g, h, y, hy):
     ``g`` [B, 2H]; ``h`` (or None: zeros) and ``hy`` [B, H] float32, which may
     be the same tensor; ``y`` [B, H] in g's type, or None."""
     m = _choice(SCAN_MODES, mode, "mode")
-    dt, w = _elements(g, "g", 2)
+    dt, w, dev = _elements(g, "g", 2)
     B, H2 = g.shape
     if H2 % 2:
         raise ValueError("g must have an even number of columns")
     bh = (B, H2 // 2)
     _check(load_library().rnn_scan_step(
-        _stream(), m, w, B, H2 // 2, _addr(g, "g", dt, g.shape), _addr(h, "h", torch.float32, bh, True),
-        _addr(y, "y", dt, bh, True), _addr(hy, "hy", torch.float32, bh)), "rnn_scan_step")
+        _on(dev), m, w, B, H2 // 2, _addr(g, "g", dev, dt, g.shape), _addr(h, "h", dev, torch.float32, bh, True),
+        _addr(y, "y", dev, dt, bh, True), _addr(hy, "hy", dev, torch.float32, bh)), "rnn_scan_step")
 
 
 def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
@@ -390,17 +407,17 @@ def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
     ``y`` [T, B, dirs*H]; ``hy`` [dirs, B, H] float32 (its shape gives dirs
     and H); ``h0`` as hy, or None (zeros); ``lengths`` int32 [B] or None."""
     m = _choice(SCAN_MODES, mode, "mode")
-    dt, w = _elements(g, "g", 3)
+    dt, w, dev = _elements(g, "g", 3)
     if not isinstance(hy, torch.Tensor) or hy.dim() != 3:
         raise ValueError("hy must be a tensor [dirs, B, H]")
     T, B = g.shape[:2]
     D, H = hy.shape[0], hy.shape[2]
     st = (D, B, H)
-    wp, wn = _room(ws, "ws")
+    wp, wn = _room(ws, "ws", dev)
     _check(load_library().rnn_scan_forward(
-        _stream(), m, w, T, B, H, D, _addr(g, "g", dt, (T, B, D * 2 * H)),
-        _addr(h0, "h0", torch.float32, st, True), _addr(lengths, "lengths", torch.int32, (B,), True),
-        _addr(y, "y", dt, (T, B, D * H)), _addr(hy, "hy", torch.float32, st), wp, wn), "rnn_scan_forward")
+        _on(dev), m, w, T, B, H, D, _addr(g, "g", dev, dt, (T, B, D * 2 * H)),
+        _addr(h0, "h0", dev, torch.float32, st, True), _addr(lengths, "lengths", dev, torch.int32, (B,), True),
+        _addr(y, "y", dev, dt, (T, B, D * H)), _addr(hy, "hy", dev, torch.float32, st), wp, wn), "rnn_scan_forward")
 
 
 def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
@@ -408,21 +425,22 @@ def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
     h0 and lengths): ``dy`` [T, B, dirs*H], ``dhy`` as hy or None (zeros);
     ``dg`` as g, ``dh0`` [dirs, B, H] float32 (its shape gives dirs and H)."""
     m = _choice(SCAN_MODES, mode, "mode")
-    dt, w = _elements(g, "g", 3)
+    dt, w, dev = _elements(g, "g", 3)
     if not isinstance(dh0, torch.Tensor) or dh0.dim() != 3:
         raise ValueError("dh0 must be a tensor [dirs, B, H]")
     T, B = g.shape[:2]
     D, H = dh0.shape[0], dh0.shape[2]
     st = (D, B, H)
-    wp, wn = _room(ws, "ws")
+    wp, wn = _room(ws, "ws", dev)
     _check(load_library().rnn_scan_backward(
-        _stream(), m, w, T, B, H, D, _addr(g, "g", dt, (T, B, D * 2 * H)),
-        _addr(h0, "h0", torch.float32, st, True), _addr(lengths, "lengths", torch.int32, (B,), True),
-        _addr(dy, "dy", dt, (T, B, D * H)), _addr(dhy, "dhy", torch.float32, st, True),
-        _addr(dg, "dg", dt, (T, B, D * 2 * H)), _addr(dh0, "dh0", torch.float32, st), wp, wn), "rnn_scan_backward")
+        _on(dev), m, w, T, B, H, D, _addr(g, "g", dev, dt, (T, B, D * 2 * H)),
+        _addr(h0, "h0", dev, torch.float32, st, True), _addr(lengths, "lengths", dev, torch.int32, (B,), True),
+        _addr(dy, "dy", dev, dt, (T, B, D * H)), _addr(dhy, "dhy", dev, torch.float32, st, True),
+        _addr(dg, "dg", dev, dt, (T, B, D * 2 * H)), _addr(dh0, "dh0", dev, torch.float32, st), wp, wn), "rnn_scan_backward")
 
 
 def rnn_ffn_workspace_size(M: int, D: int, F: int, wtype: str, save: str = "none") -> int:
+    _ints(M, D, F)
     n = ctypes.c_size_t()
     _check(load_library().rnn_ffn_workspace_size(M, D, F, _choice(WTYPES, wtype, "wtype"),
                                                  _choice(SAVES, save, "save"), ctypes.byref(n)),
@@ -432,6 +450,7 @@ def rnn_ffn_workspace_size(M: int, D: int, F: int, wtype: str, save: str = "none
 
 def rnn_ffn_reserve_size(M: int, D: int, F: int, wtype: str, save: str = "none") -> int:
     """Bytes that rnn_ffn_forward keeps for rnn_ffn_backward (0 for "none")."""
+    _ints(M, D, F)
     n = ctypes.c_size_t()
     _check(load_library().rnn_ffn_reserve_size(M, D, F, _choice(WTYPES, wtype, "wtype"),
                                                _choice(SAVES, save, "save"), ctypes.byref(n)),
@@ -445,15 +464,15 @@ def rnn_ffn_forward(act, x, w_in, w_out, y, ws, save="none", reserve=None):
     all float32 or all bfloat16; act "sigmoid", "silu" or "gelu" (tanh form);
     save "none", "full" or "int8": what ``reserve`` keeps for backward."""
     a, sv = _choice(ACTS, act, "act"), _choice(SAVES, save, "save")
-    dt, w = _elements(x, "x", 2)
+    dt, w, dev = _elements(x, "x", 2)
     _elements(w_out, "w_out", 2)
     M, D = x.shape
     F = w_out.shape[1]
-    wp, wn = _room(ws, "ws")
-    rp, rn = _room(reserve, "reserve", True)
+    wp, wn = _room(ws, "ws", dev)
+    rp, rn = _room(reserve, "reserve", dev, True)
     _check(load_library().rnn_ffn_forward(
-        _stream(), a, w, sv, M, D, F, _addr(x, "x", dt, (M, D)), _addr(w_in, "w_in", dt, (2 * F, D)),
-        _addr(w_out, "w_out", dt, (D, F)), _addr(y, "y", dt, (M, D)), wp, wn, rp, rn), "rnn_ffn_forward")
+        _on(dev), a, w, sv, M, D, F, _addr(x, "x", dev, dt, (M, D)), _addr(w_in, "w_in", dev, dt, (2 * F, D)),
+        _addr(w_out, "w_out", dev, dt, (D, F)), _addr(y, "y", dev, dt, (M, D)), wp, wn, rp, rn), "rnn_ffn_forward")
 
 
 def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reserve):
@@ -461,21 +480,22 @@ def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reser
     be None with save "int8"; each of ``dx``, ``dw_in`` and ``dw_out`` may be
     None (not wanted)."""
     a, sv = _choice(ACTS, act, "act"), _choice(SAVES, save, "save")
-    dt, w = _elements(dy, "dy", 2)
+    dt, w, dev = _elements(dy, "dy", 2)
     _elements(w_out, "w_out", 2)
     M, D = dy.shape
     F = w_out.shape[1]
-    wp, wn = _room(ws, "ws")
-    rp, rn = _room(reserve, "reserve")
+    wp, wn = _room(ws, "ws", dev)
+    rp, rn = _room(reserve, "reserve", dev)
     _check(load_library().rnn_ffn_backward(
-        _stream(), a, w, sv, M, D, F, _addr(x, "x", dt, (M, D), True), _addr(w_in, "w_in", dt, (2 * F, D)),
-        _addr(w_out, "w_out", dt, (D, F)), _addr(dy, "dy", dt, (M, D)), _addr(dx, "dx", dt, (M, D), True),
-        _addr(dw_in, "dw_in", dt, (2 * F, D), True), _addr(dw_out, "dw_out", dt, (D, F), True), wp, wn, rp, rn),
+        _on(dev), a, w, sv, M, D, F, _addr(x, "x", dev, dt, (M, D), True), _addr(w_in, "w_in", dev, dt, (2 * F, D)),
+        _addr(w_out, "w_out", dev, dt, (D, F)), _addr(dy, "dy", dev, dt, (M, D)), _addr(dx, "dx", dev, dt, (M, D), True),
+        _addr(dw_in, "dw_in", dev, dt, (2 * F, D), True), _addr(dw_out, "dw_out", dev, dt, (D, F), True), wp, wn, rp, rn),
         "rnn_ffn_backward")
 
 
 def rnn_checkpoint_size(rows: int, cols: int) -> int:
     """Bytes of the 8-bit checkpoint of a matrix [rows, cols]."""
+    _ints(rows, cols)
     n = ctypes.c_size_t()
     _check(load_library().rnn_checkpoint_size(rows, cols, ctypes.byref(n)), "rnn_checkpoint_size")
     return n.value
@@ -484,19 +504,19 @@ def rnn_checkpoint_size(rows: int, cols: int) -> int:
 def rnn_checkpoint_store(x, kept):
     """Keep ``x`` [rows, cols] in 8 bits a value with one power of two per 32
     columns of a row, in the buffer ``kept``."""
-    dt, w = _elements(x, "x", 2)
-    kp, kn = _room(kept, "kept")
-    _check(load_library().rnn_checkpoint_store(_stream(), w, x.shape[0], x.shape[1], _addr(x, "x", dt, x.shape),
+    dt, w, dev = _elements(x, "x", 2)
+    kp, kn = _room(kept, "kept", dev)
+    _check(load_library().rnn_checkpoint_store(_on(dev), w, x.shape[0], x.shape[1], _addr(x, "x", dev, dt, x.shape),
                                                kp, kn), "rnn_checkpoint_store")
 
 
 def rnn_checkpoint_load(kept, x):
     """Read a checkpoint of a matrix of x's shape back into ``x`` [rows, cols]
     (float32 or bfloat16; both hold its values exactly)."""
-    dt, w = _elements(x, "x", 2)
-    kp, kn = _room(kept, "kept")
-    _check(load_library().rnn_checkpoint_load(_stream(), w, x.shape[0], x.shape[1], kp, kn,
-                                              _addr(x, "x", dt, x.shape)), "rnn_checkpoint_load")
+    dt, w, dev = _elements(x, "x", 2)
+    kp, kn = _room(kept, "kept", dev)
+    _check(load_library().rnn_checkpoint_load(_on(dev), w, x.shape[0], x.shape[1], kp, kn,
+                                              _addr(x, "x", dev, dt, x.shape)), "rnn_checkpoint_load")
 
 
 # ------------------------------------------------------------ weight packing

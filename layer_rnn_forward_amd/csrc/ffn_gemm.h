@@ -278,12 +278,6 @@ __device__ __forceinline__ void load_group16(const int16_t* q, int ex, float (&v
   }
 }
 
-__device__ __forceinline__ void act_one(int act, float g, float& a, float& da) {
-  if (act == ACT_SILU) act_pair<ACT_SILU>(g, a, da);
-  else if (act == ACT_GELU) act_pair<ACT_GELU>(g, a, da);
-  else act_pair<ACT_SIGMOID>(g, a, da);
-}
-
 template <int ACT, bool BF, int SAVE>
 __device__ __forceinline__ void glu_tile(const f32x16& gv, const f32x16& uv, const FfnGemm& p, long long m, int f, int h) {
   float a[16], da[16], o[16];

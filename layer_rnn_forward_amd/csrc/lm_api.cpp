@@ -240,6 +240,18 @@ rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn
   if (!x || !y || (F > 0 && (!w_in || !w_out))) return RNN_STATUS_INVALID_ARG;
   const int bf = wtype == RNN_W_BF16;
   const hipStream_t s = hs(stream);
+  if (save == RNN_SAVE_NONE && M <= kFfnRows) {
+    FfnRows r{};
+    r.M = M; r.R = F; r.K = D;
+    r.x = x; r.ldx = D; r.w = w_in;
+    r.out = at<void>(ws, p.h); r.ldo = p.Fp;
+    r.act = act;
+    LM_TRY(dev(rnn_launch_ffn_rows(r, bf, 1, s)));
+    r.R = D; r.K = F;
+    r.x = r.out; r.ldx = p.Fp; r.w = w_out;
+    r.out = y; r.ldo = D;
+    return dev(rnn_launch_ffn_rows(r, bf, 0, s));
+  }
   Pads pads;
   const void* xp = pads.add(x, M, D, p.Dp, at<void>(ws, p.x));
   const void* wi = pads.add(w_in, 2LL * F, D, p.Dp, at<void>(ws, p.w_in));

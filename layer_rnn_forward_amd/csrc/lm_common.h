@@ -73,6 +73,19 @@ struct FfnGemm {
   long long ldh;
 };
 
+// One product of the block for few rows (ffn_rows.hip): w [R or 2R, K]
+// contiguous, any alignment.
+constexpr int kFfnRows = 64;   // rows at most
+struct FfnRows {
+  int M, R, K;
+  const void* x;
+  long long ldx;
+  const void* w;
+  void* out;
+  long long ldo;
+  int act;               // of the gated product
+};
+
 // Copies of up to three matrices with rows padded by zeros to a multiple of
 // 16 bytes.
 struct PadJob {
@@ -94,6 +107,7 @@ hipError_t rnn_launch_scan_bwd(const rnnk::ScanParams& p, int mode, int bf16, hi
 hipError_t rnn_launch_ffn_glu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
 hipError_t rnn_launch_ffn_dglu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
 hipError_t rnn_launch_ffn_store(const rnnk::FfnGemm& p, int bf16, int layout, hipStream_t s);
+hipError_t rnn_launch_ffn_rows(const rnnk::FfnRows& p, int bf16, int glu, hipStream_t s);
 hipError_t rnn_launch_pad(const rnnk::PadJob& j, int bf16, hipStream_t s);
 
 hipError_t rnn_launch_ckpt_store(int bf16, int rows, int cols, const void* x, void* kept, hipStream_t s);

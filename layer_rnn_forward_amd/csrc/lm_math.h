@@ -1,6 +1,8 @@
 // Activations and elements of the language-model operators (gfx950).
 #pragma once
 
+#include <type_traits>
+
 #include "device_util.h"
 #include "lm_common.h"
 
@@ -18,6 +20,12 @@ __device__ __forceinline__ void el_store(El<BF16>* p, float v) {
   if constexpr (BF16) *p = f2bf(v); else *p = v;
 }
 
+// N bytes at any address (global loads and stores take 16 bytes at any alignment)
+template <int N>
+struct __attribute__((packed, aligned(1))) Bytes {
+  uint32_t w[N / 4];
+};
+
 // sigmoid(p) and sigmoid(-p) from e = exp(-|p|) <= 1: 1/(1+e) is the larger
 // of the two and e/(1+e) the smaller, so neither cancels nor overflows.
 __device__ __forceinline__ void sigmoid_pair(float p, float& pos, float& neg) {
@@ -25,7 +33,6 @@ __device__ __forceinline__ void sigmoid_pair(float p, float& pos, float& neg) {
   const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
   pos = p >= 0.f ? big : small;
   neg = p >= 0.f ? small : big;
-  if (p != p) pos = neg = p;
 }
 
 // act(g) and its derivative.
@@ -48,6 +55,14 @@ __device__ __forceinline__ void act_pair(float g, float& a, float& da) {
       da = s + g * s * n;
     }
   }
+}
+
+__device__ __forceinline__ float act_of(int act, float g) {
+  float a, da;
+  if (act == ACT_SILU) act_pair<ACT_SILU>(g, a, da);
+  else if (act == ACT_GELU) act_pair<ACT_GELU>(g, a, da);
+  else act_pair<ACT_SIGMOID>(g, a, da);
+  return a;
 }
 
 }  // namespace rnnk
