@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librnn_mi355x.so")
-SOURCES = ["checkpoint.hip", "dropout.hip", "ffn.hip", "ffn_rows.hip", "gemm.hip", "layout.hip", "lm_api.cpp", "recurrent.hip",
+SOURCES = ["checkpoint.hip", "dropout.hip", "ffn.hip", "ffn_dglu.hip", "ffn_glu.hip", "ffn_rows.hip", "gemm.hip", "layout.hip", "lm_api.cpp", "recurrent.hip",
            "recurrent_gru2.hip", "rnn_api.cpp", "scan.hip",
            *[f"recurrent_{m}_{k}.hip" for m in ("tanh", "lstm", "gru") for k in ("fwd", "bwd")]]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -84,22 +84,28 @@ struct Operand {
     }
   }
 
-  // fill one stage: k values base + [0, BK), those at or past kleft are zero.
-  // HALF > 0: of every 2 * HALF tile rows the second HALF are read from base2
+  // load j of the fill of one stage: k values base + [0, BK), those at or past
+  // kleft are zero.  HALF > 0: of every 2 * HALF tile rows the second HALF are
+  // read from base2
   template <int HALF = 0>
-  __device__ __forceinline__ void load(const char* base, int kleft, lds_char* stage, int wave,
+  __device__ __forceinline__ void load(int j, const char* base, int kleft, lds_char* stage, int wave,
                                        const char* base2 = nullptr) const {
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const unsigned v = klane[ROWS ? 0 : j] < kleft ? voff[j] : kOutside;
-      const char* b = base;
-      if constexpr (HALF > 0) b = (8 * (4 * j + wave)) % (2 * HALF) >= HALF ? base2 : base;
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)b, 0, 0x7fffffff, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(stage + (4 * j + wave) * 1024),
-                                               16, v, 0, 0, 0);
-    }
+    const unsigned v = klane[ROWS ? 0 : j] < kleft ? voff[j] : kOutside;
+    const char* b = base;
+    if constexpr (HALF > 0) b = (8 * (4 * j + wave)) % (2 * HALF) >= HALF ? base2 : base;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)b, 0, 0x7fffffff, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(stage + (4 * j + wave) * 1024), 16,
+                                             v, 0, 0, 0);
   }
 };
+
+// The transposing LDS read.  (A restrict pointer: without it the compiler waits
+// for every load into LDS before each of these; the product's own waits and
+// barriers order them.)
+__device__ __forceinline__ u32x2 read_tr(const lds_char* __restrict p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+}
 
 // Fragment reader of a wave's T tiles of 32 rows.
 template <bool BF, bool ROWS, int R, int T>
@@ -125,22 +131,17 @@ struct Reader {
       for (int t = 0; t < T; ++t) off[t] = q * 4 * Op::PITCH + (first + t * 32 + i) * 4;
     }
   }
-  __device__ __forceinline__ void read(const lds_char* stage, int kk, u32x4 (&f)[T]) const {
+  __device__ __forceinline__ void read(const lds_char* stage, int kk, int t, u32x4& f) const {
+    if constexpr (ROWS) {
+      f = *(const __attribute__((address_space(3))) u32x4*)(stage + off[kk] + t * 32 * 128);
+    } else if constexpr (BF) {
+      const lds_char* p = stage + off[t] + kk * 16 * Op::PITCH;
+      const u32x2 a = read_tr(p), b = read_tr(p + 4 * Op::PITCH);
+      f = u32x4{a.x, a.y, b.x, b.y};
+    } else {
+      const lds_char* p = stage + off[t] + kk * 8 * Op::PITCH;
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      if constexpr (ROWS) {
-        f[t] = *(const __attribute__((address_space(3))) u32x4*)(stage + off[kk] + t * 32 * 128);
-      } else if constexpr (BF) {
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const lds_char* p = stage + off[t] + kk * 16 * Op::PITCH;
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * Op::PITCH)));
-        f[t] = u32x4{a.x, a.y, b.x, b.y};
-      } else {
-        const lds_char* p = stage + off[t] + kk * 8 * Op::PITCH;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[t][e] = *(const __attribute__((address_space(3))) unsigned*)(p + e * Op::PITCH);
-      }
+      for (int e = 0; e < 4; ++e) f[e] = *(const __attribute__((address_space(3))) unsigned*)(p + e * Op::PITCH);
     }
   }
 };
@@ -210,128 +211,140 @@ __device__ __forceinline__ unsigned group_top(const float (&v)[16]) {
 
 constexpr int kBadGroup = -128;   // exponent byte of a group that holds an infinity or a NaN
 
-// 32 columns of a row as 8-bit checkpoint units; q points at the group's first byte.
-__device__ __forceinline__ void store_group8(int8_t* q, int8_t* ex, const float (&v)[16], int h) {
+// What is saved for backward lies tile by tile: 32 rows x 32 columns, each
+// lane's 16 values where its lane number says, so that a wave writes and reads
+// them in runs of 1 KB (rows of C would be 64 byte pieces).  A group of 32
+// columns is a row of a tile, and its exponent byte is at the row's number.
+//
+// 8 bits: checkpoint units (include/rnn.h), 16 bytes a lane.
+__device__ __forceinline__ u32x4 pack8(const float (&v)[16], int& ex) {
   const unsigned top = group_top(v);
   const bool bad = top >= 0x7f800000u;
   const int e = max((int)(top >> 23) - 133, -126);
   const float inv = bad ? 0.f : __uint_as_float((unsigned)(127 - e) << 23);
-  unsigned w[4];
+  u32x4 w;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     w[j] = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int x = (int)fminf(fmaxf(rintf(v[4 * j + k] * inv), -127.f), 127.f);
-      w[j] |= (unsigned)(x & 255) << (8 * k);
+      // + 1.5 * 2^23 rounds to the nearest whole number, ties to even, and leaves it in the low bits
+      const float u = __builtin_amdgcn_fmed3f(fmaf(v[4 * j + k], inv, 12582912.f), 12582912.f - 127.f, 12582912.f + 127.f);
+      w[j] |= (__float_as_uint(u) & 255u) << (8 * k);
     }
   }
-  // four columns a word: after the exchange half h holds columns 16i + 8h .. +7
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const auto s = __builtin_amdgcn_permlane32_swap(w[2 * i], w[2 * i + 1], false, false);
-    *reinterpret_cast<u32x2*>(q + 16 * i + 8 * h) = u32x2{s[0], s[1]};
-  }
-  if (h == 0) *ex = bad ? kBadGroup : (int8_t)e;
+  ex = bad ? kBadGroup : e;
+  return w;
 }
-__device__ __forceinline__ void load_group8(const int8_t* q, int ex, float (&v)[16], int h) {
+__device__ __forceinline__ void unpack8(const u32x4& w, int ex, float (&v)[16]) {
   const float s = ex == kBadGroup ? __uint_as_float(0x7fc00000u) : __uint_as_float((unsigned)(127 + ex) << 23);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const unsigned w = *reinterpret_cast<const unsigned*>(q + 8 * j + 4 * h);
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[4 * j + k] = (float)(int8_t)(w >> (8 * k)) * s;
-  }
+    for (int k = 0; k < 4; ++k) v[4 * j + k] = (float)(int8_t)(w[j] >> (8 * k)) * s;
 }
 
-// 32 columns of a row in 16 bits: whole numbers of 2^e, |q| <= 2^14, e the
-// exponent of the group's largest magnitude - 14, so the error is at most
-// 2^-14 of that magnitude (bf16 would be off by up to 2^-8 of each value, and
-// a product of two such values by twice that).  Adding 1.5 * 2^23 rounds to
-// the nearest whole number, ties to even, and leaves it in the low bits.
-__device__ __forceinline__ void store_group16(int16_t* q, int8_t* ex, const float (&v)[16], int h) {
+// 16 bits: whole numbers of 2^e, |q| <= 2^14, e the exponent of the group's
+// largest magnitude - 14, so the error is at most 2^-14 of that magnitude
+// (bf16 would be off by up to 2^-8 of each value, and a product of two such
+// values by twice that).
+__device__ __forceinline__ void pack16(const float (&v)[16], u32x4 (&w)[2], int& ex) {
   const unsigned top = group_top(v);
   const bool bad = top >= 0x7f800000u;
   const int e = max((int)(top >> 23) - 140, -126);
   const float inv = bad ? 0.f : __uint_as_float((unsigned)(127 - e) << 23);
-  unsigned w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const unsigned lo = __float_as_uint(fmaf(v[2 * i], inv, 12582912.f)), hi = __float_as_uint(fmaf(v[2 * i + 1], inv, 12582912.f));
-    w[i] = (lo & 0xffffu) | (hi << 16);
+    w[i / 4][i % 4] = __builtin_amdgcn_perm(hi, lo, 0x05040100);   // both lower halves
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const auto s0 = __builtin_amdgcn_permlane32_swap(w[4 * i], w[4 * i + 2], false, false);
-    const auto s1 = __builtin_amdgcn_permlane32_swap(w[4 * i + 1], w[4 * i + 3], false, false);
-    *reinterpret_cast<u32x4*>(q + 16 * i + 8 * h) = u32x4{s0[0], s1[0], s0[1], s1[1]};
-  }
-  if (h == 0) *ex = bad ? kBadGroup : (int8_t)e;
+  ex = bad ? kBadGroup : e;
 }
-__device__ __forceinline__ void load_group16(const int16_t* q, int ex, float (&v)[16], int h) {
+__device__ __forceinline__ void unpack16(const u32x4 (&w)[2], int ex, float (&v)[16]) {
   const float s = ex == kBadGroup ? __uint_as_float(0x7fc00000u) : __uint_as_float((unsigned)(127 + ex) << 23);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(q + 8 * j + 4 * h);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[4 * j + k] = (float)(int16_t)(w[k / 2] >> (16 * (k & 1))) * s;
-  }
+  for (int i = 0; i < 16; ++i) v[i] = (float)(int16_t)(w[i / 8][i / 2 % 4] >> (16 * (i & 1))) * s;
 }
 
+// One of the two saved tensors' tile: 1 (8 bits), 2 (16 bits) or 4 (fp32)
+// pieces of 16 bytes a lane.
+template <bool BF, int SAVE>
+struct Saved {
+  static constexpr int N = SAVE == SAVE_INT8 ? 1 : BF ? 2 : 4;
+  u32x4 w[N];
+  int ex;
+
+  __device__ __forceinline__ void pack(const float (&v)[16]) {
+    if constexpr (SAVE == SAVE_INT8) w[0] = pack8(v, ex);
+    else if constexpr (BF) pack16(v, w, ex);
+    else
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = __float_as_uint(v[i]);
+  }
+  __device__ __forceinline__ void unpack(float (&v)[16]) const {
+    if constexpr (SAVE == SAVE_INT8) unpack8(w[0], ex, v);
+    else if constexpr (BF) unpack16(w, ex, v);
+    else
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i / 4][i % 4]);
+  }
+  // values at `to` + tile * 1 KB * N, exponents at `e` + tile * 32
+  __device__ __forceinline__ void store(void* to, int8_t* e, long long tile, int lane) const {
+    u32x4* p = (u32x4*)to + tile * (64 * N) + lane;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[64 * i] = w[i];
+    if ((BF || SAVE == SAVE_INT8) && lane < 32) e[tile * 32 + lane] = (int8_t)ex;
+  }
+  __device__ __forceinline__ void load(const void* from, const int8_t* e, long long tile, int lane) {
+    const u32x4* p = (const u32x4*)from + tile * (64 * N) + lane;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = p[64 * i];
+    ex = BF || SAVE == SAVE_INT8 ? e[tile * 32 + (lane & 31)] : 0;
+  }
+};
+
+// projections of 32 columns -> the gated product, and what is saved
 template <int ACT, bool BF, int SAVE>
-__device__ __forceinline__ void glu_tile(const f32x16& gv, const f32x16& uv, const FfnGemm& p, long long m, int f, int h) {
+__device__ __forceinline__ void glu_tile(const f32x16& gv, const f32x16& uv, const FfnGemm& p, long long m, int f, int lane) {
   float a[16], da[16], o[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     act_pair<ACT>(gv[i], a[i], da[i]);
     o[i] = a[i] * uv[i];
+    da[i] *= uv[i];
   }
-  store_row<BF>((El<BF>*)p.C + m * p.ldc + f, o, h, 32, true);
-  if constexpr (SAVE == SAVE_FULL) {
+  store_row<BF>((El<BF>*)p.C + m * p.ldc + f, o, lane >> 5, 32, true);
+  if constexpr (SAVE != SAVE_NONE) {
+    const long long tile = (m >> 5) * p.lds + (f >> 5);
+    Saved<BF, SAVE> s0, s1;
+    if constexpr (SAVE == SAVE_INT8) {
+      float g[16], u[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) da[i] *= uv[i];
-    const long long at = m * p.lds + f, ate = m * p.lde + f / kGroup;
-    if constexpr (BF) {
-      store_group16((int16_t*)p.s0 + at, p.e0 + ate, a, h);
-      store_group16((int16_t*)p.s1 + at, p.e1 + ate, da, h);
+      for (int i = 0; i < 16; ++i) {
+        g[i] = gv[i];
+        u[i] = uv[i];
+      }
+      s0.pack(g);
+      s1.pack(u);
     } else {
-      store_row<false>((float*)p.s0 + at, a, h, 32, true);
-      store_row<false>((float*)p.s1 + at, da, h, 32, true);
+      s0.pack(a);
+      s1.pack(da);
     }
-  } else if constexpr (SAVE == SAVE_INT8) {
-    const long long at = m * p.lds + f, ate = m * p.lde + f / kGroup;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      a[i] = gv[i];
-      da[i] = uv[i];
-    }
-    store_group8((int8_t*)p.s0 + at, p.e0 + ate, a, h);
-    store_group8((int8_t*)p.s1 + at, p.e1 + ate, da, h);
+    s0.store(p.s0, p.e0, tile, lane);
+    s1.store(p.s1, p.e1, tile, lane);
   }
 }
 
 // dh of 32 columns -> dgate, dup (and the gated product again, from 8 bits)
 template <int ACT, bool BF, int SAVE>
-__device__ __forceinline__ void dglu_tile(const f32x16& dh, const FfnGemm& p, long long m, int f, int h) {
-  const long long at = m * p.lds + f, ate = m * p.lde + f / kGroup;
+__device__ __forceinline__ void dglu_tile(const f32x16& dh, const Saved<BF, SAVE>& s0, const Saved<BF, SAVE>& s1,
+                                          const FfnGemm& p, long long m, int f, int lane) {
+  const int h = lane >> 5;
   float a[16], b[16];
-  if constexpr (SAVE == SAVE_FULL) {
-    if constexpr (BF) {
-      load_group16((const int16_t*)p.s0 + at, p.e0[ate], a, h);
-      load_group16((const int16_t*)p.s1 + at, p.e1[ate], b, h);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 x = *reinterpret_cast<const float4*>((const float*)p.s0 + at + 8 * j + 4 * h);
-        const float4 y = *reinterpret_cast<const float4*>((const float*)p.s1 + at + 8 * j + 4 * h);
-        a[4 * j] = x.x, a[4 * j + 1] = x.y, a[4 * j + 2] = x.z, a[4 * j + 3] = x.w;
-        b[4 * j] = y.x, b[4 * j + 1] = y.y, b[4 * j + 2] = y.z, b[4 * j + 3] = y.w;
-      }
-    }
-  } else {
+  s0.unpack(a);
+  s1.unpack(b);
+  if constexpr (SAVE == SAVE_INT8) {
     float hh[16];
-    load_group8((const int8_t*)p.s0 + at, p.e0[ate], a, h);
-    load_group8((const int8_t*)p.s1 + at, p.e1[ate], b, h);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x, dx;
@@ -356,7 +369,7 @@ __device__ __forceinline__ void dglu_tile(const f32x16& dh, const FfnGemm& p, lo
 
 enum FfnEpi { FFN_STORE = 0, FFN_GLU = 1, FFN_DGLU = 2 };
 
-template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int OCC>
+template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
 __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   constexpr int TM = 64 * MT, TN = 64 * NT, ES = BF ? 2 : 4, BK = 128 / ES;
   constexpr int FN = EPI == FFN_GLU ? TN / 2 : TN;   // columns of C per tile
@@ -396,18 +409,34 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   const long long astep = (AROWS ? (long long)BK : BK * p.lda) * ES, bstep = (BROWS ? (long long)BK : BK * p.ldb) * ES;
 
   // K in up to two segments of p.kseg (a multiple of BK) columns of A, of
-  // which p.K are real; the second starts p.kseg later in A and p.K later in B
+  // which p.K are real; the second starts p.kseg later in A and p.K later in
+  // B.  Steps past the last fill their stage with zeros that nobody reads.
   const int nseg = (p.K + BK - 1) / BK, nk = nseg * p.segs;
-  auto fill = [&](int kt, int st) {
-    const int seg = kt >= nseg ? 1 : 0, k0 = kt - seg * nseg;
-    const char* a = abase + k0 * astep + seg * (AROWS ? (long long)p.kseg : p.kseg * p.lda) * ES;
-    const char* b = bbase + k0 * bstep + seg * (BROWS ? (long long)p.K : p.K * p.ldb) * ES;
-    const int left = p.K - k0 * BK;
-    la.load(a, left, lds + st * STAGE, wave);
-    if constexpr (EPI == FFN_GLU)
-      lb.template load<16 * NT>(b, left, lds + st * STAGE + OpA::BYTES, wave, b + p.N * p.ldb * ES);
-    else
-      lb.load(b, left, lds + st * STAGE + OpA::BYTES, wave);
+  const char* fa_at = abase;
+  const char* fb_at = bbase;
+  int fill_left = p.K, fill_kt = 0;
+  auto advance = [&] {
+    ++fill_kt;
+    fa_at += astep;
+    fb_at += bstep;
+    fill_left -= BK;
+    if (fill_kt == nseg && p.segs == 2) {
+      fa_at = abase + (AROWS ? (long long)p.kseg : p.kseg * p.lda) * ES;
+      fb_at = bbase + (BROWS ? (long long)p.K : p.K * p.ldb) * ES;
+      fill_left = p.K;
+    }
+  };
+  constexpr int LOADS = OpA::LOADS + OpB::LOADS;
+  auto fill = [&](int from, int to, lds_char* stage) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      if (j < from || j >= to) continue;
+      if (j < OpA::LOADS) la.load(j, fa_at, fill_left, stage, wave);
+      else if constexpr (EPI == FFN_GLU)
+        lb.template load<16 * NT>(j - OpA::LOADS, fb_at, fill_left, stage + OpA::BYTES, wave, fb_at + p.N * p.ldb * ES);
+      else
+        lb.load(j - OpA::LOADS, fb_at, fill_left, stage + OpA::BYTES, wave);
+    }
   };
 
   Reader<BF, AROWS, TM, MT> ra;
@@ -423,87 +452,140 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
+  // FFN_DGLU: the saved tiles, asked for AHEAD tiles before they are used (the
+  // first before the products).  Tiles past the edges repeat the last one, and
+  // their values are not used.
+  constexpr int AHEAD = 2;
+  Saved<BF, SAVE> saved[EPI == FFN_DGLU ? AHEAD + 1 : 1][2];
+  auto prefetch = [&](int t) {
+    const int i = t / NT, j = t % NT;
+    const long long tile = min((m0 + wm) / 32 + i, (p.M - 1) / 32) * p.lds + min((n0 + wn) / 32 + j, (int)p.lds - 1);
+    saved[t % (AHEAD + 1)][0].load(p.s0, p.e0, tile, lane);
+    saved[t % (AHEAD + 1)][1].load(p.s1, p.e1, tile, lane);
+  };
+  if constexpr (EPI == FFN_DGLU) {
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t) prefetch(t);
+  }
+
   u32x4 fa[2][MT], fb[2][NT];
   if (nk > 0) {
-    fill(0, 0);
+    fill(0, LOADS, lds);
+    advance();
     __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if (nk > 1) fill(1, 1);
-    ra.read(lds, 0, fa[0]);
-    rb.read(lds + OpA::BYTES, 0, fb[0]);
+    fill(0, LOADS, lds + STAGE);
+    advance();
+#pragma unroll
+    for (int j = 0; j < NT; ++j) rb.read(lds + OpA::BYTES, 0, j, fb[0][j]);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ra.read(lds, 0, i, fa[0][i]);
   }
   for (int kt = 0; kt < nk; ++kt) {
-    const lds_char* sa = lds + (kt & 1) * STAGE;
+    lds_char* const now = lds + (kt & 1) * STAGE;
+    const lds_char* const next = lds + (~kt & 1) * STAGE;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      if (kk < 3) {
-        ra.read(sa, kk + 1, fa[(kk + 1) & 1]);
-        rb.read(sa + OpA::BYTES, kk + 1, fb[(kk + 1) & 1]);
-      } else {
+      const lds_char* const from = kk < 3 ? now : next;
+      if (kk == 3) {
         // this stage's fragments are in registers; the next stage is whole
         // once this wave's loads and everyone's have landed
-        __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (kt + 1 < nk) {
-          const lds_char* sn = lds + ((kt + 1) & 1) * STAGE;
-          ra.read(sn, 0, fa[0]);
-          rb.read(sn + OpA::BYTES, 0, fb[0]);
-          if (kt + 2 < nk) fill(kt + 2, kt & 1);
+      }
+      // among the products: the next fragments, then this stage's refill.
+      // The order is kept as written: one wave a SIMD has nothing else to
+      // cover them with
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[i][j] = mfma32<BF>(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
+          if (i == 0) rb.read(from + OpA::BYTES, (kk + 1) & 3, j, fb[(kk + 1) & 1][j]);
+          if (i == 1) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+              if (t * NT / MT == j) ra.read(from, (kk + 1) & 3, t, fa[(kk + 1) & 1][t]);
+          }
+          const int at = i * NT + j;
+          if (kk == 3) fill(at * LOADS / (MT * NT), (at + 1) * LOADS / (MT * NT), now);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma32<BF>(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
+      if (kk == 3) advance();
     }
   }
+  // no load into LDS outlives the workgroup
+  __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
 
-  const int h = lane >> 5;
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const long long m = m0 + wm + i * 32 + (lane & 31);
-    if (m >= p.M) continue;
-    if constexpr (EPI == FFN_STORE) {
-      // rows of the second half (p.mseg and on) close the gap of the first's padding
-      long long row = m;
-      if (p.mseg) {
-        const int half = m >= p.mseg ? 1 : 0;
-        const long long in2 = m - (half ? p.mseg : 0);
-        if (in2 >= p.mreal) continue;
-        row = half * (long long)p.mreal + in2;
-      }
+    if (m < p.M) {
+      if constexpr (EPI == FFN_STORE) {
+        // rows of the second half (p.mseg and on) close the gap of the first's padding
+        long long row = m;
+        bool real = true;
+        if (p.mseg) {
+          const int half = m >= p.mseg ? 1 : 0;
+          const long long in2 = m - (half ? p.mseg : 0);
+          real = in2 < p.mreal;
+          row = half * (long long)p.mreal + in2;
+        }
+        if (real) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int n = n0 + wn + j * 32;
-        if (n >= p.N) continue;
-        float v[16];
+          for (int j = 0; j < NT; ++j) {
+            const int n = n0 + wn + j * 32;
+            if (n < p.N) {
+              float v[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
-        store_row<BF>((El<BF>*)p.C + row * p.ldc + n, v, h, p.N - n, p.cvec);
-      }
-    } else if constexpr (EPI == FFN_GLU) {
+              for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
+              store_row<BF>((El<BF>*)p.C + row * p.ldc + n, v, lane >> 5, p.N - n, p.cvec);
+            }
+          }
+        }
+      } else if constexpr (EPI == FFN_GLU) {
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j) {
-        const int f = n0 + (wave & 1) * 16 * NT + j * 32;
-        if (f >= p.N) continue;
-        if (p.act == ACT_SILU) glu_tile<ACT_SILU, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, h);
-        else if (p.act == ACT_GELU) glu_tile<ACT_GELU, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, h);
-        else glu_tile<ACT_SIGMOID, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, h);
-      }
-    } else {
+        for (int j = 0; j < NT / 2; ++j) {
+          const int f = n0 + (wave & 1) * 16 * NT + j * 32;
+          if (f < p.N) glu_tile<ACT, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, lane);
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int f = n0 + wn + j * 32;
-        if (f >= p.N) continue;
-        if (SAVE == SAVE_FULL || p.act == ACT_SILU) dglu_tile<ACT_SILU, BF, SAVE>(acc[i][j], p, m, f, h);
-        else if (p.act == ACT_GELU) dglu_tile<ACT_GELU, BF, SAVE>(acc[i][j], p, m, f, h);
-        else dglu_tile<ACT_SIGMOID, BF, SAVE>(acc[i][j], p, m, f, h);
+        for (int j = 0; j < NT; ++j) {
+          const int f = n0 + wn + j * 32;
+          const int t = i * NT + j;
+          if (t + AHEAD < MT * NT) prefetch(t + AHEAD);
+          const Saved<BF, SAVE>(&s)[2] = saved[t % (AHEAD + 1)];
+          if (f < p.N) dglu_tile<ACT, BF, SAVE>(acc[i][j], s[0], s[1], p, m, f, lane);
+        }
       }
     }
   }
+}
+
+template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
+hipError_t ffn_launch(const FfnGemm& p, hipStream_t s) {
+  constexpr int FN = EPI == FFN_GLU ? 32 * NT : 64 * NT;
+  const long long tiles = ((p.M + 64LL * MT - 1) / (64 * MT)) * ((p.N + FN - 1LL) / FN);
+  if (tiles > 0x7ffffff0LL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((ffn_gemm_kernel<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT, OCC>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                     dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+// 256 x 256 tiles, one workgroup per CU, where their rounds cost less than
+// those of 128 x 128 tiles at two per CU
+template <bool AROWS, bool BROWS, int EPI, int SAVE, int ACT>
+hipError_t ffn_pick(const FfnGemm& p, int bf16, hipStream_t s) {
+  if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  if (!bf16) return ffn_launch<false, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, s);
+  const long long cols = EPI == FFN_GLU ? 2LL * p.N : p.N;
+  const long long t256 = ((p.M + 255LL) / 256) * ((cols + 255) / 256), t128 = ((p.M + 127LL) / 128) * ((cols + 127) / 128);
+  if (8 * ((t256 + 255) / 256) <= 5 * ((t128 + 511) / 512)) return ffn_launch<true, AROWS, BROWS, 4, 4, EPI, SAVE, ACT, 1>(p, s);
+  return ffn_launch<true, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, s);
 }
 
 }  // namespace rnnk

@@ -123,11 +123,12 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
   o = 0;
   if (save != RNN_SAVE_NONE) {
     const size_t vs = save == RNN_SAVE_INT8 ? 1 : wtype == RNN_W_BF16 ? 2 : 4;
-    p.s0 = take(m * p.Fp * vs);
-    p.s1 = take(m * p.Fp * vs);
+    const size_t tiles = (m + 31) / 32 * (p.Fp / 32);
+    p.s0 = take(tiles * 1024 * vs);
+    p.s1 = take(tiles * 1024 * vs);
     if (vs < 4) {
-      p.e0 = take(m * (p.Fp / kGroup));
-      p.e1 = take(m * (p.Fp / kGroup));
+      p.e0 = take(tiles * 32);
+      p.e1 = take(tiles * 32);
     }
     if (save == RNN_SAVE_FULL) p.rh = take(m * p.Fp * es);
     else p.rx = take(ckpt_bytes(m, D));
@@ -158,8 +159,7 @@ void ffn_saved(FfnGemm& g, const FfnPlan& p, void* reserve) {
   g.s1 = at<void>(reserve, p.s1);
   g.e0 = at<int8_t>(reserve, p.e0);
   g.e1 = at<int8_t>(reserve, p.e1);
-  g.lds = p.Fp;
-  g.lde = p.Fp / kGroup;
+  g.lds = p.Fp / 32;
 }
 
 }  // namespace

@@ -61,14 +61,14 @@ struct FfnGemm {
   // rows [0, 2 * mreal) of C
   int mseg, mreal;
   int act;
-  // saved for backward, rows of lds values and lde exponents: act(g) and
-  // u act'(g) (RNN_SAVE_FULL; 16 bits with exponents, or fp32), or g and u
-  // (RNN_SAVE_INT8)
+  // saved for backward in tiles of 32 x 32 with their exponents, lds tiles a
+  // row of tiles: act(g) and u act'(g) (RNN_SAVE_FULL; 16 bits, or fp32
+  // without exponents), or g and u (RNN_SAVE_INT8)
   void* s0;
   void* s1;
   int8_t* e0;
   int8_t* e1;
-  long long lds, lde;
+  long long lds;
   void* h;               // FFN_DGLU with RNN_SAVE_INT8: the gated product, again
   long long ldh;
 };

@@ -35,25 +35,28 @@ __device__ __forceinline__ void sigmoid_pair(float p, float& pos, float& neg) {
   neg = p >= 0.f ? small : big;
 }
 
-// act(g) and its derivative.
+// act(g) and its derivative.  silu(g) = g s(g) and, with 2z = 2 sqrt(2/pi)
+// (g + 0.044715 g^3), gelu(g) = g (1 + tanh z) / 2 = g s(2z): one exponential
+// and one reciprocal each.  (g s(w))' = s + g s (1 - s) w'.
 template <int ACT>
 __device__ __forceinline__ void act_pair(float g, float& a, float& da) {
-  if constexpr (ACT == ACT_GELU) {
-    constexpr float c = 0.7978845608028654f;   // sqrt(2 / pi)
-    const float g2 = g * g;
-    const float t = tanhf_(c * (g + 0.044715f * g2 * g));
-    a = 0.5f * g * (1.f + t);
-    da = 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * c * (1.f + 0.134145f * g2);
+  if constexpr (ACT == ACT_SIGMOID) {
+    float n;
+    sigmoid_pair(g, a, n);
+    da = a * n;
   } else {
-    float s, n;
-    sigmoid_pair(g, s, n);
-    if constexpr (ACT == ACT_SIGMOID) {
-      a = s;
-      da = s * n;
-    } else {
-      a = g * s;
-      da = s + g * s * n;
+    constexpr float c = 1.5957691216057308f, c3 = c * 0.044715f, l = -1.4426950408889634f;   // c = 2 sqrt(2 / pi)
+    float x = l * g, slope = 1.f;
+    if constexpr (ACT == ACT_GELU) {
+      const float g2 = g * g;
+      x = fmaf(l * c3, g2, l * c) * g;
+      slope = fmaf(3.f * c3, g2, c);
     }
+    // x > 128: the exponential is infinite and s is 0, as it should be
+    const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x));
+    a = g * s;
+    const float n = 1.f - s;
+    da = fmaf(ACT == ACT_GELU ? a * slope : a, n, s);
   }
 }
 
