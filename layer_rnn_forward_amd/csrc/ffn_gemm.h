@@ -43,6 +43,8 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) char lds_char;
 
+constexpr int kStep = 128;     // bytes of k in a stage
+constexpr int kStagesA = 3, kStagesB = 2;
 constexpr unsigned kOutside = 0x80000000u;   // byte offset past any operand tile: reads zeros
 
 // s_waitcnt immediate (gfx9 encoding), export count not waited on.
@@ -51,10 +53,10 @@ constexpr int wait_imm(int vm, int lgkm) { return (((vm >> 4) & 3) << 14) | ((lg
 template <bool BF, bool ROWS, int R>   // R: tile rows (m or n) of the operand
 struct Operand {
   static constexpr int ES = BF ? 2 : 4;
-  static constexpr int BK = 128 / ES;
-  static constexpr int BYTES = R * 128;              // one stage
-  static constexpr int LOADS = BYTES / 4096;         // 1 KB loads per wave and stage
-  static constexpr int PITCH = ROWS ? 128 : R * ES;  // bytes of an LDS row
+  static constexpr int BK = kStep / ES;
+  static constexpr int BYTES = R * kStep;              // one stage
+  static constexpr int LOADS = BYTES / 4096;           // 1 KB loads per wave and stage
+  static constexpr int PITCH = ROWS ? kStep : R * ES;  // bytes of an LDS row
 
   unsigned voff[LOADS];   // byte offset of each load's piece in the tile (kOutside: no such row)
   int klane[ROWS ? 1 : LOADS];   // k (in elements) of each load's piece within a step
@@ -71,9 +73,9 @@ struct Operand {
     for (int j = 0; j < LOADS; ++j) {
       const int pos = (4 * j + wave) * 1024 + lane * 16;
       if constexpr (ROWS) {
-        const int r = pos / 128, c = (lane & 7) ^ (r & 7);
+        const int r = pos / kStep, c = (lane & 7) ^ (r >> 1 & 7);
         const int gr = row(r);
-        klane[0] = c * (16 / ES);      // r & 7 = lane / 8 for every load
+        klane[0] = c * (16 / ES);      // r >> 1 & 7 is the same for every load
         voff[j] = gr < 0 ? kOutside : (unsigned)(gr * ld * ES) + (unsigned)(c * 16);
       } else {
         const int k = pos / PITCH, c = (pos % PITCH) / 16 ^ swz(k);
@@ -117,7 +119,7 @@ struct Reader {
     const int q = lane >> 5, i = lane & 31;
     if constexpr (ROWS) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) off[kk] = (first + i) * 128 + (((kk * 2 + q) ^ (i & 7)) * 16);
+      for (int kk = 0; kk < 4; ++kk) off[kk] = (first + i) * kStep + (((kk * 2 + q) ^ (i >> 1 & 7)) * 16);
     } else if constexpr (BF) {
       // 16 lanes read 4 k x 16 r: lane j of them k = j / 4, r = 4 (j % 4)..+3, and receive r = j, 4 k
       const int j = lane & 15, k = q * 8 + (j >> 2);
@@ -133,7 +135,7 @@ struct Reader {
   }
   __device__ __forceinline__ void read(const lds_char* stage, int kk, int t, u32x4& f) const {
     if constexpr (ROWS) {
-      f = *(const __attribute__((address_space(3))) u32x4*)(stage + off[kk] + t * 32 * 128);
+      f = *(const __attribute__((address_space(3))) u32x4*)(stage + off[kk] + t * 32 * kStep);
     } else if constexpr (BF) {
       const lds_char* p = stage + off[t] + kk * 16 * Op::PITCH;
       const u32x2 a = read_tr(p), b = read_tr(p + 4 * Op::PITCH);
@@ -371,13 +373,13 @@ enum FfnEpi { FFN_STORE = 0, FFN_GLU = 1, FFN_DGLU = 2 };
 
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
 __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
-  constexpr int TM = 64 * MT, TN = 64 * NT, ES = BF ? 2 : 4, BK = 128 / ES;
+  constexpr int TM = 64 * MT, TN = 64 * NT, ES = BF ? 2 : 4, BK = kStep / ES;
   constexpr int FN = EPI == FFN_GLU ? TN / 2 : TN;   // columns of C per tile
   using OpA = Operand<BF, AROWS, TM>;
   using OpB = Operand<BF, BROWS, TN>;
-  constexpr int STAGE = OpA::BYTES + OpB::BYTES;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
-  lds_char* const lds = (lds_char*)smem;
+  __shared__ __attribute__((aligned(1024))) char smem[kStagesA * OpA::BYTES + kStagesB * OpB::BYTES];
+  lds_char* const lds_a = (lds_char*)smem;
+  lds_char* const lds_b = lds_a + kStagesA * OpA::BYTES;
 
   // tiles: contiguous runs per XCD; inside, groups of 8 tile rows, column by
   // column, so that the tiles in flight on one XCD share few row blocks
@@ -412,31 +414,33 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   // which p.K are real; the second starts p.kseg later in A and p.K later in
   // B.  Steps past the last fill their stage with zeros that nobody reads.
   const int nseg = (p.K + BK - 1) / BK, nk = nseg * p.segs;
-  const char* fa_at = abase;
-  const char* fb_at = bbase;
-  int fill_left = p.K, fill_kt = 0;
-  auto advance = [&] {
-    ++fill_kt;
-    fa_at += astep;
-    fb_at += bstep;
-    fill_left -= BK;
-    if (fill_kt == nseg && p.segs == 2) {
-      fa_at = abase + (AROWS ? (long long)p.kseg : p.kseg * p.lda) * ES;
-      fb_at = bbase + (BROWS ? (long long)p.K : p.K * p.ldb) * ES;
-      fill_left = p.K;
+  struct Fill {
+    const char* at;
+    int left, kt;
+  } qa{abase, p.K, 0}, qb{bbase, p.K, 0};
+  auto advance = [&](Fill& q, const char* second, long long step) {
+    q.at += step;
+    q.left -= BK;
+    if (++q.kt == nseg && p.segs == 2) {
+      q.at = second;
+      q.left = p.K;
     }
   };
-  constexpr int LOADS = OpA::LOADS + OpB::LOADS;
-  auto fill = [&](int from, int to, lds_char* stage) {
+  auto next_a = [&] { advance(qa, abase + (AROWS ? (long long)p.kseg : p.kseg * p.lda) * ES, astep); };
+  auto next_b = [&] { advance(qb, bbase + (BROWS ? (long long)p.K : p.K * p.ldb) * ES, bstep); };
+  constexpr int LA = OpA::LOADS, LB = OpB::LOADS;
+  auto fill_a = [&](int from, int to, lds_char* stage) {
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      if (j < from || j >= to) continue;
-      if (j < OpA::LOADS) la.load(j, fa_at, fill_left, stage, wave);
-      else if constexpr (EPI == FFN_GLU)
-        lb.template load<16 * NT>(j - OpA::LOADS, fb_at, fill_left, stage + OpA::BYTES, wave, fb_at + p.N * p.ldb * ES);
-      else
-        lb.load(j - OpA::LOADS, fb_at, fill_left, stage + OpA::BYTES, wave);
-    }
+    for (int j = 0; j < LA; ++j)
+      if (j >= from && j < to) la.load(j, qa.at, qa.left, stage, wave);
+  };
+  auto fill_b = [&](int from, int to, lds_char* stage) {
+#pragma unroll
+    for (int j = 0; j < LB; ++j)
+      if (j >= from && j < to) {
+        if constexpr (EPI == FFN_GLU) lb.template load<16 * NT>(j, qb.at, qb.left, stage, wave, qb.at + p.N * p.ldb * ES);
+        else lb.load(j, qb.at, qb.left, stage, wave);
+      }
   };
 
   Reader<BF, AROWS, TM, MT> ra;
@@ -469,53 +473,78 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   }
 
   u32x4 fa[2][MT], fb[2][NT];
+  lds_char *a0 = lds_a, *a1 = a0 + OpA::BYTES, *a2 = a1 + OpA::BYTES;   // of steps kt, kt + 1, kt + 2
+  lds_char *b0 = lds_b, *b1 = b0 + OpB::BYTES;
   if (nk > 0) {
-    fill(0, LOADS, lds);
-    advance();
-    __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+    fill_b(0, LB, b0);
+    next_b();
+    fill_a(0, LA, a0);
+    next_a();
+    fill_a(0, LA, a1);
+    next_a();
+    fill_b(0, LB * 3 / 4, b1);
+    __builtin_amdgcn_s_waitcnt(wait_imm(LA + LB * 3 / 4, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    fill(0, LOADS, lds + STAGE);
-    advance();
 #pragma unroll
-    for (int j = 0; j < NT; ++j) rb.read(lds + OpA::BYTES, 0, j, fb[0][j]);
+    for (int j = 0; j < NT; ++j) rb.read(b0, 0, j, fb[0][j]);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) ra.read(lds, 0, i, fa[0][i]);
+    for (int i = 0; i < MT; ++i) ra.read(a0, 0, i, fa[0][i]);
   }
   for (int kt = 0; kt < nk; ++kt) {
-    lds_char* const now = lds + (kt & 1) * STAGE;
-    const lds_char* const next = lds + (~kt & 1) * STAGE;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      const lds_char* const from = kk < 3 ? now : next;
       if (kk == 3) {
-        // this stage's fragments are in registers; the next stage is whole
-        // once this wave's loads and everyone's have landed
-        __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+        // this step's fragments are in registers; the next step's stages are
+        // whole once this wave's loads and everyone's have landed, all but
+        // those of the step after it
+        __builtin_amdgcn_s_waitcnt(wait_imm(LA, 0));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
       }
-      // among the products: the next fragments, then this stage's refill.
-      // The order is kept as written: one wave a SIMD has nothing else to
-      // cover them with
+      // Among the products: the next fragments, then a few loads.  The order is
+      // kept as written: one wave a SIMD has nothing else to cover them with.
+      // The loads are spread over the step because a CU takes 16 cycles for
+      // each, and a wave that has to wait for its turn issues no products.
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           acc[i][j] = mfma32<BF>(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
-          if (i == 0) rb.read(from + OpA::BYTES, (kk + 1) & 3, j, fb[(kk + 1) & 1][j]);
+          if (i == 0) rb.read(kk < 3 ? b0 : b1, (kk + 1) & 3, j, fb[(kk + 1) & 1][j]);
           if (i == 1) {
 #pragma unroll
             for (int t = 0; t < MT; ++t)
-              if (t * NT / MT == j) ra.read(from, (kk + 1) & 3, t, fa[(kk + 1) & 1][t]);
+              if (t * NT / MT == j) ra.read(kk < 3 ? a0 : a1, (kk + 1) & 3, t, fa[(kk + 1) & 1][t]);
           }
+          constexpr int S = MT * NT;
           const int at = i * NT + j;
-          if (kk == 3) fill(at * LOADS / (MT * NT), (at + 1) * LOADS / (MT * NT), now);
+          auto share = [&](int from, int n, int k) { return from + n * k / S; };   // of n loads from `from` on
+          if (kk == 3) {
+            fill_b(share(0, LB * 3 / 4, at), share(0, LB * 3 / 4, at + 1), b0);
+          } else if (kk == 0) {
+            constexpr int X = LB - LB * 3 / 4;
+            const int lo = share(0, X + LA / 4, at), hi = share(0, X + LA / 4, at + 1);
+            fill_b(LB - X + min(lo, X), LB - X + min(hi, X), b1);
+            if (lo < X && hi >= X) next_b();
+            fill_a(max(lo - X, 0), max(hi - X, 0), a2);
+          } else {
+            constexpr int Y = LA * 5 / 8;
+            if (kk == 1) fill_a(share(LA / 4, Y - LA / 4, at), share(LA / 4, Y - LA / 4, at + 1), a2);
+            else fill_a(share(Y, LA - Y, at), share(Y, LA - Y, at + 1), a2);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if (kk == 3) advance();
+      if (kk == 2) next_a();
     }
+    lds_char* const t = a0;
+    a0 = a1;
+    a1 = a2;
+    a2 = t;
+    lds_char* const u = b0;
+    b0 = b1;
+    b1 = u;
   }
   // no load into LDS outlives the workgroup
   __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
