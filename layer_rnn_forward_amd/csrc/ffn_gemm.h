@@ -30,6 +30,7 @@
 // in two lanes.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "lm_math.h"
@@ -371,21 +372,24 @@ __device__ __forceinline__ void dglu_tile(const f32x16& dh, const Saved<BF, SAVE
 
 enum FfnEpi { FFN_STORE = 0, FFN_GLU = 1, FFN_DGLU = 2 };
 
-template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
-__global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
+// LDS of one product
+template <bool BF, int MT, int NT>
+constexpr int ffn_lds() { return (kStagesA * 64 * MT + kStagesB * 64 * NT) * kStep; }
+
+// Tile `block` of a product that has `blocks` (a multiple of 8) workgroups.
+template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT>
+__device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int block, int blocks) {
   constexpr int TM = 64 * MT, TN = 64 * NT, ES = BF ? 2 : 4, BK = kStep / ES;
   constexpr int FN = EPI == FFN_GLU ? TN / 2 : TN;   // columns of C per tile
   using OpA = Operand<BF, AROWS, TM>;
   using OpB = Operand<BF, BROWS, TN>;
-  __shared__ __attribute__((aligned(1024))) char smem[kStagesA * OpA::BYTES + kStagesB * OpB::BYTES];
   lds_char* const lds_a = (lds_char*)smem;
   lds_char* const lds_b = lds_a + kStagesA * OpA::BYTES;
 
   // tiles: contiguous runs per XCD; inside, groups of 8 tile rows, column by
   // column, so that the tiles in flight on one XCD share few row blocks
   const int tm = (p.M + TM - 1) / TM, tn = (p.N + FN - 1) / FN;
-  const int per = (int)gridDim.x / 8;
-  const int lin = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  const int lin = block % 8 * (blocks / 8) + block / 8;
   if (lin >= tm * tn) return;
   constexpr int GM = 8;
   const int grp = lin / (GM * tn), in = lin - grp * GM * tn, gm = min(GM, tm - grp * GM);
@@ -469,7 +473,7 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   };
   if constexpr (EPI == FFN_DGLU) {
 #pragma unroll
-    for (int t = 0; t < AHEAD; ++t) prefetch(t);
+    for (int t = 0; t < AHEAD && t < MT * NT; ++t) prefetch(t);
   }
 
   u32x4 fa[2][MT], fb[2][NT];
@@ -512,7 +516,7 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
         for (int j = 0; j < NT; ++j) {
           acc[i][j] = mfma32<BF>(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
           if (i == 0) rb.read(kk < 3 ? b0 : b1, (kk + 1) & 3, j, fb[(kk + 1) & 1][j]);
-          if (i == 1) {
+          if (i == (MT > 1 ? 1 : 0)) {
 #pragma unroll
             for (int t = 0; t < MT; ++t)
               if (t * NT / MT == j) ra.read(kk < 3 ? a0 : a1, (kk + 1) & 3, t, fa[(kk + 1) & 1][t]);
@@ -596,25 +600,111 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
 }
 
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
-hipError_t ffn_launch(const FfnGemm& p, hipStream_t s) {
-  constexpr int FN = EPI == FFN_GLU ? 32 * NT : 64 * NT;
-  const long long tiles = ((p.M + 64LL * MT - 1) / (64 * MT)) * ((p.N + FN - 1LL) / FN);
+__global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
+  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds<BF, MT, NT>()];
+  ffn_product<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT>(p, smem, (int)blockIdx.x, (int)gridDim.x);
+}
+
+// ---------------------------------------------------------------- launches
+// Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 64 x 64 (four; of
+// the gated product 64 x 128).
+enum FfnTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
+constexpr int kTile[3] = {256, 128, 64};
+
+inline long long ffn_tiles(const FfnGemm& p, int tile, bool glu) {
+  if (p.M <= 0 || p.N <= 0) return 0;
+  const int fn = !glu ? kTile[tile] : tile == TILE_64 ? 64 : kTile[tile] / 2;
+  return ((long long)p.M + kTile[tile] - 1) / kTile[tile] * (((long long)p.N + fn - 1) / fn);
+}
+inline long long ffn_steps(const FfnGemm& p, int bf16) {
+  const int bk = kStep / (bf16 ? 2 : 4);
+  return ((long long)p.K + bk - 1) / bk * p.segs;
+}
+
+// Time of products that run together in tiles of one size, longest first: the
+// tiles are dealt to the places of 256 CUs.  A step's time, measured (units of
+// 10 ns), with the CU to itself and per place when all are taken:
+//   bf16   256: 1.45 us   128: 0.50 us, two a CU 0.86 us   64: 0.40 us, three a CU 0.54 us
+//   fp32                  128: 1.9 us,  two a CU 3.8 us    64: 0.5 us,  three a CU 1.44 us
+inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, int tile) {
+  static constexpr double alone[2][3] = {{0, 190, 50}, {145, 50, 40}}, full[2][3] = {{0, 380, 144}, {145, 86, 54}};
+  static constexpr int places[3] = {256, 512, 768};
+  struct Group {
+    double time;
+    long long count;
+  } g[8] = {{0, places[tile]}};
+  int groups = 1;
+  long long all = 0;
+  for (int i = 0; i < n; ++i) all += ffn_tiles(*p[i], tile, glu);
+  const double step = (all <= 256 ? alone : full)[bf16][tile] * (glu && tile == TILE_64 ? 2 : 1);
+  double last = 0;
+  for (int i = 0; i < n; ++i) {
+    long long tiles = ffn_tiles(*p[i], tile, glu);
+    const double len = ((double)ffn_steps(*p[i], bf16) + 4) * step;   // 4: its start and end
+    while (tiles > 0) {
+      int e = 0;   // the places that are free first
+      for (int k = 1; k < groups; ++k)
+        if (g[k].time < g[e].time) e = k;
+      const long long whole = tiles / places[tile];
+      if (groups == 1 && whole > 1) {   // full rounds
+        g[0].time += (double)whole * len;
+        last = std::max(last, g[0].time);
+        tiles -= whole * places[tile];
+        continue;
+      }
+      const long long m = std::min(tiles, g[e].count);
+      const Group put{g[e].time + len, m};
+      last = std::max(last, put.time);
+      tiles -= m;
+      if (m == g[e].count) g[e] = put;
+      else {
+        g[e].count -= m;
+        int k = 0;
+        while (k < groups && (k == e || g[k].time != put.time)) ++k;
+        if (k < groups) g[k].count += m;
+        else if (groups < 8) g[groups++] = put;
+        else g[e].count += m;
+      }
+    }
+  }
+  return last;
+}
+
+inline int ffn_tile(const FfnGemm* const* p, int n, int bf16, bool glu) {
+  int best = bf16 ? TILE_256 : TILE_128;
+  double least = ffn_time(p, n, bf16, glu, best);
+  for (int t = best + 1; t <= TILE_64; ++t) {
+    const double time = ffn_time(p, n, bf16, glu, t);
+    if (time < least) {
+      least = time;
+      best = t;
+    }
+  }
+  return best;
+}
+
+template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
+hipError_t ffn_launch(const FfnGemm& p, long long tiles, hipStream_t s) {
   if (tiles > 0x7ffffff0LL) return hipErrorInvalidValue;
   hipLaunchKernelGGL((ffn_gemm_kernel<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT, OCC>), dim3((unsigned)((tiles + 7) / 8 * 8)),
                      dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
-// 256 x 256 tiles, one workgroup per CU, where their rounds cost less than
-// those of 128 x 128 tiles at two per CU
 template <bool AROWS, bool BROWS, int EPI, int SAVE, int ACT>
 hipError_t ffn_pick(const FfnGemm& p, int bf16, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  if (!bf16) return ffn_launch<false, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, s);
-  const long long cols = EPI == FFN_GLU ? 2LL * p.N : p.N;
-  const long long t256 = ((p.M + 255LL) / 256) * ((cols + 255) / 256), t128 = ((p.M + 127LL) / 128) * ((cols + 127) / 128);
-  if (8 * ((t256 + 255) / 256) <= 5 * ((t128 + 511) / 512)) return ffn_launch<true, AROWS, BROWS, 4, 4, EPI, SAVE, ACT, 1>(p, s);
-  return ffn_launch<true, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, s);
+  const FfnGemm* one[1] = {&p};
+  const int tile = ffn_tile(one, 1, bf16, EPI == FFN_GLU);
+  const long long tiles = ffn_tiles(p, tile, EPI == FFN_GLU);
+  constexpr int N64 = EPI == FFN_GLU ? 2 : 1;
+  if (!bf16) {
+    if (tile == TILE_128) return ffn_launch<false, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, tiles, s);
+    return ffn_launch<false, AROWS, BROWS, 1, N64, EPI, SAVE, ACT, 3>(p, tiles, s);
+  }
+  if (tile == TILE_256) return ffn_launch<true, AROWS, BROWS, 4, 4, EPI, SAVE, ACT, 1>(p, tiles, s);
+  if (tile == TILE_128) return ffn_launch<true, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, tiles, s);
+  return ffn_launch<true, AROWS, BROWS, 1, N64, EPI, SAVE, ACT, 3>(p, tiles, s);
 }
 
 }  // namespace rnnk

@@ -141,7 +141,7 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
 struct Pads {
   PadJob j{};
   const void* add(const void* src, long long rows, int cols, int ld, void* dst) {
-    if (cols == ld && ((uintptr_t)src & 15) == 0) return src;
+    if (cols == 0 || (cols == ld && ((uintptr_t)src & 15) == 0)) return src;
     const int i = j.n++;
     j.src[i] = src;
     j.dst[i] = dst;
@@ -274,7 +274,7 @@ rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn
   o.B = wo; o.ldb = p.Fo;
   o.C = y; o.ldc = D; o.cvec = store16(y, D, p.es);
   o.segs = 1;
-  return dev(rnn_launch_ffn_store(o, bf, 0, s));
+  return dev(rnn_launch_ffn_store(o, bf, s));
 }
 
 rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn_save_t save, int M, int D, int F,
@@ -296,18 +296,11 @@ rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rn
   const void* wi = rows && dx ? pads.add(w_in, 2LL * F, D, p.Dp, at<void>(ws, p.w_in)) : nullptr;
   const void* wo = rows ? pads.add(w_out, D, F, p.Fo, at<void>(ws, p.w_out)) : nullptr;
   const void* dyp = rows ? pads.add(dy, M, D, p.Dp, at<void>(ws, p.dy)) : nullptr;
-  LM_TRY(dev(rnn_launch_pad(pads.j, bf, s)));
   const void* xp = nullptr;
-  if (rows && dw_in) {
-    if (save == RNN_SAVE_INT8) {
-      LM_TRY(dev(rnn_launch_ckpt_load(bf, M, D, at<const void>(reserve, p.rx), at<void>(ws, p.x), p.Dp, s)));
-      xp = at<void>(ws, p.x);
-    } else {
-      Pads px;
-      xp = px.add(x, M, D, p.Dp, at<void>(ws, p.x));
-      LM_TRY(dev(rnn_launch_pad(px.j, bf, s)));
-    }
-  }
+  if (rows && dw_in) xp = save == RNN_SAVE_INT8 ? at<const void>(ws, p.x) : pads.add(x, M, D, p.Dp, at<void>(ws, p.x));
+  LM_TRY(dev(rnn_launch_pad(pads.j, bf, s)));
+  if (rows && dw_in && save == RNN_SAVE_INT8)
+    LM_TRY(dev(rnn_launch_ckpt_load(bf, M, D, at<const void>(reserve, p.rx), at<void>(ws, p.x), p.Dp, s)));
   void* dgu = at<void>(ws, p.dgu);
   void* res = const_cast<void*>(reserve);   // read only
   const void* h = save == RNN_SAVE_FULL ? at<void>(res, p.rh) : at<void>(ws, p.h);
@@ -321,35 +314,29 @@ rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rn
   ffn_saved(g, p, res);
   g.h = at<void>(ws, p.h); g.ldh = p.Fp;
   LM_TRY(dev(rnn_launch_ffn_dglu(g, bf, save, s)));
+  FfnGemm o{}, win{}, wout{};
+  o.segs = win.segs = wout.segs = 1;
   if (dx) {
-    FfnGemm o{};
     o.M = M; o.N = D; o.K = F;
     o.A = dgu; o.lda = 2LL * p.Fp;
     o.B = wi; o.ldb = p.Dp;
     o.C = dx; o.ldc = D; o.cvec = store16(dx, D, p.es);
     o.segs = 2; o.kseg = p.Fp;
-    LM_TRY(dev(rnn_launch_ffn_store(o, bf, 1, s)));
   }
   if (dw_in && F > 0) {
-    FfnGemm o{};
-    o.M = 2 * p.Fp; o.N = D; o.K = M;
-    o.A = dgu; o.lda = 2LL * p.Fp;
-    o.B = xp; o.ldb = p.Dp;
-    o.C = dw_in; o.ldc = D; o.cvec = store16(dw_in, D, p.es);
-    o.segs = 1;
-    o.mseg = p.Fp; o.mreal = F;
-    LM_TRY(dev(rnn_launch_ffn_store(o, bf, 2, s)));
+    win.M = 2 * p.Fp; win.N = D; win.K = M;
+    win.A = dgu; win.lda = 2LL * p.Fp;
+    win.B = xp; win.ldb = p.Dp;
+    win.C = dw_in; win.ldc = D; win.cvec = store16(dw_in, D, p.es);
+    win.mseg = p.Fp; win.mreal = F;
   }
   if (dw_out) {
-    FfnGemm o{};
-    o.M = D; o.N = F; o.K = M;
-    o.A = dyp; o.lda = p.Dp;
-    o.B = h; o.ldb = p.Fp;
-    o.C = dw_out; o.ldc = F; o.cvec = store16(dw_out, F, p.es);
-    o.segs = 1;
-    LM_TRY(dev(rnn_launch_ffn_store(o, bf, 2, s)));
+    wout.M = D; wout.N = F; wout.K = M;
+    wout.A = dyp; wout.lda = p.Dp;
+    wout.B = h; wout.ldb = p.Fp;
+    wout.C = dw_out; wout.ldc = F; wout.cvec = store16(dw_out, F, p.es);
   }
-  return RNN_STATUS_SUCCESS;
+  return dev(rnn_launch_ffn_grads(o, win, wout, bf, s));
 }
 
 rnn_status_t rnn_checkpoint_size(int rows, int cols, size_t* bytes) {

@@ -86,14 +86,14 @@ struct FfnRows {
   int act;               // of the gated product
 };
 
-// Copies of up to three matrices with rows padded by zeros to a multiple of
+// Copies of up to four matrices with rows padded by zeros to a multiple of
 // 16 bytes.
 struct PadJob {
   int n;
-  const void* src[3];
-  void* dst[3];
-  long long rows[3];
-  int cols[3], ld[3];    // ld: columns of dst
+  const void* src[4];
+  void* dst[4];
+  long long rows[4];
+  int cols[4], ld[4];    // ld: columns of dst
 };
 
 }  // namespace rnnk
@@ -103,10 +103,12 @@ hipError_t rnn_launch_scan_step(int mode, int bf16, int B, int H, const void* g,
 hipError_t rnn_launch_scan_fwd(const rnnk::ScanParams& p, int mode, int bf16, hipStream_t s);
 hipError_t rnn_launch_scan_bwd(const rnnk::ScanParams& p, int mode, int bf16, hipStream_t s);
 
-// layout: 0 rows x rows, 1 rows x columns, 2 columns x columns (A, B)
 hipError_t rnn_launch_ffn_glu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
 hipError_t rnn_launch_ffn_dglu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
-hipError_t rnn_launch_ffn_store(const rnnk::FfnGemm& p, int bf16, int layout, hipStream_t s);
+hipError_t rnn_launch_ffn_store(const rnnk::FfnGemm& p, int bf16, hipStream_t s);
+// those that are not wanted have M = 0
+hipError_t rnn_launch_ffn_grads(const rnnk::FfnGemm& dx, const rnnk::FfnGemm& dw_in, const rnnk::FfnGemm& dw_out, int bf16,
+                                hipStream_t s);
 hipError_t rnn_launch_ffn_rows(const rnnk::FfnRows& p, int bf16, int glu, hipStream_t s);
 hipError_t rnn_launch_pad(const rnnk::PadJob& j, int bf16, hipStream_t s);
 
