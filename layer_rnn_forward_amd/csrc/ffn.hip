@@ -47,60 +47,96 @@ __global__ __launch_bounds__(256) void pad_kernel(const PadJob j) {
   }
 }
 
-// The three products of the backward pass that are left once dgate and dup are
-// there, in one launch: their tiles fill the CUs together, where each alone
-// leaves part of its last round empty.
-struct Grads {
-  FfnGemm dx, dw_in, dw_out;
+// Up to three products in one launch.  Backward's three, once dgate and dup
+// are there, fill the CUs together, where each alone leaves part of its last
+// round empty.
+struct Jobs {
+  FfnGemm p[3];
   int begin[3], blocks[3];
 };
+__device__ __forceinline__ int job_of(const Jobs& j, int b) {
+  for (int i = 0; i < 2; ++i)
+    if (b >= j.begin[i] && b < j.begin[i] + j.blocks[i]) return i;
+  return 2;
+}
+
 template <bool BF, int T, int OCC>
-__global__ __launch_bounds__(256, OCC) void grads_kernel(const Grads g) {
+__global__ __launch_bounds__(256, OCC) void store_kernel(const Jobs j) {
   __shared__ __attribute__((aligned(1024))) char smem[ffn_lds<BF, T, T>()];
-  const int b = (int)blockIdx.x;
-  if (b >= g.begin[0] && b < g.begin[0] + g.blocks[0]) {
-    ffn_product<BF, true, false, T, T, FFN_STORE, SAVE_NONE, 0>(g.dx, smem, b - g.begin[0], g.blocks[0]);
-  } else {
-    const bool in = b >= g.begin[1] && b < g.begin[1] + g.blocks[1];
-    const FfnGemm p = in ? g.dw_in : g.dw_out;
-    ffn_product<BF, false, false, T, T, FFN_STORE, SAVE_NONE, 0>(p, smem, b - g.begin[in ? 1 : 2], g.blocks[in ? 1 : 2]);
+  ffn_product<BF, true, true, T, T, FFN_STORE, SAVE_NONE, 0>(j.p[0], smem, (int)blockIdx.x, j.blocks[0]);
+}
+template <bool BF, int T, int OCC>
+__global__ __launch_bounds__(256, OCC) void grads_kernel(const Jobs j) {
+  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds<BF, T, T>()];
+  const int b = (int)blockIdx.x, i = job_of(j, b);
+  const FfnGemm p = j.p[i];
+  if (i == 0) ffn_product<BF, true, false, T, T, FFN_STORE, SAVE_NONE, 0>(p, smem, b - j.begin[0], j.blocks[0]);
+  else ffn_product<BF, false, false, T, T, FFN_STORE, SAVE_NONE, 0>(p, smem, b - j.begin[i], j.blocks[i]);
+}
+template <bool BF, int T>
+__global__ __launch_bounds__(256) void sum_kernel(const Jobs j) {
+  const int b = (int)blockIdx.x, i = job_of(j, b);
+  const FfnGemm p = j.p[i];
+  ffn_sum<BF, T, T>(p, b - j.begin[i]);
+}
+
+template <bool BACK, bool BF, int T, int OCC>
+void start(const Jobs& j, long long blocks, hipStream_t s) {
+  if (BACK) hipLaunchKernelGGL((grads_kernel<BF, T, OCC>), dim3((unsigned)blocks), dim3(256), 0, s, j);
+  else hipLaunchKernelGGL((store_kernel<BF, T, OCC>), dim3((unsigned)blocks), dim3(256), 0, s, j);
+}
+
+template <bool BACK>
+hipError_t run(Jobs& j, const int (&order)[3], int tile, int bf16, hipStream_t s) {
+  Jobs sums = j;
+  long long at = 0, sum_at = 0;
+  for (int i : order) {
+    const long long tiles = ffn_tiles(j.p[i], tile, false), blocks = (tiles * std::max(j.p[i].splits, 1) + 7) / 8 * 8;
+    if (at + blocks > 0x7ffffff0LL) return hipErrorInvalidValue;
+    j.begin[i] = (int)at;
+    j.blocks[i] = (int)blocks;
+    at += blocks;
+    sums.begin[i] = (int)sum_at;
+    sums.blocks[i] = j.p[i].splits > 1 ? (int)tiles : 0;
+    sum_at += sums.blocks[i];
   }
+  if (at == 0) return hipSuccess;
+  if (!bf16) {
+    if (tile == TILE_128) start<BACK, false, 2, 2>(j, at, s);
+    else start<BACK, false, 1, 3>(j, at, s);
+  } else if (tile == TILE_256) {
+    start<BACK, true, 4, 1>(j, at, s);
+  } else if (tile == TILE_128) {
+    start<BACK, true, 2, 2>(j, at, s);
+  } else {
+    start<BACK, true, 1, 3>(j, at, s);
+  }
+  if (sum_at > 0) {
+    const dim3 grid((unsigned)sum_at), block(256);
+    if (!bf16) {
+      if (tile == TILE_128) hipLaunchKernelGGL((sum_kernel<false, 2>), grid, block, 0, s, sums);
+      else hipLaunchKernelGGL((sum_kernel<false, 1>), grid, block, 0, s, sums);
+    } else if (tile == TILE_128) {   // (256 x 256 tiles are not split)
+      hipLaunchKernelGGL((sum_kernel<true, 2>), grid, block, 0, s, sums);
+    } else {
+      hipLaunchKernelGGL((sum_kernel<true, 1>), grid, block, 0, s, sums);
+    }
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t rnn_launch_ffn_store(const FfnGemm& p, int bf16, hipStream_t s) {
-  return ffn_pick<true, true, FFN_STORE, SAVE_NONE, 0>(p, bf16, s);
+hipError_t rnn_launch_ffn_store(const FfnGemm& p, int tile, int bf16, hipStream_t s) {
+  Jobs j{};
+  j.p[0] = p;
+  const int order[3] = {0, 1, 2};
+  return run<false>(j, order, tile, bf16, s);
 }
 
-hipError_t rnn_launch_ffn_grads(const FfnGemm& dx, const FfnGemm& dw_in, const FfnGemm& dw_out, int bf16, hipStream_t s) {
-  const FfnGemm* all[3] = {&dx, &dw_in, &dw_out};
-  Grads g{dx, dw_in, dw_out, {}, {}};
-  int order[3] = {0, 1, 2};   // the longest tiles first
-  if (ffn_steps(dx, bf16) < ffn_steps(dw_in, bf16)) order[0] = 1, order[1] = 2, order[2] = 0;
-  const FfnGemm* sorted[3] = {all[order[0]], all[order[1]], all[order[2]]};
-  const int tile = ffn_tile(sorted, 3, bf16, false);
-  long long at = 0;
-  for (int i : order) {
-    const long long blocks = (ffn_tiles(*all[i], tile, false) + 7) / 8 * 8;
-    if (at + blocks > 0x7ffffff0LL) return hipErrorInvalidValue;
-    g.begin[i] = (int)at;
-    g.blocks[i] = (int)blocks;
-    at += blocks;
-  }
-  if (at == 0) return hipSuccess;
-  const dim3 grid((unsigned)at), block(256);
-  if (!bf16) {
-    if (tile == TILE_128) hipLaunchKernelGGL((grads_kernel<false, 2, 2>), grid, block, 0, s, g);
-    else hipLaunchKernelGGL((grads_kernel<false, 1, 3>), grid, block, 0, s, g);
-  } else if (tile == TILE_256) {
-    hipLaunchKernelGGL((grads_kernel<true, 4, 1>), grid, block, 0, s, g);
-  } else if (tile == TILE_128) {
-    hipLaunchKernelGGL((grads_kernel<true, 2, 2>), grid, block, 0, s, g);
-  } else {
-    hipLaunchKernelGGL((grads_kernel<true, 1, 3>), grid, block, 0, s, g);
-  }
-  return hipGetLastError();
+hipError_t rnn_launch_ffn_grads(const FfnGemm (&p)[3], const int (&order)[3], int tile, int bf16, hipStream_t s) {
+  Jobs j{{p[0], p[1], p[2]}, {}, {}};
+  return run<true>(j, order, tile, bf16, s);
 }
 
 hipError_t rnn_launch_pad(const PadJob& j, int bf16, hipStream_t s) {

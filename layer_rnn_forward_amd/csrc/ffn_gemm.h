@@ -33,6 +33,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "ffn_plan.h"
 #include "lm_math.h"
 
 namespace rnnk {
@@ -44,7 +45,6 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kStep = 128;     // bytes of k in a stage
 constexpr int kStagesA = 3, kStagesB = 2;
 constexpr unsigned kOutside = 0x80000000u;   // byte offset past any operand tile: reads zeros
 
@@ -214,6 +214,36 @@ __device__ __forceinline__ unsigned group_top(const float (&v)[16]) {
 
 constexpr int kBadGroup = -128;   // exponent byte of a group that holds an infinity or a NaN
 
+// A wave's MT x NT tiles to C: rows from m0, columns from n0.
+template <bool BF, int MT, int NT>
+__device__ __forceinline__ void store_tiles(const f32x16 (&acc)[MT][NT], const FfnGemm& p, long long m0, int n0, int lane) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const long long m = m0 + i * 32 + (lane & 31);
+    // rows of the second half (p.mseg and on) close the gap of the first's padding
+    long long row = m;
+    bool real = m < p.M;
+    if (p.mseg) {
+      const int half = m >= p.mseg ? 1 : 0;
+      const long long in = m - (half ? p.mseg : 0);
+      real = real && in < p.mreal;
+      row = half * (long long)p.mreal + in;
+    }
+    if (real) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int n = n0 + j * 32;
+        if (n < p.N) {
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
+          store_row<BF>((El<BF>*)p.C + row * p.ldc + n, v, lane >> 5, p.N - n, p.cvec);
+        }
+      }
+    }
+  }
+}
+
 // What is saved for backward lies tile by tile: 32 rows x 32 columns, each
 // lane's 16 values where its lane number says, so that a wave writes and reads
 // them in runs of 1 KB (rows of C would be 64 byte pieces).  A group of 32
@@ -372,15 +402,25 @@ __device__ __forceinline__ void dglu_tile(const f32x16& dh, const Saved<BF, SAVE
 
 enum FfnEpi { FFN_STORE = 0, FFN_GLU = 1, FFN_DGLU = 2 };
 
+// Tile `lin` of tm x tn: groups of 8 tile rows, column by column.
+__device__ __forceinline__ void tile_at(int lin, int tm, int tn, int& m, int& n) {
+  constexpr int GM = 8;
+  const int grp = lin / (GM * tn), in = lin - grp * GM * tn, gm = min(GM, tm - grp * GM);
+  m = grp * GM + in % gm;
+  n = in / gm;
+}
+
 // LDS of one product
 template <bool BF, int MT, int NT>
 constexpr int ffn_lds() { return (kStagesA * 64 * MT + kStagesB * 64 * NT) * kStep; }
 
-// Tile `block` of a product that has `blocks` (a multiple of 8) workgroups.
+// Piece `block` of a product that has `blocks` (a multiple of 8) workgroups: a
+// tile, or a split of a tile's k, whose sums go to p.part.
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT>
 __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int block, int blocks) {
   constexpr int TM = 64 * MT, TN = 64 * NT, ES = BF ? 2 : 4, BK = kStep / ES;
   constexpr int FN = EPI == FFN_GLU ? TN / 2 : TN;   // columns of C per tile
+  constexpr bool SPLIT = EPI == FFN_STORE && MT < 4;
   using OpA = Operand<BF, AROWS, TM>;
   using OpB = Operand<BF, BROWS, TN>;
   lds_char* const lds_a = (lds_char*)smem;
@@ -389,11 +429,16 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
   // tiles: contiguous runs per XCD; inside, groups of 8 tile rows, column by
   // column, so that the tiles in flight on one XCD share few row blocks
   const int tm = (p.M + TM - 1) / TM, tn = (p.N + FN - 1) / FN;
-  const int lin = block % 8 * (blocks / 8) + block / 8;
+  int lin = block % 8 * (blocks / 8) + block / 8, split = 0;
+  if (SPLIT && p.splits > 1) {
+    split = lin % p.splits;
+    lin /= p.splits;
+  }
   if (lin >= tm * tn) return;
-  constexpr int GM = 8;
-  const int grp = lin / (GM * tn), in = lin - grp * GM * tn, gm = min(GM, tm - grp * GM);
-  const int m0 = (grp * GM + in % gm) * TM, n0 = (in / gm) * FN;
+  int m0, n0;
+  tile_at(lin, tm, tn, m0, n0);
+  m0 *= TM;
+  n0 *= FN;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * 32 * MT, wn = (wave & 1) * 32 * NT;
@@ -417,11 +462,17 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
   // K in up to two segments of p.kseg (a multiple of BK) columns of A, of
   // which p.K are real; the second starts p.kseg later in A and p.K later in
   // B.  Steps past the last fill their stage with zeros that nobody reads.
-  const int nseg = (p.K + BK - 1) / BK, nk = nseg * p.segs;
+  const int nseg = (p.K + BK - 1) / BK;
+  int k0 = 0, nk = nseg * p.segs;
+  if (SPLIT && p.splits > 1) {
+    const int per = (nk + p.splits - 1) / p.splits;
+    k0 = min(split * per, nk);
+    nk = min(per, nk - k0);
+  }
   struct Fill {
     const char* at;
     int left, kt;
-  } qa{abase, p.K, 0}, qb{bbase, p.K, 0};
+  };
   auto advance = [&](Fill& q, const char* second, long long step) {
     q.at += step;
     q.left -= BK;
@@ -430,8 +481,12 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
       q.left = p.K;
     }
   };
-  auto next_a = [&] { advance(qa, abase + (AROWS ? (long long)p.kseg : p.kseg * p.lda) * ES, astep); };
-  auto next_b = [&] { advance(qb, bbase + (BROWS ? (long long)p.K : p.K * p.ldb) * ES, bstep); };
+  const char* const a2nd = abase + (AROWS ? (long long)p.kseg : p.kseg * p.lda) * ES;
+  const char* const b2nd = bbase + (BROWS ? (long long)p.K : p.K * p.ldb) * ES;
+  const int seg = k0 >= nseg ? 1 : 0, kin = k0 - seg * nseg;
+  Fill qa{(seg ? a2nd : abase) + kin * astep, p.K - kin * BK, k0}, qb{(seg ? b2nd : bbase) + kin * bstep, p.K - kin * BK, k0};
+  auto next_a = [&] { advance(qa, a2nd, astep); };
+  auto next_b = [&] { advance(qb, b2nd, bstep); };
   constexpr int LA = OpA::LOADS, LB = OpB::LOADS;
   auto fill_a = [&](int from, int to, lds_char* stage) {
 #pragma unroll
@@ -553,39 +608,33 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
   // no load into LDS outlives the workgroup
   __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
 
+  if constexpr (EPI == FFN_STORE) {
+    if (SPLIT && p.splits > 1) {
+      float4* to = (float4*)p.part + ((long long)split * tm * tn + lin) * (MT * NT * 4 * 256) + tid;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            to[((i * NT + j) * 4 + e) * 256] =
+                make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
+    } else {
+      store_tiles<BF, MT, NT>(acc, p, m0 + wm, n0 + wn, lane);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const long long m = m0 + wm + i * 32 + (lane & 31);
     if (m < p.M) {
-      if constexpr (EPI == FFN_STORE) {
-        // rows of the second half (p.mseg and on) close the gap of the first's padding
-        long long row = m;
-        bool real = true;
-        if (p.mseg) {
-          const int half = m >= p.mseg ? 1 : 0;
-          const long long in2 = m - (half ? p.mseg : 0);
-          real = in2 < p.mreal;
-          row = half * (long long)p.mreal + in2;
-        }
-        if (real) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const int n = n0 + wn + j * 32;
-            if (n < p.N) {
-              float v[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = acc[i][j][e];
-              store_row<BF>((El<BF>*)p.C + row * p.ldc + n, v, lane >> 5, p.N - n, p.cvec);
-            }
-          }
-        }
-      } else if constexpr (EPI == FFN_GLU) {
+      if constexpr (EPI == FFN_GLU) {
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
           const int f = n0 + (wave & 1) * 16 * NT + j * 32;
           if (f < p.N) glu_tile<ACT, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, lane);
         }
-      } else {
+      } else if constexpr (EPI == FFN_DGLU) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int f = n0 + wn + j * 32;
@@ -605,84 +654,36 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   ffn_product<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT>(p, smem, (int)blockIdx.x, (int)gridDim.x);
 }
 
+// Add the splits of a tile in their order and store it.
+template <bool BF, int MT, int NT>
+__device__ __forceinline__ void ffn_sum(const FfnGemm& p, int lin) {
+  const int tm = (p.M + 64 * MT - 1) / (64 * MT), tn = (p.N + 64 * NT - 1) / (64 * NT);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float4* from = (const float4*)p.part + (long long)lin * (MT * NT * 4 * 256) + tid;
+  const long long next = (long long)tm * tn * (MT * NT * 4 * 256);
+  f32x16 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+      for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = from[s * next + ((i * NT + j) * 4 + e) * 256];
+          acc[i][j][4 * e] += v.x;
+          acc[i][j][4 * e + 1] += v.y;
+          acc[i][j][4 * e + 2] += v.z;
+          acc[i][j][4 * e + 3] += v.w;
+        }
+    }
+  int m, n;
+  tile_at(lin, tm, tn, m, n);
+  store_tiles<BF, MT, NT>(acc, p, m * 64 * MT + (wave >> 1) * 32 * MT, n * 64 * NT + (wave & 1) * 32 * NT, lane);
+}
+
 // ---------------------------------------------------------------- launches
-// Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 64 x 64 (four; of
-// the gated product 64 x 128).
-enum FfnTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
-constexpr int kTile[3] = {256, 128, 64};
-
-inline long long ffn_tiles(const FfnGemm& p, int tile, bool glu) {
-  if (p.M <= 0 || p.N <= 0) return 0;
-  const int fn = !glu ? kTile[tile] : tile == TILE_64 ? 64 : kTile[tile] / 2;
-  return ((long long)p.M + kTile[tile] - 1) / kTile[tile] * (((long long)p.N + fn - 1) / fn);
-}
-inline long long ffn_steps(const FfnGemm& p, int bf16) {
-  const int bk = kStep / (bf16 ? 2 : 4);
-  return ((long long)p.K + bk - 1) / bk * p.segs;
-}
-
-// Time of products that run together in tiles of one size, longest first: the
-// tiles are dealt to the places of 256 CUs.  A step's time, measured (units of
-// 10 ns), with the CU to itself and per place when all are taken:
-//   bf16   256: 1.45 us   128: 0.50 us, two a CU 0.86 us   64: 0.40 us, three a CU 0.54 us
-//   fp32                  128: 1.9 us,  two a CU 3.8 us    64: 0.5 us,  three a CU 1.44 us
-inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, int tile) {
-  static constexpr double alone[2][3] = {{0, 190, 50}, {145, 50, 40}}, full[2][3] = {{0, 380, 144}, {145, 86, 54}};
-  static constexpr int places[3] = {256, 512, 768};
-  struct Group {
-    double time;
-    long long count;
-  } g[8] = {{0, places[tile]}};
-  int groups = 1;
-  long long all = 0;
-  for (int i = 0; i < n; ++i) all += ffn_tiles(*p[i], tile, glu);
-  const double step = (all <= 256 ? alone : full)[bf16][tile] * (glu && tile == TILE_64 ? 2 : 1);
-  double last = 0;
-  for (int i = 0; i < n; ++i) {
-    long long tiles = ffn_tiles(*p[i], tile, glu);
-    const double len = ((double)ffn_steps(*p[i], bf16) + 4) * step;   // 4: its start and end
-    while (tiles > 0) {
-      int e = 0;   // the places that are free first
-      for (int k = 1; k < groups; ++k)
-        if (g[k].time < g[e].time) e = k;
-      const long long whole = tiles / places[tile];
-      if (groups == 1 && whole > 1) {   // full rounds
-        g[0].time += (double)whole * len;
-        last = std::max(last, g[0].time);
-        tiles -= whole * places[tile];
-        continue;
-      }
-      const long long m = std::min(tiles, g[e].count);
-      const Group put{g[e].time + len, m};
-      last = std::max(last, put.time);
-      tiles -= m;
-      if (m == g[e].count) g[e] = put;
-      else {
-        g[e].count -= m;
-        int k = 0;
-        while (k < groups && (k == e || g[k].time != put.time)) ++k;
-        if (k < groups) g[k].count += m;
-        else if (groups < 8) g[groups++] = put;
-        else g[e].count += m;
-      }
-    }
-  }
-  return last;
-}
-
-inline int ffn_tile(const FfnGemm* const* p, int n, int bf16, bool glu) {
-  int best = bf16 ? TILE_256 : TILE_128;
-  double least = ffn_time(p, n, bf16, glu, best);
-  for (int t = best + 1; t <= TILE_64; ++t) {
-    const double time = ffn_time(p, n, bf16, glu, t);
-    if (time < least) {
-      least = time;
-      best = t;
-    }
-  }
-  return best;
-}
-
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
 hipError_t ffn_launch(const FfnGemm& p, long long tiles, hipStream_t s) {
   if (tiles > 0x7ffffff0LL) return hipErrorInvalidValue;
@@ -695,7 +696,7 @@ template <bool AROWS, bool BROWS, int EPI, int SAVE, int ACT>
 hipError_t ffn_pick(const FfnGemm& p, int bf16, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
   const FfnGemm* one[1] = {&p};
-  const int tile = ffn_tile(one, 1, bf16, EPI == FFN_GLU);
+  const int tile = ffn_choose(one, 1, bf16, EPI == FFN_GLU, false).tile;
   const long long tiles = ffn_tiles(p, tile, EPI == FFN_GLU);
   constexpr int N64 = EPI == FFN_GLU ? 2 : 1;
   if (!bf16) {

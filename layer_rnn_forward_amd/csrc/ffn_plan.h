@@ -1,0 +1,172 @@
+// Host side of the feed-forward block's products: tile sizes and splits.
+#pragma once
+
+#include <algorithm>
+
+#include "lm_common.h"
+
+namespace rnnk {
+
+constexpr int kStep = 128;     // bytes of k in a step
+
+// Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 64 x 64 (three; of
+// the gated product 64 x 128).
+enum FfnTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
+constexpr int kTile[3] = {256, 128, 64};
+
+inline long long ffn_tiles(const FfnGemm& p, int tile, bool glu) {
+  if (p.M <= 0 || p.N <= 0) return 0;
+  const int fn = !glu ? kTile[tile] : tile == TILE_64 ? 64 : kTile[tile] / 2;
+  return ((long long)p.M + kTile[tile] - 1) / kTile[tile] * (((long long)p.N + fn - 1) / fn);
+}
+inline long long ffn_steps(const FfnGemm& p, int bf16) {
+  const int bk = kStep / (bf16 ? 2 : 4);
+  return ((long long)p.K + bk - 1) / bk * p.segs;
+}
+
+struct FfnChoice {
+  int tile = 0;
+  int splits[3] = {1, 1, 1};
+};
+
+// Time of products that run together, longest first: their pieces are dealt
+// to the places of 256 CUs.  A step's time, measured (units of 10 ns), with the
+// CU to itself and with all of its places taken (in between: linear):
+//   bf16   256: 1.45 us   128: 0.50 us, two a CU 0.86 us   64: 0.31 us, three a CU 0.54 us
+//   fp32                  128: 1.9 us,  two a CU 3.8 us    64: 0.5 us,  three a CU 1.44 us
+// A step of the gated product's 64 x 128 takes 1.3 (alone) or 2 of a 64 x 64's.
+inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const FfnChoice& c) {
+  static constexpr double alone[2][3] = {{0, 190, 50}, {145, 50, 31}}, full[2][3] = {{0, 380, 144}, {145, 86, 54}};
+  static constexpr int most[3] = {1, 2, 3};
+  long long all = 0;
+  double after = 0;
+  for (int i = 0; i < n; ++i) {
+    const long long pieces = ffn_tiles(*p[i], c.tile, glu) * c.splits[i];
+    all += pieces;
+    // a second launch, and the partial sums' way out and back at about 3 TB/s
+    if (c.splits[i] > 1) after = std::max(after, 500.0) + (double)pieces * kTile[c.tile] * kTile[c.tile] * 8 / 3e4;
+  }
+  const int occ = (int)std::max(1LL, std::min<long long>(most[c.tile], (all + 255) / 256)), places = 256 * occ;
+  const double share = occ > 1 ? (occ - 1.0) / (most[c.tile] - 1) : 0;
+  double step = alone[bf16][c.tile] + share * (full[bf16][c.tile] - alone[bf16][c.tile]);
+  if (glu && c.tile == TILE_64) step *= 1.3 + 0.7 * share;
+  struct Group {
+    double time;
+    long long count;
+  } g[8] = {{0, places}};
+  int groups = 1;
+  double last = 0;
+  for (int i = 0; i < n; ++i) {
+    long long pieces = ffn_tiles(*p[i], c.tile, glu) * c.splits[i];
+    const long long steps = (ffn_steps(*p[i], bf16) + c.splits[i] - 1) / c.splits[i];
+    const double len = ((double)steps + 4) * step;   // 4: its start and end
+    while (pieces > 0) {
+      const long long whole = pieces / places;
+      if (groups == 1 && whole > 1) {   // full rounds
+        g[0].time += (double)whole * len;
+        last = std::max(last, g[0].time);
+        pieces -= whole * places;
+        continue;
+      }
+      int e = 0;   // the places that are free first
+      for (int k = 1; k < groups; ++k)
+        if (g[k].time < g[e].time) e = k;
+      const long long m = std::min(pieces, g[e].count);
+      const Group put{g[e].time + len, m};
+      last = std::max(last, put.time);
+      pieces -= m;
+      if (m == g[e].count) {
+        g[e] = put;
+        continue;
+      }
+      g[e].count -= m;
+      int k = 0;
+      while (k < groups && (k == e || g[k].time != put.time)) ++k;
+      if (k < groups) g[k].count += m;
+      else if (groups < 8) g[groups++] = put;
+      else g[e].count += m;
+    }
+  }
+  return last + after;
+}
+
+// The tile that takes least, each with whole k and (the smaller two) with k in
+// pieces of about an equal share of the work for two places a CU (8 steps at
+// least).
+inline FfnChoice ffn_choose(const FfnGemm* const* p, int n, int bf16, bool glu, bool may_split) {
+  FfnChoice best;
+  double least = -1;
+  for (int t = bf16 ? TILE_256 : TILE_128; t <= TILE_64; ++t) {
+    for (int split = 0; split <= (may_split && t != TILE_256 ? 1 : 0); ++split) {
+      FfnChoice c;
+      c.tile = t;
+      if (split) {
+        long long work = 0;
+        for (int i = 0; i < n; ++i) work += ffn_tiles(*p[i], t, glu) * ffn_steps(*p[i], bf16);
+        const long long piece = std::max(8LL, work / 512);
+        bool any = false;
+        for (int i = 0; i < n; ++i) {
+          const long long steps = ffn_steps(*p[i], bf16);
+          if (2 * steps >= 3 * piece) c.splits[i] = (int)std::min(64LL, (steps + piece - 1) / piece);
+          any = any || c.splits[i] > 1;
+        }
+        if (!any) continue;
+      }
+      const double time = ffn_time(p, n, bf16, glu, c);
+      if (least < 0 || time < least) {
+        least = time;
+        best = c;
+      }
+    }
+  }
+  return best;
+}
+
+// Bytes of the partial sums of product i.
+inline size_t ffn_part(const FfnGemm& p, const FfnChoice& c, int i) {
+  if (c.splits[i] <= 1) return 0;
+  return (size_t)ffn_tiles(p, c.tile, false) * c.splits[i] * kTile[c.tile] * kTile[c.tile] * 4;
+}
+
+// The products that may be split, by their sizes alone: forward's second one,
+// and backward's three, longest first (the order that ffn_order gives).
+inline void ffn_forward_product(int M, int D, int F, FfnGemm& o) {
+  o.M = M;
+  o.N = D;
+  o.K = F;
+  o.segs = 1;
+}
+inline void ffn_backward_products(int M, int D, int F, int Fp, FfnGemm (&o)[3]) {
+  o[0].M = M;             // dx: k runs over dgate's columns, then dup's
+  o[0].N = D;
+  o[0].K = F;
+  o[0].segs = 2;
+  o[0].kseg = Fp;
+  o[1].M = F > 0 ? 2 * Fp : 0;   // dw_in: rows of dgate and dup with their padding
+  o[1].N = D;
+  o[1].K = M;
+  o[1].segs = 1;
+  o[1].mseg = Fp;
+  o[1].mreal = F;
+  o[2].M = D;             // dw_out
+  o[2].N = F;
+  o[2].K = M;
+  o[2].segs = 1;
+}
+inline FfnChoice ffn_choose_forward(const FfnGemm& o, int bf16) {
+  const FfnGemm* one[1] = {&o};
+  return ffn_choose(one, 1, bf16, false, true);
+}
+// splits in the products' own order; order: longest first
+inline FfnChoice ffn_choose_backward(const FfnGemm (&o)[3], int bf16, int (&order)[3]) {
+  order[0] = 0, order[1] = 1, order[2] = 2;
+  if (ffn_steps(o[0], bf16) < ffn_steps(o[1], bf16)) order[0] = 1, order[1] = 2, order[2] = 0;
+  const FfnGemm* sorted[3] = {&o[order[0]], &o[order[1]], &o[order[2]]};
+  const FfnChoice c = ffn_choose(sorted, 3, bf16, false, true);
+  FfnChoice r;
+  r.tile = c.tile;
+  for (int i = 0; i < 3; ++i) r.splits[order[i]] = c.splits[i];
+  return r;
+}
+
+}  // namespace rnnk

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 
+#include "ffn_plan.h"
 #include "lm_common.h"
 #include "rnn.h"
 
@@ -93,6 +94,12 @@ struct FfnPlan {
   // workspace: padded copies (used where rows or addresses are not 16-byte
   // aligned), the gated product, its gradients
   size_t x = 0, w_in = 0, w_out = 0, dy = 0, h = 0, dgu = 0, ws = 0;
+  // and the partial sums of split products; the choices do not depend on which
+  // gradients are wanted
+  FfnGemm out{}, grads[3] = {};
+  FfnChoice out_choice, grads_choice;
+  int order[3] = {0, 1, 2};
+  size_t out_part = 0, grads_part[3] = {};
   // reserve
   size_t s0 = 0, s1 = 0, e0 = 0, e1 = 0, rh = 0, rx = 0, reserve = 0;
 };
@@ -119,7 +126,23 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
     p.dy = take(m * p.Dp * es);
     p.dgu = take(m * 2 * p.Fp * es);
   }
-  p.ws = std::max(o, kAlign);
+  const int bf = wtype == RNN_W_BF16;
+  ffn_forward_product(M, D, F, p.out);
+  p.out_choice = ffn_choose_forward(p.out, bf);
+  p.out.splits = p.out_choice.splits[0];
+  const size_t parts = o;
+  p.out_part = take(ffn_part(p.out, p.out_choice, 0));
+  const size_t forward = o;
+  o = parts;              // the passes' partial sums share their place
+  if (save != RNN_SAVE_NONE) {
+    ffn_backward_products(M, D, F, p.Fp, p.grads);
+    p.grads_choice = ffn_choose_backward(p.grads, bf, p.order);
+    for (int i = 0; i < 3; ++i) {
+      p.grads[i].splits = p.grads_choice.splits[i];
+      p.grads_part[i] = take(ffn_part(p.grads[i], p.grads_choice, i));
+    }
+  }
+  p.ws = std::max({o, forward, kAlign});
   o = 0;
   if (save != RNN_SAVE_NONE) {
     const size_t vs = save == RNN_SAVE_INT8 ? 1 : wtype == RNN_W_BF16 ? 2 : 4;
@@ -268,13 +291,12 @@ rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn
   g.act = act;
   if (save != RNN_SAVE_NONE) ffn_saved(g, p, reserve);
   LM_TRY(dev(rnn_launch_ffn_glu(g, bf, save, s)));
-  FfnGemm o{};
-  o.M = M; o.N = D; o.K = F;
+  FfnGemm o = p.out;
   o.A = h; o.lda = p.Fp;
   o.B = wo; o.ldb = p.Fo;
   o.C = y; o.ldc = D; o.cvec = store16(y, D, p.es);
-  o.segs = 1;
-  return dev(rnn_launch_ffn_store(o, bf, s));
+  o.part = at<void>(ws, p.out_part);
+  return dev(rnn_launch_ffn_store(o, p.out_choice.tile, bf, s));
 }
 
 rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn_save_t save, int M, int D, int F,
@@ -314,29 +336,21 @@ rnn_status_t rnn_ffn_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rn
   ffn_saved(g, p, res);
   g.h = at<void>(ws, p.h); g.ldh = p.Fp;
   LM_TRY(dev(rnn_launch_ffn_dglu(g, bf, save, s)));
-  FfnGemm o{}, win{}, wout{};
-  o.segs = win.segs = wout.segs = 1;
-  if (dx) {
-    o.M = M; o.N = D; o.K = F;
-    o.A = dgu; o.lda = 2LL * p.Fp;
-    o.B = wi; o.ldb = p.Dp;
-    o.C = dx; o.ldc = D; o.cvec = store16(dx, D, p.es);
-    o.segs = 2; o.kseg = p.Fp;
-  }
-  if (dw_in && F > 0) {
-    win.M = 2 * p.Fp; win.N = D; win.K = M;
-    win.A = dgu; win.lda = 2LL * p.Fp;
-    win.B = xp; win.ldb = p.Dp;
-    win.C = dw_in; win.ldc = D; win.cvec = store16(dw_in, D, p.es);
-    win.mseg = p.Fp; win.mreal = F;
-  }
-  if (dw_out) {
-    wout.M = D; wout.N = F; wout.K = M;
-    wout.A = dyp; wout.lda = p.Dp;
-    wout.B = h; wout.ldb = p.Fp;
-    wout.C = dw_out; wout.ldc = F; wout.cvec = store16(dw_out, F, p.es);
-  }
-  return dev(rnn_launch_ffn_grads(o, win, wout, bf, s));
+  FfnGemm q[3] = {p.grads[0], p.grads[1], p.grads[2]};
+  for (int i = 0; i < 3; ++i) q[i].part = at<void>(ws, p.grads_part[i]);
+  q[0].A = dgu; q[0].lda = 2LL * p.Fp;
+  q[0].B = wi; q[0].ldb = p.Dp;
+  q[0].C = dx; q[0].ldc = D; q[0].cvec = store16(dx, D, p.es);
+  if (!dx) q[0].M = 0;
+  q[1].A = dgu; q[1].lda = 2LL * p.Fp;
+  q[1].B = xp; q[1].ldb = p.Dp;
+  q[1].C = dw_in; q[1].ldc = D; q[1].cvec = store16(dw_in, D, p.es);
+  if (!dw_in) q[1].M = 0;
+  q[2].A = dyp; q[2].lda = p.Dp;
+  q[2].B = h; q[2].ldb = p.Fp;
+  q[2].C = dw_out; q[2].ldc = F; q[2].cvec = store16(dw_out, F, p.es);
+  if (!dw_out) q[2].M = 0;
+  return dev(rnn_launch_ffn_grads(q, p.order, p.grads_choice.tile, bf, s));
 }
 
 rnn_status_t rnn_checkpoint_size(int rows, int cols, size_t* bytes) {

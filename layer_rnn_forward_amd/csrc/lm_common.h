@@ -60,6 +60,9 @@ struct FfnGemm {
   // mseg > 0: rows [0, mreal) and [mseg, mseg + mreal) of the product are
   // rows [0, 2 * mreal) of C
   int mseg, mreal;
+  // splits > 1: k in that many pieces, whose sums are added in a second launch
+  int splits;
+  void* part;
   int act;
   // saved for backward in tiles of 32 x 32 with their exponents, lds tiles a
   // row of tiles: act(g) and u act'(g) (RNN_SAVE_FULL; 16 bits, or fp32
@@ -105,10 +108,10 @@ hipError_t rnn_launch_scan_bwd(const rnnk::ScanParams& p, int mode, int bf16, hi
 
 hipError_t rnn_launch_ffn_glu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
 hipError_t rnn_launch_ffn_dglu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
-hipError_t rnn_launch_ffn_store(const rnnk::FfnGemm& p, int bf16, hipStream_t s);
-// those that are not wanted have M = 0
-hipError_t rnn_launch_ffn_grads(const rnnk::FfnGemm& dx, const rnnk::FfnGemm& dw_in, const rnnk::FfnGemm& dw_out, int bf16,
-                                hipStream_t s);
+// y, and dx, dw_in, dw_out (those that are not wanted have M = 0); `order`:
+// longest first
+hipError_t rnn_launch_ffn_store(const rnnk::FfnGemm& p, int tile, int bf16, hipStream_t s);
+hipError_t rnn_launch_ffn_grads(const rnnk::FfnGemm (&p)[3], const int (&order)[3], int tile, int bf16, hipStream_t s);
 hipError_t rnn_launch_ffn_rows(const rnnk::FfnRows& p, int bf16, int glu, hipStream_t s);
 hipError_t rnn_launch_pad(const rnnk::PadJob& j, int bf16, hipStream_t s);
 
