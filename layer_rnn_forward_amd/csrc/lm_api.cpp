@@ -121,7 +121,7 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
   p.x = take(m * p.Dp * es);
   p.w_in = take(2 * (size_t)F * p.Dp * es);
   p.w_out = take((size_t)D * p.Fo * es);
-  if (save != RNN_SAVE_FULL) p.h = take(m * p.Fp * es);
+  if (save != RNN_SAVE_FULL) p.h = take((save == RNN_SAVE_NONE && M <= kFfnRows ? 2 : 1) * m * p.Fp * es);   // few rows: and the rests
   if (save != RNN_SAVE_NONE) {
     p.dy = take(m * p.Dp * es);
     p.dgu = take(m * 2 * p.Fp * es);

@@ -79,6 +79,7 @@ struct FfnGemm {
 // One product of the block for few rows (ffn_rows.hip): w [R or 2R, K]
 // contiguous, any alignment.
 constexpr int kFfnRows = 64;   // rows at most
+// bf16: the gated product's rows are followed by the rests of their rounding
 struct FfnRows {
   int M, R, K;
   const void* x;
