@@ -320,15 +320,15 @@ def _addr(t, name, dev, dtype, shape, optional=False):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor" + (" or None" if optional else ""))
+    if t.get_device() == dev >= 0 and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if dev < 0 or t.get_device() != dev:
         raise ValueError(f"{name} must be a device tensor, on the same device as the others")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _room(t, name, dev, optional=False):
@@ -350,7 +350,9 @@ def _elements(t, name, dims):
         raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    _ints(*t.shape)
+    for n in t.shape:
+        if n > 0x7fffffff:
+            raise ValueError(f"{n} does not fit a C int")
     return t.dtype, _WTYPE_OF[t.dtype], t.get_device()
 
 
@@ -364,7 +366,7 @@ def _on(dev):
     """The current stream, which has to be of the tensors' device."""
     if dev < 0:
         raise ValueError("the tensors must be device tensors")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():      # (initialised: it has tensors)
         raise ValueError(f"the tensors' device ({dev}) must be the current one")
     return torch._C._cuda_getCurrentRawStream(dev)
 
@@ -395,9 +397,11 @@ def rnn_scan_step(mode, g, h, y, hy):
     if H2 % 2:
         raise ValueError("g must have an even number of columns")
     bh = (B, H2 // 2)
-    _check(load_library().rnn_scan_step(
+    status = (_LIB or load_library()).rnn_scan_step(
         _on(dev), m, w, B, H2 // 2, _addr(g, "g", dev, dt, g.shape), _addr(h, "h", dev, torch.float32, bh, True),
-        _addr(y, "y", dev, dt, bh, True), _addr(hy, "hy", dev, torch.float32, bh)), "rnn_scan_step")
+        _addr(y, "y", dev, dt, bh, True), _addr(hy, "hy", dev, torch.float32, bh))
+    if status:
+        _check(status, "rnn_scan_step")
 
 
 def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
@@ -414,10 +418,12 @@ def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
     D, H = hy.shape[0], hy.shape[2]
     st = (D, B, H)
     wp, wn = _room(ws, "ws", dev)
-    _check(load_library().rnn_scan_forward(
+    status = (_LIB or load_library()).rnn_scan_forward(
         _on(dev), m, w, T, B, H, D, _addr(g, "g", dev, dt, (T, B, D * 2 * H)),
         _addr(h0, "h0", dev, torch.float32, st, True), _addr(lengths, "lengths", dev, torch.int32, (B,), True),
-        _addr(y, "y", dev, dt, (T, B, D * H)), _addr(hy, "hy", dev, torch.float32, st), wp, wn), "rnn_scan_forward")
+        _addr(y, "y", dev, dt, (T, B, D * H)), _addr(hy, "hy", dev, torch.float32, st), wp, wn)
+    if status:
+        _check(status, "rnn_scan_forward")
 
 
 def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
@@ -432,11 +438,13 @@ def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
     D, H = dh0.shape[0], dh0.shape[2]
     st = (D, B, H)
     wp, wn = _room(ws, "ws", dev)
-    _check(load_library().rnn_scan_backward(
+    status = (_LIB or load_library()).rnn_scan_backward(
         _on(dev), m, w, T, B, H, D, _addr(g, "g", dev, dt, (T, B, D * 2 * H)),
         _addr(h0, "h0", dev, torch.float32, st, True), _addr(lengths, "lengths", dev, torch.int32, (B,), True),
         _addr(dy, "dy", dev, dt, (T, B, D * H)), _addr(dhy, "dhy", dev, torch.float32, st, True),
-        _addr(dg, "dg", dev, dt, (T, B, D * 2 * H)), _addr(dh0, "dh0", dev, torch.float32, st), wp, wn), "rnn_scan_backward")
+        _addr(dg, "dg", dev, dt, (T, B, D * 2 * H)), _addr(dh0, "dh0", dev, torch.float32, st), wp, wn)
+    if status:
+        _check(status, "rnn_scan_backward")
 
 
 def rnn_ffn_workspace_size(M: int, D: int, F: int, wtype: str, save: str = "none") -> int:
@@ -470,9 +478,11 @@ def rnn_ffn_forward(act, x, w_in, w_out, y, ws, save="none", reserve=None):
     F = w_out.shape[1]
     wp, wn = _room(ws, "ws", dev)
     rp, rn = _room(reserve, "reserve", dev, True)
-    _check(load_library().rnn_ffn_forward(
+    status = (_LIB or load_library()).rnn_ffn_forward(
         _on(dev), a, w, sv, M, D, F, _addr(x, "x", dev, dt, (M, D)), _addr(w_in, "w_in", dev, dt, (2 * F, D)),
-        _addr(w_out, "w_out", dev, dt, (D, F)), _addr(y, "y", dev, dt, (M, D)), wp, wn, rp, rn), "rnn_ffn_forward")
+        _addr(w_out, "w_out", dev, dt, (D, F)), _addr(y, "y", dev, dt, (M, D)), wp, wn, rp, rn)
+    if status:
+        _check(status, "rnn_ffn_forward")
 
 
 def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reserve):
@@ -486,11 +496,12 @@ def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reser
     F = w_out.shape[1]
     wp, wn = _room(ws, "ws", dev)
     rp, rn = _room(reserve, "reserve", dev)
-    _check(load_library().rnn_ffn_backward(
+    status = (_LIB or load_library()).rnn_ffn_backward(
         _on(dev), a, w, sv, M, D, F, _addr(x, "x", dev, dt, (M, D), True), _addr(w_in, "w_in", dev, dt, (2 * F, D)),
         _addr(w_out, "w_out", dev, dt, (D, F)), _addr(dy, "dy", dev, dt, (M, D)), _addr(dx, "dx", dev, dt, (M, D), True),
-        _addr(dw_in, "dw_in", dev, dt, (2 * F, D), True), _addr(dw_out, "dw_out", dev, dt, (D, F), True), wp, wn, rp, rn),
-        "rnn_ffn_backward")
+        _addr(dw_in, "dw_in", dev, dt, (2 * F, D), True), _addr(dw_out, "dw_out", dev, dt, (D, F), True), wp, wn, rp, rn)
+    if status:
+        _check(status, "rnn_ffn_backward")
 
 
 def rnn_checkpoint_size(rows: int, cols: int) -> int:
@@ -506,8 +517,10 @@ def rnn_checkpoint_store(x, kept):
     columns of a row, in the buffer ``kept``."""
     dt, w, dev = _elements(x, "x", 2)
     kp, kn = _room(kept, "kept", dev)
-    _check(load_library().rnn_checkpoint_store(_on(dev), w, x.shape[0], x.shape[1], _addr(x, "x", dev, dt, x.shape),
-                                               kp, kn), "rnn_checkpoint_store")
+    status = (_LIB or load_library()).rnn_checkpoint_store(_on(dev), w, x.shape[0], x.shape[1], _addr(x, "x", dev, dt, x.shape),
+                                               kp, kn)
+    if status:
+        _check(status, "rnn_checkpoint_store")
 
 
 def rnn_checkpoint_load(kept, x):
@@ -515,8 +528,10 @@ def rnn_checkpoint_load(kept, x):
     (float32 or bfloat16; both hold its values exactly)."""
     dt, w, dev = _elements(x, "x", 2)
     kp, kn = _room(kept, "kept", dev)
-    _check(load_library().rnn_checkpoint_load(_on(dev), w, x.shape[0], x.shape[1], kp, kn,
-                                              _addr(x, "x", dev, dt, x.shape)), "rnn_checkpoint_load")
+    status = (_LIB or load_library()).rnn_checkpoint_load(_on(dev), w, x.shape[0], x.shape[1], kp, kn,
+                                              _addr(x, "x", dev, dt, x.shape))
+    if status:
+        _check(status, "rnn_checkpoint_load")
 
 
 # ------------------------------------------------------------ weight packing

@@ -48,7 +48,7 @@ __device__ __forceinline__ void act_pair(float g, float& a, float& da) {
     constexpr float c = 1.5957691216057308f, c3 = c * 0.044715f, l = -1.4426950408889634f;   // c = 2 sqrt(2 / pi)
     float x = l * g, slope = 1.f;
     if constexpr (ACT == ACT_GELU) {
-      const float g2 = g * g;
+      const float g2 = fminf(g * g, 1e10f);   // beyond, s is 0 or 1 and the slope must not overflow
       x = fmaf(l * c3, g2, l * c) * g;
       slope = fmaf(3.f * c3, g2, c);
     }
@@ -56,7 +56,7 @@ __device__ __forceinline__ void act_pair(float g, float& a, float& da) {
     const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x));
     a = g * s;
     const float n = 1.f - s;
-    da = fmaf(ACT == ACT_GELU ? a * slope : a, n, s);
+    da = fmaf(ACT == ACT_GELU ? slope * n : n, a, s);
   }
 }
 
