@@ -388,7 +388,10 @@ rnn_status_t rnn_profile_read(rnn_handle_t h, int kernel, long long* launches, d
  * q; y [T, B, dirs * H]; h0, hy [dirs, B, H] fp32.  Direction 1 walks from the
  * last step to the first.  `lengths` (device, int32 [B], or NULL) as in
  * rnn_set_sequence_lengths: past a row's length the state is carried, y is 0,
- * and g is not used (whatever it holds). */
+ * and g is not used (whatever it holds).  Steps are composed in pieces
+ * (h = A h_before + B): with RNN_SCAN_LINEAR and |a| > 1 a state that is not
+ * zero becomes infinite where the product of a over up to 1024 steps in a row
+ * leaves fp32's range, also where the state itself would not. */
 typedef enum RNN_ENUM_BASE { RNN_SCAN_GATED = 0, RNN_SCAN_LINEAR = 1 } rnn_scan_mode_t;
 
 /* Bytes of the workspace of one forward call and the backward calls that
@@ -404,8 +407,8 @@ rnn_status_t rnn_scan_step(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype
 /* All steps.  h0 NULL: zeros; hy NULL: not wanted.  The workspace then holds
  * what rnn_scan_backward reads.  The time axis is split among workgroups that
  * pass the state on; a workgroup whose bounded wait for the state expires
- * sets the workspace's first 32-bit word and carries on with NaN, so that
- * every workgroup ends. */
+ * sets the workspace's first 32-bit word (0 after a pass in which none did)
+ * and carries on with NaN, so that every workgroup ends. */
 rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
                               const void* g, const float* h0, const int* lengths, void* y, float* hy, void* ws,
                               size_t ws_bytes);
@@ -426,12 +429,17 @@ typedef enum RNN_ENUM_BASE { RNN_ACT_SIGMOID = 0, RNN_ACT_SILU = 1, RNN_ACT_GELU
 
 /* What the forward call leaves in the reserve for the backward call:
  *   RNN_SAVE_NONE   nothing (inference)
- *   RNN_SAVE_FULL   the projections and the gated product
+ *   RNN_SAVE_FULL   act(g), u act'(g) (g, u: the projections; with bf16 in 16
+ *                   bits, whole numbers of a power of two that 32 values share)
+ *                   and the gated product act(g) u in the element type
  *   RNN_SAVE_INT8   x and the projections as 8-bit checkpoints (the format of
  *                   rnn_checkpoint_store); backward then needs no x */
 typedef enum RNN_ENUM_BASE { RNN_SAVE_NONE = 0, RNN_SAVE_FULL = 1, RNN_SAVE_INT8 = 2 } rnn_save_t;
 
-/* UNSUPPORTED: D or F >= 2^20, or M >= 2^30. */
+/* The workspace holds padded copies of operands whose rows are not whole,
+ * aligned 16-byte pieces, the gated product or its gradients, and partial sums
+ * of products that split k; nothing in it outlives a call.
+ * UNSUPPORTED: D or F >= 2^20, or M >= 2^30. */
 rnn_status_t rnn_ffn_workspace_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
 rnn_status_t rnn_ffn_reserve_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
 
