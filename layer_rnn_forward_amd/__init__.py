@@ -1,6 +1,6 @@
 """MI355X-native fused stacked RNN operator (vanilla tanh RNN, LSTM, GRU).
 
-A thin ctypes binding over ``librnn_mi355x.so`` (HIP kernels for gfx950 plus
+A thin binding (ctypes, and compiled entries for the language-model operators) over ``librnn_mi355x.so`` (HIP kernels for gfx950 plus
 a C ABI, declared in ``include/rnn.h``).  Functions carry the C names and only
 marshal arguments: torch tensors become device pointers, the current torch
 stream becomes the HIP stream.  Every step of the computation runs in the

@@ -19,6 +19,7 @@ KERNEL_NAMES = ["gemm_input", "recurrent_fwd", "recurrent_bwd", "gemm_dx", "gemm
 STATUS_DEVICE_TIMEOUT = -7
 
 _LIB = None
+_CALL = None      # the compiled entries of the language-model operators (csrc/call.cpp)
 
 
 class RNNError(RuntimeError):
@@ -36,7 +37,7 @@ def lib_path() -> str:
 
 def load_library():
     """Load the HIP library; raises if it has not been built."""
-    global _LIB
+    global _LIB, _CALL
     if _LIB is not None:
         return _LIB
     path = lib_path()
@@ -89,7 +90,15 @@ def load_library():
     lib.rnn_status_string.restype = ctypes.c_char_p
     lib.rnn_static_workspace_bytes.argtypes = []
     lib.rnn_static_workspace_bytes.restype = ctypes.c_size_t
-    _LIB = lib
+    try:
+        from . import _call
+    except ImportError as e:
+        raise RuntimeError(f"{os.path.dirname(path)}/_call.so cannot be loaded ({e}): build the extension first "
+                           "(python -m layer_rnn_forward_amd.build)") from e
+    _call.bind(*(ctypes.cast(getattr(lib, n), vp).value for n in (
+        "rnn_scan_step", "rnn_scan_forward", "rnn_scan_backward", "rnn_ffn_forward", "rnn_ffn_backward",
+        "rnn_checkpoint_size", "rnn_checkpoint_store", "rnn_checkpoint_load")))
+    _LIB, _CALL = lib, _call
     return lib
 
 
@@ -310,7 +319,23 @@ def rnn_profile_read(h, kernel: int):
 
 
 # ------------------------------------------------- language-model operators
+# Each call goes to its compiled entry (_call), which checks its arguments and
+# returns the status, or None where a check failed; the code after it then
+# finds the failing check and raises.
 _WTYPE_OF = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _entries():
+    load_library()
+    return _CALL
+
+
+def _done(status, where):
+    """Whether the compiled entry made the call (raises if it failed)."""
+    if status is None:
+        return False
+    _check(status, where)
+    return True
 
 
 def _addr(t, name, dev, dtype, shape, optional=False):
@@ -391,6 +416,9 @@ def rnn_scan_step(mode, g, h, y, hy):
     """One step of the gated linear recurrence (a generated token):
     ``g`` [B, 2H]; ``h`` (or None: zeros) and ``hy`` [B, H] float32, which may
     be the same tensor; ``y`` [B, H] in g's type, or None."""
+    status = (_CALL or _entries()).scan_step(mode, g, h, y, hy)
+    if status == 0 or _done(status, "rnn_scan_step"):
+        return
     m = _choice(SCAN_MODES, mode, "mode")
     dt, w, dev = _elements(g, "g", 2)
     B, H2 = g.shape
@@ -410,6 +438,9 @@ def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
     "gated" a = sigmoid(p), b = sigmoid(-p) tanh(q); "linear" a = p, b = q.
     ``y`` [T, B, dirs*H]; ``hy`` [dirs, B, H] float32 (its shape gives dirs
     and H); ``h0`` as hy, or None (zeros); ``lengths`` int32 [B] or None."""
+    status = (_CALL or _entries()).scan_forward(mode, g, h0, lengths, y, hy, ws)
+    if status == 0 or _done(status, "rnn_scan_forward"):
+        return
     m = _choice(SCAN_MODES, mode, "mode")
     dt, w, dev = _elements(g, "g", 3)
     if not isinstance(hy, torch.Tensor) or hy.dim() != 3:
@@ -430,6 +461,9 @@ def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
     """Gradients of the rnn_scan_forward call that filled ``ws`` (same mode, g,
     h0 and lengths): ``dy`` [T, B, dirs*H], ``dhy`` as hy or None (zeros);
     ``dg`` as g, ``dh0`` [dirs, B, H] float32 (its shape gives dirs and H)."""
+    status = (_CALL or _entries()).scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws)
+    if status == 0 or _done(status, "rnn_scan_backward"):
+        return
     m = _choice(SCAN_MODES, mode, "mode")
     dt, w, dev = _elements(g, "g", 3)
     if not isinstance(dh0, torch.Tensor) or dh0.dim() != 3:
@@ -471,6 +505,9 @@ def rnn_ffn_forward(act, x, w_in, w_out, y, ws, save="none", reserve=None):
     w_in = [Wg; Wu]: ``x``, ``y`` [M, D], ``w_in`` [2F, D], ``w_out`` [D, F],
     all float32 or all bfloat16; act "sigmoid", "silu" or "gelu" (tanh form);
     save "none", "full" or "int8": what ``reserve`` keeps for backward."""
+    status = (_CALL or _entries()).ffn_forward(act, x, w_in, w_out, y, ws, save, reserve)
+    if status == 0 or _done(status, "rnn_ffn_forward"):
+        return
     a, sv = _choice(ACTS, act, "act"), _choice(SAVES, save, "save")
     dt, w, dev = _elements(x, "x", 2)
     _elements(w_out, "w_out", 2)
@@ -489,6 +526,9 @@ def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reser
     """Gradients of the rnn_ffn_forward call that filled ``reserve``; ``x`` may
     be None with save "int8"; each of ``dx``, ``dw_in`` and ``dw_out`` may be
     None (not wanted)."""
+    status = (_CALL or _entries()).ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reserve)
+    if status == 0 or _done(status, "rnn_ffn_backward"):
+        return
     a, sv = _choice(ACTS, act, "act"), _choice(SAVES, save, "save")
     dt, w, dev = _elements(dy, "dy", 2)
     _elements(w_out, "w_out", 2)
@@ -506,6 +546,9 @@ def rnn_ffn_backward(act, x, w_in, w_out, dy, dx, dw_in, dw_out, ws, save, reser
 
 def rnn_checkpoint_size(rows: int, cols: int) -> int:
     """Bytes of the 8-bit checkpoint of a matrix [rows, cols]."""
+    size = (_CALL or _entries()).checkpoint_size(rows, cols)
+    if size is not None:
+        return size
     _ints(rows, cols)
     n = ctypes.c_size_t()
     _check(load_library().rnn_checkpoint_size(rows, cols, ctypes.byref(n)), "rnn_checkpoint_size")
@@ -515,6 +558,9 @@ def rnn_checkpoint_size(rows: int, cols: int) -> int:
 def rnn_checkpoint_store(x, kept):
     """Keep ``x`` [rows, cols] in 8 bits a value with one power of two per 32
     columns of a row, in the buffer ``kept``."""
+    status = (_CALL or _entries()).checkpoint_store(x, kept)
+    if status == 0 or _done(status, "rnn_checkpoint_store"):
+        return
     dt, w, dev = _elements(x, "x", 2)
     kp, kn = _room(kept, "kept", dev)
     status = (_LIB or load_library()).rnn_checkpoint_store(_on(dev), w, x.shape[0], x.shape[1], _addr(x, "x", dev, dt, x.shape),
@@ -526,6 +572,9 @@ def rnn_checkpoint_store(x, kept):
 def rnn_checkpoint_load(kept, x):
     """Read a checkpoint of a matrix of x's shape back into ``x`` [rows, cols]
     (float32 or bfloat16; both hold its values exactly)."""
+    status = (_CALL or _entries()).checkpoint_load(kept, x)
+    if status == 0 or _done(status, "rnn_checkpoint_load"):
+        return
     dt, w, dev = _elements(x, "x", 2)
     kp, kn = _room(kept, "kept", dev)
     status = (_LIB or load_library()).rnn_checkpoint_load(_on(dev), w, x.shape[0], x.shape[1], kp, kn,

@@ -19,6 +19,7 @@ LIB = os.path.join(PKG, "librnn_mi355x.so")
 SOURCES = ["checkpoint.hip", "dropout.hip", "ffn.hip", "ffn_dglu.hip", "ffn_glu.hip", "ffn_rows.hip", "gemm.hip", "layout.hip", "lm_api.cpp", "recurrent.hip",
            "recurrent_gru2.hip", "rnn_api.cpp", "scan.hip",
            *[f"recurrent_{m}_{k}.hip" for m in ("tanh", "lstm", "gru") for k in ("fwd", "bwd")]]
+CALL_LIB = os.path.join(PKG, "_call.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -84,7 +85,28 @@ def _build(out_lib: str, obj_dir: str, sanitize: bool, verbose: bool, defines=()
 
 
 def build(verbose: bool = False) -> str:
-    return _build(LIB, BUILD, False, verbose)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        call = ex.submit(build_call)
+        lib = _build(LIB, BUILD, False, verbose)
+        call.result()
+    return lib
+
+
+def build_call() -> str:
+    """The Python entries of the language-model operators (csrc/call.cpp): host code against the installed torch."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = CALL_LIB + ".tmp"
+    _run(["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(t, "include"), "-isystem",
+          os.path.join(t, "include", "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+          "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "call.cpp"), "-o", tmp,
+          "-L", os.path.join(t, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, CALL_LIB)
+    return CALL_LIB
 
 
 def build_perturbed(verbose: bool = False) -> str:
