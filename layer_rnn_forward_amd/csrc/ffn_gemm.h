@@ -402,9 +402,9 @@ __device__ __forceinline__ void dglu_tile(const f32x16& dh, const Saved<BF, SAVE
 
 enum FfnEpi { FFN_STORE = 0, FFN_GLU = 1, FFN_DGLU = 2 };
 
-// Tile `lin` of tm x tn: groups of 8 tile rows, column by column.
+// Tile `lin` of tm x tn: groups of 4 tile rows, column by column.
 __device__ __forceinline__ void tile_at(int lin, int tm, int tn, int& m, int& n) {
-  constexpr int GM = 8;
+  constexpr int GM = 4;
   const int grp = lin / (GM * tn), in = lin - grp * GM * tn, gm = min(GM, tm - grp * GM);
   m = grp * GM + in % gm;
   n = in / gm;
@@ -426,7 +426,7 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
   lds_char* const lds_a = (lds_char*)smem;
   lds_char* const lds_b = lds_a + kStagesA * OpA::BYTES;
 
-  // tiles: contiguous runs per XCD; inside, groups of 8 tile rows, column by
+  // tiles: contiguous runs per XCD; inside, groups of 4 tile rows, column by
   // column, so that the tiles in flight on one XCD share few row blocks
   const int tm = (p.M + TM - 1) / TM, tn = (p.N + FN - 1) / FN;
   int lin = block % 8 * (blocks / 8) + block / 8, split = 0;
@@ -570,15 +570,18 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           acc[i][j] = mfma32<BF>(fb[kk & 1][j], fa[kk & 1][i], acc[i][j]);
-          if (i == 0) rb.read(kk < 3 ? b0 : b1, (kk + 1) & 3, j, fb[(kk + 1) & 1][j]);
-          if (i == (MT > 1 ? 1 : 0)) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-              if (t * NT / MT == j) ra.read(kk < 3 ? a0 : a1, (kk + 1) & 3, t, fa[(kk + 1) & 1][t]);
-          }
           constexpr int S = MT * NT;
           const int at = i * NT + j;
           auto share = [&](int from, int n, int k) { return from + n * k / S; };   // of n loads from `from` on
+          // fragments in the order in which they will be used
+#pragma unroll
+          for (int r = 0; r < MT + NT; ++r) {
+            if (r < share(0, MT + NT, at) || r >= share(0, MT + NT, at + 1)) continue;
+            if (r == 0) rb.read(kk < 3 ? b0 : b1, (kk + 1) & 3, 0, fb[(kk + 1) & 1][0]);
+            else if (r == 1) ra.read(kk < 3 ? a0 : a1, (kk + 1) & 3, 0, fa[(kk + 1) & 1][0]);
+            else if (r <= NT) rb.read(kk < 3 ? b0 : b1, (kk + 1) & 3, r - 1, fb[(kk + 1) & 1][r - 1]);
+            else ra.read(kk < 3 ? a0 : a1, (kk + 1) & 3, r - NT, fa[(kk + 1) & 1][r - NT]);
+          }
           if (kk == 3) {
             fill_b(share(0, LB * 3 / 4, at), share(0, LB * 3 / 4, at + 1), b0);
           } else if (kk == 0) {

@@ -154,3 +154,27 @@ def test_binding_refuses_tensors_of_other_shapes_and_types():
         R.rnn_checkpoint_store(x, ws[:7])
     with pytest.raises(ValueError, match="C int"):
         R.rnn_scan_workspace_size(1 << 32, 1, 1)
+
+
+@pytest.mark.parametrize("dtype,T,B,H,dirs", [("bf16", 3000, 2, 200, 2), ("f32", 700, 3, 75, 1), ("bf16", 100, 2, 64, 1)])
+def test_backward_again_and_again(dtype, T, B, H, dirs):
+    """Backward passes that follow one forward pass, eager or in a graph of their own, give the same gradients."""
+    c = scan.make("gated", dtype, T, B, H, dirs, [T] + [T // 3] * (B - 1))
+    want = scan.run(c)
+    g, h0, n, dy, dhy = (scan.cuda(c[k]) for k in ("g", "h0", "lengths", "dy", "dhy"))
+    ws = torch.full((R.rnn_scan_workspace_size(T, B, H, dirs),), 0x11, dtype=torch.uint8, device="cuda")
+    R.rnn_scan_forward("gated", g, h0, n, torch.empty_like(want["y"]), torch.empty_like(want["hy"]), ws)
+    dg, dh0 = torch.empty_like(g), torch.empty_like(h0)
+    for _ in range(3):
+        dg.fill_(3.0)
+        R.rnn_scan_backward("gated", g, h0, n, dy, dhy, dg, dh0, ws)
+        assert torch.equal(dg, want["dg"]) and torch.equal(dh0, want["dh0"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        R.rnn_scan_backward("gated", g, h0, n, dy, dhy, dg, dh0, ws)
+    for _ in range(3):
+        dg.fill_(5.0)
+        (g.float() * 2).sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dg, want["dg"]) and torch.equal(dh0, want["dh0"])
