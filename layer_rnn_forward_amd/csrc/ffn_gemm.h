@@ -9,25 +9,37 @@
 //
 // Tile: 64*MT x 64*NT per workgroup of 2 x 2 waves, each wave MT x NT
 // accumulators of 32 x 32; 128 bytes of k per step (64 bf16 or 32 fp32
-// values), two LDS stages filled by 16-byte buffer loads straight into LDS.
-// Every lane's byte offset in a tile is fixed and the tile's base advances in
-// scalar registers; a lane whose row or k lies outside the operand asks for
-// an offset past the buffer's range, which the hardware answers with zeros,
-// so edges cost one select and no branch.  The fragments of the next 16 (or
-// 8) k are read while those of this one are multiplied, and the step's
-// barrier stands before its last quarter of products, when every fragment of
-// the stage is in registers: the stage is refilled at once and the products
-// hide the wait.
+// values), filled by 16-byte buffer loads straight into LDS: three stages of A
+// and two of B, which is all of the 160 KB for 256 x 256 tiles.  Every lane's
+// byte offset in a tile is fixed and the tile's base advances in scalar
+// registers; a lane whose row or k lies outside the operand asks for an offset
+// past the buffer's range, which the hardware answers with zeros, so edges
+// cost one select and no branch.  The fragments of the next 16 (or 8) k are
+// read while those of this one are multiplied, and the step's barrier stands
+// before its last quarter of products, when every fragment of the stage is in
+// registers.
 //
 // LDS layouts (16-byte pieces, so that the lanes of a read hit distinct
-// banks):  rows: tile row r is 128 bytes, piece c at c ^ (r & 7).  columns:
-// LDS row k holds the tile's r, piece c at c ^ swz(k); bf16 fragments are
-// read with the transposing 8-byte LDS read (four k of one r per lane).
+// banks):  rows: tile row r is 128 bytes, piece c at c ^ (r >> 1 & 7).
+// columns: LDS row k holds the tile's r, piece c at c ^ swz(k); bf16 fragments
+// are read with the transposing 8-byte LDS read (four k of one r per lane).
 //
 // The weight operand B is the MFMA's first operand, so a lane's accumulators
 // are runs of four neighbouring n of one row m: rows of C are stored in
 // 16-byte pieces, and the 32 columns of a group that shares an exponent lie
 // in two lanes.
+//
+// Bound by the matrix cores at the clock that power leaves them (1.6 - 1.7 GHz):
+// 275 GFLOP (8192 x 2048, k 8192, rows x rows) take 0.235 ms, 1170 TFLOP/s, the
+// MFMA busy for 70 % of the cycles; with every refill left out it is 0.160 ms at
+// 2.2 GHz.  Measured on that product, or on the 8192 x 2048 x 8192 training step
+// (now 2.07 ms):  all loads right after the barrier 2.26 ms (a CU takes 16
+// cycles for each, and the wave that waits for its turn issues no products);
+// 64-byte steps in four stages 0.268 ms (rows then ask the L2 for twice as many
+// lines, one a cycle and channel: all it has); pieces at c ^ (r & 7) conflict
+// two ways; groups of 8 tile rows 2.09 ms; the fragments' reads ahead of the
+// loads or spread evenly: the same.  16 x 16 accumulators (0.226 ms) need 64
+// more fragment registers, and the epilogues then spill.
 #pragma once
 
 #include <algorithm>
