@@ -395,7 +395,7 @@ rnn_status_t rnn_profile_read(rnn_handle_t h, int kernel, long long* launches, d
 typedef enum RNN_ENUM_BASE { RNN_SCAN_GATED = 0, RNN_SCAN_LINEAR = 1 } rnn_scan_mode_t;
 
 /* Bytes of the workspace of one forward call and the backward calls that
- * follow it.  UNSUPPORTED: B * H * dirs >= 2^30. */
+ * follow it.  UNSUPPORTED: B * H * dirs >= 2^30, or T >= 2^31 - 1024. */
 rnn_status_t rnn_scan_workspace_size(int T, int B, int H, int dirs, size_t* bytes);
 
 /* One step of one direction (a generated token): g [B, 2 * H], h [B, H] (NULL:

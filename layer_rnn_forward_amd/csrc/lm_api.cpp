@@ -38,6 +38,7 @@ rnn_status_t scan_sizes(int T, int B, int H, int dirs) {
   if (T < 0 || B < 0 || H < 0 || (dirs != 1 && dirs != 2)) return RNN_STATUS_INVALID_ARG;
   // B * H first: it fits 64 bits, times dirs as well
   if ((long long)B * H * dirs >= (1LL << 30)) return RNN_STATUS_UNSUPPORTED;
+  if (T > 0x7fffffff - 1024) return RNN_STATUS_UNSUPPORTED;   // the last chunk's steps are counted past T
   return RNN_STATUS_SUCCESS;
 }
 

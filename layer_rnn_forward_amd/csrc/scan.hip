@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "lm_math.h"
+#include "recurrent_util.h"
 
 using namespace rnnk;
 
@@ -219,6 +220,7 @@ __device__ __forceinline__ Place place(const ScanParams& p, int VW, unsigned& sh
   Place r;
   r.pos = 0;
   if (p.chunks > 1) {
+    perturb_pause(wave_tag(), 0u, 3u);
     if (threadIdx.x == 0) shared = atomicAdd(p.counters + tile * 16LL, 1u);
     __syncthreads();
     r.pos = __builtin_amdgcn_readfirstlane(shared);
@@ -257,12 +259,14 @@ __device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, 
         tB[e] = apply(a, tB[e], sB[w][lane * VW + e]);
       }
     const bool ends = pos % SUPER == SUPER - 1, more = pos + 1 < p.chunks;
+    perturb_pause(wave_tag(), pos, 4u);
     if (more && !ends && live)
 #pragma unroll
       for (int e = 0; e < VW; ++e) publish2(p.maps + (long long)pos * C + c + e, tA[e], tB[e]);
 #pragma unroll
     for (int e = 0; e < VW; ++e) h[e] = first && live ? first[c + e] : 0.f;
     if (pos > 0) wait_state<VW, SUPER>(p, pos, C, c, live, h);
+    perturb_pause(wave_tag(), pos, 5u);
     if (more && ends && live)
 #pragma unroll
       for (int e = 0; e < VW; ++e) publish(p.state + (long long)(pos / SUPER + 1) * C + c + e, apply(tA[e], h[e], tB[e]));
