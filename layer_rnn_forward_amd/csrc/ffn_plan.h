@@ -91,19 +91,19 @@ inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const
 }
 
 // The tile that takes least, each with whole k and (the smaller two) with k in
-// pieces of about an equal share of the work for two places a CU (8 steps at
-// least).
+// pieces of an equal share of the work for one to four places a CU, 8 steps at
+// least.
 inline FfnChoice ffn_choose(const FfnGemm* const* p, int n, int bf16, bool glu, bool may_split) {
   FfnChoice best;
   double least = -1;
   for (int t = bf16 ? TILE_256 : TILE_128; t <= TILE_64; ++t) {
-    for (int split = 0; split <= (may_split && t != TILE_256 ? 1 : 0); ++split) {
+    long long work = 0;
+    for (int i = 0; i < n; ++i) work += ffn_tiles(*p[i], t, glu) * ffn_steps(*p[i], bf16);
+    for (int share = 0; share <= (may_split && t != TILE_256 ? 4 : 0); ++share) {
       FfnChoice c;
       c.tile = t;
-      if (split) {
-        long long work = 0;
-        for (int i = 0; i < n; ++i) work += ffn_tiles(*p[i], t, glu) * ffn_steps(*p[i], bf16);
-        const long long piece = std::max(8LL, work / 512);
+      if (share) {
+        const long long piece = std::max(8LL, (work + 256 * share - 1) / (256 * share));
         bool any = false;
         for (int i = 0; i < n; ++i) {
           const long long steps = ffn_steps(*p[i], bf16);
