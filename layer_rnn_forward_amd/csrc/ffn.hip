@@ -77,7 +77,7 @@ template <bool BF, int T>
 __global__ __launch_bounds__(256) void sum_kernel(const Jobs j) {
   const int b = (int)blockIdx.x, i = job_of(j, b);
   const FfnGemm p = j.p[i];
-  ffn_sum<BF, T, T>(p, b - j.begin[i]);
+  ffn_sum<BF, T, T, FFN_STORE, SAVE_NONE, 0>(p, b - j.begin[i]);
 }
 
 template <bool BACK, bool BF, int T, int OCC>

@@ -380,6 +380,23 @@ __device__ __forceinline__ void glu_tile(const f32x16& gv, const f32x16& uv, con
   }
 }
 
+// A wave's tiles, 16 * NT gate columns and then the up columns of the same:
+// rows from m0, columns from f0.
+template <int ACT, bool BF, int SAVE, int MT, int NT>
+__device__ __forceinline__ void glu_tiles(const f32x16 (&acc)[MT][NT], const FfnGemm& p, long long m0, int f0, int lane) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const long long m = m0 + i * 32 + (lane & 31);
+    if (m < p.M) {
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) {
+        const int f = f0 + j * 32;
+        if (f < p.N) glu_tile<ACT, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, lane);
+      }
+    }
+  }
+}
+
 // dh of 32 columns -> dgate, dup (and the gated product again, from 8 bits)
 template <int ACT, bool BF, int SAVE>
 __device__ __forceinline__ void dglu_tile(const f32x16& dh, const Saved<BF, SAVE>& s0, const Saved<BF, SAVE>& s1,
@@ -432,7 +449,7 @@ template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, in
 __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int block, int blocks) {
   constexpr int TM = 64 * MT, TN = 64 * NT, ES = BF ? 2 : 4, BK = kStep / ES;
   constexpr int FN = EPI == FFN_GLU ? TN / 2 : TN;   // columns of C per tile
-  constexpr bool SPLIT = EPI == FFN_STORE && MT < 4;
+  constexpr bool SPLIT = EPI != FFN_DGLU && MT < 4;
   using OpA = Operand<BF, AROWS, TM>;
   using OpB = Operand<BF, BROWS, TN>;
   lds_char* const lds_a = (lds_char*)smem;
@@ -623,8 +640,8 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
   // no load into LDS outlives the workgroup
   __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
 
-  if constexpr (EPI == FFN_STORE) {
-    if (SPLIT && p.splits > 1) {
+  if constexpr (SPLIT) {
+    if (p.splits > 1) {
       float4* to = (float4*)p.part + ((long long)split * tm * tn + lin) * (MT * NT * 4 * 256) + tid;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -634,22 +651,18 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
           for (int e = 0; e < 4; ++e)
             to[((i * NT + j) * 4 + e) * 256] =
                 make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
-    } else {
-      store_tiles<BF, MT, NT>(acc, p, m0 + wm, n0 + wn, lane);
+      return;
     }
-    return;
   }
+  if constexpr (EPI == FFN_STORE) {
+    store_tiles<BF, MT, NT>(acc, p, m0 + wm, n0 + wn, lane);
+  } else if constexpr (EPI == FFN_GLU) {
+    glu_tiles<ACT, BF, SAVE, MT, NT>(acc, p, m0 + wm, n0 + (wave & 1) * 16 * NT, lane);
+  } else {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const long long m = m0 + wm + i * 32 + (lane & 31);
-    if (m < p.M) {
-      if constexpr (EPI == FFN_GLU) {
-#pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-          const int f = n0 + (wave & 1) * 16 * NT + j * 32;
-          if (f < p.N) glu_tile<ACT, BF, SAVE>(acc[i][j], acc[i][j + NT / 2], p, m, f, lane);
-        }
-      } else if constexpr (EPI == FFN_DGLU) {
+    for (int i = 0; i < MT; ++i) {
+      const long long m = m0 + wm + i * 32 + (lane & 31);
+      if (m < p.M) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int f = n0 + wn + j * 32;
@@ -669,10 +682,11 @@ __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
   ffn_product<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT>(p, smem, (int)blockIdx.x, (int)gridDim.x);
 }
 
-// Add the splits of a tile in their order and store it.
-template <bool BF, int MT, int NT>
+// Add the splits of a tile in their order; the epilogue.
+template <bool BF, int MT, int NT, int EPI, int SAVE, int ACT>
 __device__ __forceinline__ void ffn_sum(const FfnGemm& p, int lin) {
-  const int tm = (p.M + 64 * MT - 1) / (64 * MT), tn = (p.N + 64 * NT - 1) / (64 * NT);
+  constexpr int FN = EPI == FFN_GLU ? 32 * NT : 64 * NT;
+  const int tm = (p.M + 64 * MT - 1) / (64 * MT), tn = (p.N + FN - 1) / FN;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const float4* from = (const float4*)p.part + (long long)lin * (MT * NT * 4 * 256) + tid;
   const long long next = (long long)tm * tn * (MT * NT * 4 * 256);
@@ -695,23 +709,32 @@ __device__ __forceinline__ void ffn_sum(const FfnGemm& p, int lin) {
     }
   int m, n;
   tile_at(lin, tm, tn, m, n);
-  store_tiles<BF, MT, NT>(acc, p, m * 64 * MT + (wave >> 1) * 32 * MT, n * 64 * NT + (wave & 1) * 32 * NT, lane);
+  const long long m0 = m * 64 * MT + (wave >> 1) * 32 * MT;
+  const int n0 = n * FN + (wave & 1) * (FN / 2);
+  if constexpr (EPI == FFN_GLU) glu_tiles<ACT, BF, SAVE, MT, NT>(acc, p, m0, n0, lane);
+  else store_tiles<BF, MT, NT>(acc, p, m0, n0, lane);
+}
+template <bool BF, int MT, int NT, int EPI, int SAVE, int ACT>
+__global__ __launch_bounds__(256) void ffn_sum_kernel(const FfnGemm p) {
+  ffn_sum<BF, MT, NT, EPI, SAVE, ACT>(p, (int)blockIdx.x);
 }
 
 // ---------------------------------------------------------------- launches
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
 hipError_t ffn_launch(const FfnGemm& p, long long tiles, hipStream_t s) {
-  if (tiles > 0x7ffffff0LL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((ffn_gemm_kernel<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT, OCC>), dim3((unsigned)((tiles + 7) / 8 * 8)),
-                     dim3(256), 0, s, p);
+  const int splits = std::max(p.splits, 1);
+  if (tiles * splits > 0x7ffffff0LL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((ffn_gemm_kernel<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT, OCC>),
+                     dim3((unsigned)((tiles * splits + 7) / 8 * 8)), dim3(256), 0, s, p);
+  if constexpr (EPI == FFN_GLU && MT < 4) {
+    if (splits > 1) hipLaunchKernelGGL((ffn_sum_kernel<BF, MT, NT, EPI, SAVE, ACT>), dim3((unsigned)tiles), dim3(256), 0, s, p);
+  }
   return hipGetLastError();
 }
 
 template <bool AROWS, bool BROWS, int EPI, int SAVE, int ACT>
-hipError_t ffn_pick(const FfnGemm& p, int bf16, hipStream_t s) {
+hipError_t ffn_pick(const FfnGemm& p, int tile, int bf16, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  const FfnGemm* one[1] = {&p};
-  const int tile = ffn_choose(one, 1, bf16, EPI == FFN_GLU, false).tile;
   const long long tiles = ffn_tiles(p, tile, EPI == FFN_GLU);
   constexpr int N64 = EPI == FFN_GLU ? 2 : 1;
   if (!bf16) {

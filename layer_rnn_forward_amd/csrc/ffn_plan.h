@@ -16,9 +16,11 @@ constexpr int kTile[3] = {256, 128, 64};
 
 inline long long ffn_tiles(const FfnGemm& p, int tile, bool glu) {
   if (p.M <= 0 || p.N <= 0) return 0;
-  const int fn = !glu ? kTile[tile] : tile == TILE_64 ? 64 : kTile[tile] / 2;
+  const int fn = !glu ? kTile[tile] : tile == TILE_64 ? 64 : kTile[tile] / 2;   // columns of C
   return ((long long)p.M + kTile[tile] - 1) / kTile[tile] * (((long long)p.N + fn - 1) / fn);
 }
+// Accumulators of a tile.
+inline int ffn_area(int tile, bool glu) { return kTile[tile] * kTile[tile] * (glu && tile == TILE_64 ? 2 : 1); }
 inline long long ffn_steps(const FfnGemm& p, int bf16) {
   const int bk = kStep / (bf16 ? 2 : 4);
   return ((long long)p.K + bk - 1) / bk * p.segs;
@@ -34,7 +36,7 @@ struct FfnChoice {
 // CU to itself and with all of its places taken (in between: linear):
 //   bf16   256: 1.45 us   128: 0.50 us, two a CU 0.86 us   64: 0.31 us, three a CU 0.54 us
 //   fp32                  128: 1.9 us,  two a CU 3.8 us    64: 0.5 us,  three a CU 1.44 us
-// A step of the gated product's 64 x 128 takes 1.3 (alone) or 2 of a 64 x 64's.
+// A step of the gated product's 64 x 128 takes 2 of a 64 x 64's (bf16, alone: 1.3).
 inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const FfnChoice& c) {
   static constexpr double alone[2][3] = {{0, 190, 50}, {145, 50, 31}}, full[2][3] = {{0, 380, 144}, {145, 86, 54}};
   static constexpr int most[3] = {1, 2, 3};
@@ -44,12 +46,12 @@ inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const
     const long long pieces = ffn_tiles(*p[i], c.tile, glu) * c.splits[i];
     all += pieces;
     // a second launch, and the partial sums' way out and back at about 3 TB/s
-    if (c.splits[i] > 1) after = std::max(after, 500.0) + (double)pieces * kTile[c.tile] * kTile[c.tile] * 8 / 3e4;
+    if (c.splits[i] > 1) after = std::max(after, 500.0) + (double)pieces * ffn_area(c.tile, glu) * 8 / 3e4;
   }
   const int occ = (int)std::max(1LL, std::min<long long>(most[c.tile], (all + 255) / 256)), places = 256 * occ;
   const double share = occ > 1 ? (occ - 1.0) / (most[c.tile] - 1) : 0;
   double step = alone[bf16][c.tile] + share * (full[bf16][c.tile] - alone[bf16][c.tile]);
-  if (glu && c.tile == TILE_64) step *= 1.3 + 0.7 * share;
+  if (glu && c.tile == TILE_64) step *= bf16 ? 1.3 + 0.7 * share : 2;
   struct Group {
     double time;
     long long count;
@@ -92,7 +94,12 @@ inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const
 
 // The tile that takes least, each with whole k and (the smaller two) with k in
 // pieces of an equal share of the work for one to four places a CU, 8 steps at
-// least.
+// least.  A product alone has no more pieces than those places (one more would
+// start a second round); with shorter products beside it, its last piece may be
+// the shorter one.
+// Forward's projections split or whole, cold caches: 270 x 3272 x 848 fp32 92 or
+// 158 us a forward pass, 189 x 2776 x 392 bf16 28 or 48, 129 x 4096 x 4096 fp32
+// 206 or 222; 70 x 2501 x 130 fp32 with gradients 108 or 175.
 inline FfnChoice ffn_choose(const FfnGemm* const* p, int n, int bf16, bool glu, bool may_split) {
   FfnChoice best;
   double least = -1;
@@ -107,7 +114,7 @@ inline FfnChoice ffn_choose(const FfnGemm* const* p, int n, int bf16, bool glu, 
         bool any = false;
         for (int i = 0; i < n; ++i) {
           const long long steps = ffn_steps(*p[i], bf16);
-          if (2 * steps >= 3 * piece) c.splits[i] = (int)std::min(64LL, (steps + piece - 1) / piece);
+          if (2 * steps >= 3 * piece) c.splits[i] = (int)std::min(64LL, n > 1 ? (steps + piece - 1) / piece : steps / piece);
           any = any || c.splits[i] > 1;
         }
         if (!any) continue;
@@ -123,13 +130,20 @@ inline FfnChoice ffn_choose(const FfnGemm* const* p, int n, int bf16, bool glu, 
 }
 
 // Bytes of the partial sums of product i.
-inline size_t ffn_part(const FfnGemm& p, const FfnChoice& c, int i) {
+inline size_t ffn_part(const FfnGemm& p, const FfnChoice& c, int i, bool glu) {
   if (c.splits[i] <= 1) return 0;
-  return (size_t)ffn_tiles(p, c.tile, false) * c.splits[i] * kTile[c.tile] * kTile[c.tile] * 4;
+  return (size_t)ffn_tiles(p, c.tile, glu) * c.splits[i] * ffn_area(c.tile, glu) * 4;
 }
 
-// The products that may be split, by their sizes alone: forward's second one,
-// and backward's three, longest first (the order that ffn_order gives).
+// The products that may be split, by their sizes alone: forward's two, and
+// backward's last three, longest first (the order that ffn_choose_backward
+// gives).
+inline void ffn_gated_product(int M, int D, int F, FfnGemm& g) {
+  g.M = M;
+  g.N = F;
+  g.K = D;
+  g.segs = 1;
+}
 inline void ffn_forward_product(int M, int D, int F, FfnGemm& o) {
   o.M = M;
   o.N = D;
@@ -153,9 +167,9 @@ inline void ffn_backward_products(int M, int D, int F, int Fp, FfnGemm (&o)[3]) 
   o[2].K = M;
   o[2].segs = 1;
 }
-inline FfnChoice ffn_choose_forward(const FfnGemm& o, int bf16) {
+inline FfnChoice ffn_choose_forward(const FfnGemm& o, int bf16, bool glu) {
   const FfnGemm* one[1] = {&o};
-  return ffn_choose(one, 1, bf16, false, true);
+  return ffn_choose(one, 1, bf16, glu, true);
 }
 // splits in the products' own order; order: longest first
 inline FfnChoice ffn_choose_backward(const FfnGemm (&o)[3], int bf16, int (&order)[3]) {

@@ -97,10 +97,10 @@ struct FfnPlan {
   size_t x = 0, w_in = 0, w_out = 0, dy = 0, h = 0, dgu = 0, ws = 0;
   // and the partial sums of split products; the choices do not depend on which
   // gradients are wanted
-  FfnGemm out{}, grads[3] = {};
-  FfnChoice out_choice, grads_choice;
+  FfnGemm gated{}, out{}, grads[3] = {};
+  FfnChoice gated_choice, out_choice, grads_choice;
   int order[3] = {0, 1, 2};
-  size_t out_part = 0, grads_part[3] = {};
+  size_t part = 0, grads_part[3] = {};   // forward's products use theirs one after the other
   // reserve
   size_t s0 = 0, s1 = 0, e0 = 0, e1 = 0, rh = 0, rx = 0, reserve = 0;
 };
@@ -129,10 +129,13 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
   }
   const int bf = wtype == RNN_W_BF16;
   ffn_forward_product(M, D, F, p.out);
-  p.out_choice = ffn_choose_forward(p.out, bf);
+  p.out_choice = ffn_choose_forward(p.out, bf, false);
   p.out.splits = p.out_choice.splits[0];
+  ffn_gated_product(M, D, F, p.gated);
+  p.gated_choice = ffn_choose_forward(p.gated, bf, true);
+  p.gated.splits = p.gated_choice.splits[0];
   const size_t parts = o;
-  p.out_part = take(ffn_part(p.out, p.out_choice, 0));
+  p.part = take(std::max(ffn_part(p.out, p.out_choice, 0, false), ffn_part(p.gated, p.gated_choice, 0, true)));
   const size_t forward = o;
   o = parts;              // the passes' partial sums share their place
   if (save != RNN_SAVE_NONE) {
@@ -140,7 +143,7 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
     p.grads_choice = ffn_choose_backward(p.grads, bf, p.order);
     for (int i = 0; i < 3; ++i) {
       p.grads[i].splits = p.grads_choice.splits[i];
-      p.grads_part[i] = take(ffn_part(p.grads[i], p.grads_choice, i));
+      p.grads_part[i] = take(ffn_part(p.grads[i], p.grads_choice, i, false));
     }
   }
   p.ws = std::max({o, forward, kAlign});
@@ -283,20 +286,19 @@ rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn
   LM_TRY(dev(rnn_launch_pad(pads.j, bf, s)));
   if (save == RNN_SAVE_INT8) LM_TRY(dev(rnn_launch_ckpt_store(bf, M, D, x, at<void>(reserve, p.rx), s)));
   void* h = save == RNN_SAVE_FULL ? at<void>(reserve, p.rh) : at<void>(ws, p.h);
-  FfnGemm g{};
-  g.M = M; g.N = F; g.K = D;
+  FfnGemm g = p.gated;
   g.A = xp; g.lda = p.Dp;
   g.B = wi; g.ldb = p.Dp;
   g.C = h; g.ldc = p.Fp;
-  g.segs = 1;
+  g.part = at<void>(ws, p.part);
   g.act = act;
   if (save != RNN_SAVE_NONE) ffn_saved(g, p, reserve);
-  LM_TRY(dev(rnn_launch_ffn_glu(g, bf, save, s)));
+  LM_TRY(dev(rnn_launch_ffn_glu(g, p.gated_choice.tile, bf, save, s)));
   FfnGemm o = p.out;
   o.A = h; o.lda = p.Fp;
   o.B = wo; o.ldb = p.Fo;
   o.C = y; o.ldc = D; o.cvec = store16(y, D, p.es);
-  o.part = at<void>(ws, p.out_part);
+  o.part = at<void>(ws, p.part);
   return dev(rnn_launch_ffn_store(o, p.out_choice.tile, bf, s));
 }
 

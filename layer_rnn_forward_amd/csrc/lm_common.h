@@ -107,7 +107,7 @@ hipError_t rnn_launch_scan_step(int mode, int bf16, int B, int H, const void* g,
 hipError_t rnn_launch_scan_fwd(const rnnk::ScanParams& p, int mode, int bf16, hipStream_t s);
 hipError_t rnn_launch_scan_bwd(const rnnk::ScanParams& p, int mode, int bf16, hipStream_t s);
 
-hipError_t rnn_launch_ffn_glu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
+hipError_t rnn_launch_ffn_glu(const rnnk::FfnGemm& p, int tile, int bf16, int save, hipStream_t s);
 hipError_t rnn_launch_ffn_dglu(const rnnk::FfnGemm& p, int bf16, int save, hipStream_t s);
 // y, and dx, dw_in, dw_out (those that are not wanted have M = 0); `order`:
 // longest first

@@ -41,6 +41,20 @@ def test_split_products(dtype, size, act, save):
         assert torch.equal(ffn.run(c, act, save, (k,))[k], got[k]), k
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(70, 2501, 130), (130, 1500, 24), (257, 5000, 72), (300, 4100, 700), (256, 4000, 2048), (90, 700, 1)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("act,save", [("gelu", "none"), ("silu", "full"), ("sigmoid", "int8")])
+def test_split_projections(dtype, size, act, save):
+    print("CASE ffn split projections", dtype, size, act, save, flush=True)
+    c = ffn.make(*size, dtype)
+    got = ffn.run(c, act, save)
+    ffn.check(got, ffn.expected(c, act, save), c)
+    again = ffn.run(c, act, save)
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+
+
 @pytest.mark.parametrize("M", [8, 9, 16, 17, 32, 33, 63, 64, 65])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_on_both_sides_of_a_limit(M, dtype):
