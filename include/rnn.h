@@ -429,8 +429,9 @@ typedef enum RNN_ENUM_BASE { RNN_ACT_SIGMOID = 0, RNN_ACT_SILU = 1, RNN_ACT_GELU
 
 /* What the forward call leaves in the reserve for the backward call:
  *   RNN_SAVE_NONE   nothing (inference)
- *   RNN_SAVE_FULL   act(g), u act'(g) (g, u: the projections; with bf16 in 16
- *                   bits, whole numbers of a power of two that 32 values share)
+ *   RNN_SAVE_FULL   act(g), u act'(g) (g, u: the projections; with bf16 as fp16
+ *                   numbers times a power of two that 32 values share: half a
+ *                   step is 2^-11 of a value, or 2^-39 of the 32's largest)
  *                   and the gated product act(g) u in the element type
  *   RNN_SAVE_INT8   x and the projections as 8-bit checkpoints (the format of
  *                   rnn_checkpoint_store); backward then needs no x */

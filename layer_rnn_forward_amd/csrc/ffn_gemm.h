@@ -55,6 +55,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kStagesA = 3, kStagesB = 2;
@@ -289,26 +290,37 @@ __device__ __forceinline__ void unpack8(const u32x4& w, int ex, float (&v)[16]) 
     for (int k = 0; k < 4; ++k) v[4 * j + k] = (float)(int8_t)(w[j] >> (8 * k)) * s;
 }
 
-// 16 bits: whole numbers of 2^e, |q| <= 2^14, e the exponent of the group's
-// largest magnitude - 14, so the error is at most 2^-14 of that magnitude
-// (bf16 would be off by up to 2^-8 of each value, and a product of two such
-// values by twice that).
+// 16 bits: fp16 numbers times 2^e, e the exponent of the group's largest finite
+// magnitude - 14, which brings it into [2^14, 2^15).  Half a step is 2^-11 of
+// each value (2^-39 of the group's largest below 2^-28 of it); bf16 would be
+// off by up to 2^-8, and a product of two such values by twice that.  A value
+// far out takes nothing from its neighbours, and an infinity or a NaN is its
+// own (whole numbers of a common 2^e, 2^-14 of the largest for every value,
+// lost both, and took as long).
 __device__ __forceinline__ void pack16(const float (&v)[16], u32x4 (&w)[2], int& ex) {
-  const unsigned top = group_top(v);
-  const bool bad = top >= 0x7f800000u;
-  const int e = max((int)(top >> 23) - 140, -126);
-  const float inv = bad ? 0.f : __uint_as_float((unsigned)(127 - e) << 23);
+  // without the sign, and one up in the exponent: infinities and NaNs wrap to the bottom
+  unsigned top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, (__float_as_uint(v[i]) << 1) + 0x01000000u);
+  const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+  const int e = max((int)(max(both[0], both[1]) >> 24) - 142, -126);
+  const float inv = __uint_as_float((unsigned)(127 - e) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const unsigned lo = __float_as_uint(fmaf(v[2 * i], inv, 12582912.f)), hi = __float_as_uint(fmaf(v[2 * i + 1], inv, 12582912.f));
-    w[i / 4][i % 4] = __builtin_amdgcn_perm(hi, lo, 0x05040100);   // both lower halves
+    const h16x2 h = {(_Float16)(v[2 * i] * inv), (_Float16)(v[2 * i + 1] * inv)};
+    w[i / 4][i % 4] = __builtin_bit_cast(unsigned, h);
   }
-  ex = bad ? kBadGroup : e;
+  ex = e;
 }
 __device__ __forceinline__ void unpack16(const u32x4 (&w)[2], int ex, float (&v)[16]) {
-  const float s = ex == kBadGroup ? __uint_as_float(0x7fc00000u) : __uint_as_float((unsigned)(127 + ex) << 23);
+  const float s = __uint_as_float((unsigned)(127 + ex) << 23);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = (float)(int16_t)(w[i / 8][i / 2 % 4] >> (16 * (i & 1))) * s;
+  for (int i = 0; i < 8; ++i) {
+    const unsigned both = w[i / 4][i % 4];   // (a copy: a cast of the vector's element itself takes its first one)
+    const h16x2 h = __builtin_bit_cast(h16x2, both);
+    v[2 * i] = (float)h.x * s;
+    v[2 * i + 1] = (float)h.y * s;
+  }
 }
 
 // One of the two saved tensors' tile: 1 (8 bits), 2 (16 bits) or 4 (fp32)
