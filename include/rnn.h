@@ -404,7 +404,8 @@ rnn_status_t rnn_scan_workspace_size(int T, int B, int H, int dirs, size_t* byte
 rnn_status_t rnn_scan_step(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int B, int H, const void* g,
                            const float* h, void* y, float* hy);
 
-/* All steps.  h0 NULL: zeros; hy NULL: not wanted.  The workspace then holds
+/* All steps.  h0 NULL: zeros; hy NULL: not wanted; hy may be h0 itself (a
+ * state carried from piece to piece).  The workspace then holds
  * what rnn_scan_backward reads.  The time axis is split among workgroups that
  * pass the state on; a workgroup whose bounded wait for the state expires
  * sets the workspace's first 32-bit word (0 after a pass in which none did)
@@ -416,7 +417,7 @@ rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wt
 /* Gradients of a forward call with the same mode, sizes, g, h0, lengths and
  * workspace (which may have been followed by other backward calls, but by no
  * other forward call).  dy [T, B, dirs * H]; dhy [dirs, B, H] fp32 or NULL
- * (zeros); dg as g; dh0 as h0 or NULL. */
+ * (zeros); dg as g; dh0 as h0 or NULL, and may be dhy itself. */
 rnn_status_t rnn_scan_backward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
                                const void* g, const float* h0, const int* lengths, const void* dy, const float* dhy,
                                void* dg, float* dh0, void* ws, size_t ws_bytes);

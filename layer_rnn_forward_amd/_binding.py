@@ -437,7 +437,8 @@ def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
     [T, B, dirs*2*H] (for each direction H columns p, then H columns q):
     "gated" a = sigmoid(p), b = sigmoid(-p) tanh(q); "linear" a = p, b = q.
     ``y`` [T, B, dirs*H]; ``hy`` [dirs, B, H] float32 (its shape gives dirs
-    and H); ``h0`` as hy, or None (zeros); ``lengths`` int32 [B] or None."""
+    and H); ``h0`` as hy (it may be the same tensor), or None (zeros);
+    ``lengths`` int32 [B] or None."""
     status = (_CALL or _entries()).scan_forward(mode, g, h0, lengths, y, hy, ws)
     if status == 0 or _done(status, "rnn_scan_forward"):
         return
@@ -460,7 +461,8 @@ def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
 def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
     """Gradients of the rnn_scan_forward call that filled ``ws`` (same mode, g,
     h0 and lengths): ``dy`` [T, B, dirs*H], ``dhy`` as hy or None (zeros);
-    ``dg`` as g, ``dh0`` [dirs, B, H] float32 (its shape gives dirs and H)."""
+    ``dg`` as g, ``dh0`` [dirs, B, H] float32 (its shape gives dirs and H; it
+    may be the same tensor as dhy)."""
     status = (_CALL or _entries()).scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws)
     if status == 0 or _done(status, "rnn_scan_backward"):
         return

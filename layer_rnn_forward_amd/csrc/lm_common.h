@@ -39,7 +39,7 @@ struct ScanParams {
   unsigned* head;
   unsigned* counters;        // [ceil(B * H / 64)][D][16]
   unsigned long long* maps;  // [chunks][D][B][H]
-  float* state;              // [chunks / group + 1][D][B][H]
+  float* state;              // [chunks / group + 1][D][B][H], from the caller's first on
   float* starts;             // [ceil(T / kScanKeep)][D][B][H]
 };
 

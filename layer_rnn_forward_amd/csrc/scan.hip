@@ -7,7 +7,8 @@
 // bits, so the gates are read once; the waves of a workgroup hold consecutive
 // pieces of one chunk.  Each wave composes its piece, the first wave the
 // chunk; it publishes the chunk's (A, B), waits for what precedes it, and the
-// waves then walk their pieces from the true state.
+// waves then walk their pieces from the true state.  (The caller's first state
+// is read by the launch before, or by the only chunk.)
 //
 // What precedes a chunk is the state before its group of SUPER chunks,
 // followed by the maps of the group's chunks before it.  Every chunk composes
@@ -138,12 +139,20 @@ __global__ __launch_bounds__(256) void step_kernel(int B, int H, const void* gv,
   hy[i] = v;
 }
 
-// counters to zero, published words to kUnset, 16 bytes a lane
-__global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long counters, long long all) {
+// counters to zero, published words to kUnset, 16 bytes a lane; the first of
+// the states (words at .. at + C from the maps on) to the caller's, which the
+// last chunk may then overwrite (hy the same tensor as h0, dh0 as dhy)
+__global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long counters, long long all, long long at, long long C,
+                                                    const float* first) {
   if (blockIdx.x == 0 && threadIdx.x == 0) head[0] = 0;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
     const unsigned v = i < counters ? 0u : kUnset;
-    reinterpret_cast<uint4*>(head + 64)[i] = make_uint4(v, v, v, v);
+    unsigned w[4] = {v, v, v, v};
+    const long long c = (i - counters) * 4 - at;
+    if (c > -4 && c < C)
+      for (int k = 0; k < 4; ++k)
+        if (c + k >= 0 && c + k < C) w[k] = first ? word(first[c + k]) : 0u;
+    reinterpret_cast<uint4*>(head + 64)[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -266,7 +275,8 @@ __device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, 
 #pragma unroll
       for (int e = 0; e < VW; ++e) publish2(p.maps + (long long)pos * C + c + e, tA[e], tB[e]);
 #pragma unroll
-    for (int e = 0; e < VW; ++e) h[e] = first && live ? first[c + e] : 0.f;
+    for (int e = 0; e < VW; ++e)
+      h[e] = !live ? 0.f : p.chunks > 1 ? __uint_as_float(peek(p.state + c + e)) : first ? first[c + e] : 0.f;
     if (pos > 0) wait_state<VW, SUPER>(p, pos, C, c, live, h);
     perturb_pause(wave_tag(), pos, 5u);
     if (more && ends && live)
@@ -559,7 +569,7 @@ hipError_t launch(const ScanParams& p, int mode, int bf16, hipStream_t s) {
     const long long words = (long long)(p.chunks * 2 + p.chunks / (BACK ? kScanBwdSuper : kScanFwdSuper) + 1) * C;
     const long long counters = ((char*)p.maps - (char*)p.counters) / 16, all = counters + (words + 3) / 4;
     const dim3 grid((unsigned)std::min<long long>((all + 255) / 256, 2048));
-    hipLaunchKernelGGL(clear_kernel, grid, dim3(256), 0, s, p.head, counters, all);
+    hipLaunchKernelGGL(clear_kernel, grid, dim3(256), 0, s, p.head, counters, all, 2LL * p.chunks * C, C, BACK ? p.dhy : p.h0);
   }
   const dim3 grid((unsigned)(tiles * p.chunks)), block(64 * p.waves);
   if (bf16 && mode == SCAN_GATED) start<BACK, true, SCAN_GATED>(p, two, grid, block, s);
