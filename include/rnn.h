@@ -388,10 +388,12 @@ rnn_status_t rnn_profile_read(rnn_handle_t h, int kernel, long long* launches, d
  * q; y [T, B, dirs * H]; h0, hy [dirs, B, H] fp32.  Direction 1 walks from the
  * last step to the first.  `lengths` (device, int32 [B], or NULL) as in
  * rnn_set_sequence_lengths: past a row's length the state is carried, y is 0,
- * and g is not used (whatever it holds).  Steps are composed in pieces
- * (h = A h_before + B): with RNN_SCAN_LINEAR and |a| > 1 a state that is not
- * zero becomes infinite where the product of a over up to 1024 steps in a row
- * leaves fp32's range, also where the state itself would not. */
+ * and g is not used (whatever it holds).  Any finite a is allowed: states and
+ * gradients are those of the steps one after the other, within fp32 roundings
+ * of the terms they are sums of.  (Steps are composed in pieces; where the
+ * products of a leave fp32's range, which takes |a| > 1, or have become so
+ * small that it counts, the pieces are walked one after the other, which takes
+ * up to six times as long.) */
 typedef enum RNN_ENUM_BASE { RNN_SCAN_GATED = 0, RNN_SCAN_LINEAR = 1 } rnn_scan_mode_t;
 
 /* Bytes of the workspace of one forward call and the backward calls that

@@ -58,7 +58,7 @@ ScanPlan scan_plan(int T, int B, int H, int dirs) {
   scan_split(T, kScanFwdSteps, kScanFwdWaves, p.fwaves, p.fchunks);
   scan_split(T, kScanBwdSteps, kScanBwdWaves, p.bwaves, p.bchunks);
   const size_t C = (size_t)B * H * dirs;
-  auto words = [](int chunks, int super) { return chunks > 1 ? 2 * (size_t)chunks + chunks / super + 1 : 0; };
+  auto words = [](int chunks, int super) { return chunks > 1 ? 3 * (size_t)chunks + chunks / super + 1 : 0; };
   const size_t most = std::max(words(p.fchunks, kScanFwdSuper), words(p.bchunks, kScanBwdSuper));
   p.maps = kAlign + (most ? align_up(((size_t)B * H + 63) / 64 * dirs * 64) : 0);
   p.starts = p.maps + align_up(most * C * 4);
@@ -74,7 +74,9 @@ void scan_room(ScanParams& p, bool back, void* ws) {
   p.counters = at<unsigned>(ws, kAlign);
   p.starts = at<float>(ws, q.starts);
   p.maps = at<unsigned long long>(ws, q.maps);
-  p.state = reinterpret_cast<float*>(p.maps + (size_t)p.chunks * p.B * p.H * p.D);
+  const size_t C = (size_t)p.B * p.H * p.D;
+  p.state = reinterpret_cast<float*>(p.maps + p.chunks * C);
+  p.ends = p.state + (p.chunks / (back ? kScanBwdSuper : kScanFwdSuper) + 1) * C;
 }
 
 // -------------------------------------------------------------------- ffn

@@ -33,13 +33,14 @@ struct ScanParams {
   float* dh0;            // backward, or null
   int waves, chunks;     // chunks of `waves` pieces
   // workspace, in this order: [0] a wait expired (256 bytes); started chunks
-  // of each workgroup's channels, 64 bytes apart; the chunks' maps (A, B) and
-  // the states before every group of chunks, contiguous; the state before
-  // every kScanKeep-th step
+  // of each workgroup's channels, 64 bytes apart; the chunks' maps (A, B), the
+  // states before every group of chunks and the states after chunks that had
+  // to be walked, contiguous; the state before every kScanKeep-th step
   unsigned* head;
   unsigned* counters;        // [ceil(B * H / 64)][D][16]
   unsigned long long* maps;  // [chunks][D][B][H]
   float* state;              // [chunks / group + 1][D][B][H], from the caller's first on
+  float* ends;               // [chunks][D][B][H]
   float* starts;             // [ceil(T / kScanKeep)][D][B][H]
 };
 

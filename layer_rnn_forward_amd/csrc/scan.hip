@@ -7,8 +7,8 @@
 // bits, so the gates are read once; the waves of a workgroup hold consecutive
 // pieces of one chunk.  Each wave composes its piece, the first wave the
 // chunk; it publishes the chunk's (A, B), waits for what precedes it, and the
-// waves then walk their pieces from the true state.  (The caller's first state
-// is read by the launch before, or by the only chunk.)
+// waves then walk their pieces from the true state.  Only the first chunk reads
+// the caller's state, and publishes it: the last may write over it.
 //
 // What precedes a chunk is the state before its group of SUPER chunks,
 // followed by the maps of the group's chunks before it.  Every chunk composes
@@ -18,6 +18,15 @@
 // instead of N.  A workgroup takes its chunk from its channels' counter, in
 // walking order, so everything a chunk waits for is done or running (one
 // counter for all workgroups cost 20 % of a pass over 2048 steps).
+//
+// A map can leave fp32's range although no state does: linear steps with
+// |a| > 1, or a small product that a large state makes count.  Maps mark the
+// first (A is NaN); strays() finds the second from the state that the map is
+// applied to.  Such a chunk is walked piece after piece from its state, for the
+// channels that need it; a chunk whose map is not clean (no number, or small)
+// also publishes the state after it, for those that cannot use the map.  (The
+// checks cost 2 - 3 % of a pass that needs none of it; 2048 steps of 8 rows of
+// 1024 that grow and are reset: forward 0.076, backward 0.126 ms.)
 //
 // Published words are their own flags: a kernel sets them beforehand to a
 // pattern that no published value has (kUnset, a NaN pattern replaced by
@@ -34,8 +43,8 @@
 // 39 and 59 issue slots of vector work (exponentials and reciprocals count
 // four), which is 0.5 to 0.8 of the memory's time; waves that wait for each
 // other leave the two overlapped in part.  65536 steps of 1760 channels in
-// bf16: forward 0.22 ms, backward 0.35 ms (3.3 and 3.5 TB/s); 2048 steps of 8
-// rows of 1024: 0.030 and 0.042 ms.  One thread per channel that walks every
+// bf16: forward 0.21 ms, backward 0.34 ms (3.4 and 3.6 TB/s); 2048 steps of 8
+// rows of 1024: 0.031 and 0.042 ms.  One thread per channel that walks every
 // step took 96 ms and 2.7 ms for both passes.  Measured against the split
 // used (forward 16 steps x 8 waves in groups of 8, backward 8 x 8 in groups
 // of 4; forward / backward ms of the long case): 4 waves 0.24 / 0.37, 8 steps
@@ -108,9 +117,17 @@ __device__ __forceinline__ void coeffs(float p, float q, float& a, float& na, fl
   }
 }
 
-// A h + B; a state of exactly zero stays out of the product, so that an A
-// which overflowed (linear steps with |a| > 1) does not turn it into NaN
-__device__ __forceinline__ float apply(float A, float h, float B) { return h == 0.f ? B : fmaf(A, h, B); }
+// A map (A, B) stands for the steps it was composed from unless A or B left
+// fp32's range (steps with |a| > 1; A is then NaN), or what an A near the
+// bottom of the range has lost, up to 2^-142, times h would count in
+// r = A h + B.
+__device__ __forceinline__ bool clean(float A) { return fabsf(A) >= 0x1p-102f; }
+__device__ __forceinline__ bool strays(float h, float r) { return !(fabsf(r) >= fabsf(h) * 0x1p-118f); }
+// `low`: the smallest product on the way, `grew`: whether a coefficient was
+// above 1; growth after such a loss carries it further
+__device__ __forceinline__ float mark(float A, float B, bool grew, float low) {
+  return __builtin_isfinite(A) && __builtin_isfinite(B) && !(grew && low < 0x1p-102f) ? A : __uint_as_float(0x7fc00000u);
+}
 
 __device__ __forceinline__ unsigned word(float v) {
   const unsigned u = __float_as_uint(v);
@@ -139,20 +156,12 @@ __global__ __launch_bounds__(256) void step_kernel(int B, int H, const void* gv,
   hy[i] = v;
 }
 
-// counters to zero, published words to kUnset, 16 bytes a lane; the first of
-// the states (words at .. at + C from the maps on) to the caller's, which the
-// last chunk may then overwrite (hy the same tensor as h0, dh0 as dhy)
-__global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long counters, long long all, long long at, long long C,
-                                                    const float* first) {
+// counters to zero, published words to kUnset, 16 bytes a lane
+__global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long counters, long long all) {
   if (blockIdx.x == 0 && threadIdx.x == 0) head[0] = 0;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
     const unsigned v = i < counters ? 0u : kUnset;
-    unsigned w[4] = {v, v, v, v};
-    const long long c = (i - counters) * 4 - at;
-    if (c > -4 && c < C)
-      for (int k = 0; k < 4; ++k)
-        if (c + k >= 0 && c + k < C) w[k] = first ? word(first[c + k]) : 0u;
-    reinterpret_cast<uint4*>(head + 64)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(head + 64)[i] = make_uint4(v, v, v, v);
   }
 }
 
@@ -184,17 +193,19 @@ __device__ __forceinline__ void wait_words(const ScanParams& p, int count, Word 
 }
 
 // The state that chunk `pos` (in walking order) starts from: the wave's VW
-// channels at `c` of `C`.  h holds the sequence's first state.  The maps since
-// the last published state are composed first, then that state is waited for.
-template <int VW, int SUPER>
-__device__ void wait_state(const ScanParams& p, int pos, long long C, long long c, bool live, float (&h)[VW]) {
+// channels at `c` of `C`.  The maps since the last published state are composed
+// (A, B) first, then that state (s) is waited for.
+template <int MODE, int VW, int SUPER>
+__device__ __forceinline__ void wait_state(const ScanParams& p, int pos, long long C, long long c, bool live, float (&A)[VW],
+                                           float (&B)[VW], float (&s)[VW]) {
   const int sup = pos / SUPER, n = pos - sup * SUPER;
   constexpr int N = 4;
-  float A[VW], B[VW];
+  float low[VW];
+  bool grew[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    A[e] = 1.f;
-    B[e] = 0.f;
+    low[e] = 1.f;
+    grew[e] = false;
   }
   for (int j0 = 0; j0 < n; j0 += N) {
     unsigned long long m[N][VW];
@@ -208,17 +219,47 @@ __device__ void wait_state(const ScanParams& p, int pos, long long C, long long 
         for (int e = 0; e < VW; ++e) {
           const float a = __uint_as_float((unsigned)m[j][e]);
           A[e] *= a;
-          B[e] = apply(a, B[e], __uint_as_float((unsigned)(m[j][e] >> 32)));
+          B[e] = fmaf(a, B[e], __uint_as_float((unsigned)(m[j][e] >> 32)));
+          if constexpr (MODE == SCAN_LINEAR) {
+            grew[e] |= fabsf(a) > 1.f;
+            low[e] = fminf(low[e], fabsf(A[e]));
+          }
         }
   }
-  if (sup > 0) {
+#pragma unroll
+  for (int e = 0; e < VW; ++e) A[e] = mark(A[e], B[e], grew[e], low[e]);
+  unsigned u[1][VW];
+  wait_words<1, VW>(p, 1, u, [&](int, int e) { return live ? peek(p.state + (long long)sup * C + c + e) : 0u; });
+#pragma unroll
+  for (int e = 0; e < VW; ++e) s[e] = __uint_as_float(u[0][e]);
+}
+
+// For the channels `again`, whose composed maps stray: the chunks' maps once
+// more, one after the other from the group's first state; a chunk whose map is
+// not clean publishes the state after it, too.
+template <int VW, int SUPER>
+__device__ __forceinline__ void step_by_step(const ScanParams& p, int pos, long long C, long long c, const bool (&again)[VW],
+                                             float (&h)[VW]) {
+  const int sup = pos / SUPER, n = pos - sup * SUPER;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const long long at = (long long)(sup * SUPER + j) * C + c;
+    bool wait[VW], any = false;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      const unsigned long long m = again[e] ? peek2(p.maps + at + e) : 0ull;
+      const float A = __uint_as_float((unsigned)m);
+      wait[e] = again[e] && !clean(A);
+      if (again[e]) h[e] = fmaf(A, h[e], __uint_as_float((unsigned)(m >> 32)));
+      any |= wait[e];
+    }
+    if (!__any(any)) continue;
     unsigned u[1][VW];
-    wait_words<1, VW>(p, 1, u, [&](int, int e) { return live ? peek(p.state + (long long)sup * C + c + e) : 0u; });
+    wait_words<1, VW>(p, 1, u, [&](int, int e) { return wait[e] ? peek(p.ends + at + e) : 0u; });
 #pragma unroll
-    for (int e = 0; e < VW; ++e) h[e] = __uint_as_float(u[0][e]);
+    for (int e = 0; e < VW; ++e)
+      if (wait[e]) h[e] = __uint_as_float(u[0][e]);
   }
-#pragma unroll
-  for (int e = 0; e < VW; ++e) h[e] = apply(A[e], h[e], B[e]);
 }
 
 // The chunk and channels of a workgroup.
@@ -243,54 +284,170 @@ __device__ __forceinline__ Place place(const ScanParams& p, int VW, unsigned& sh
   return r;
 }
 
+// LDS of a workgroup's exchange: the waves' maps and whether one could stray,
+// the state before the chunk (and, where the pieces are walked one after the
+// other, before and after each), the lanes that need that
+template <int VW, int MW>
+struct Exchange {
+  float A[MW][64 * VW], B[MW][64 * VW], h[MW + 1][64 * VW];
+  unsigned risk[MW], any;
+  unsigned long long slow[VW], out[VW];
+};
+
 // compose the waves' maps to the chunk's, find the state before the chunk,
-// pass it on; returns the state before this wave's piece
-template <int VW, int SUPER, int MW>
+// pass it on; returns the state before this wave's piece.  end(x): the state x
+// before this wave's piece becomes the one after it.
+template <int MODE, int VW, int SUPER, int MW, class End>
 __device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, long long c, bool live, const float* first,
-                                     int wave, int lane, int W, float (&sA)[MW][64 * VW], float (&sB)[MW][64 * VW],
-                                     float (&sh)[64 * VW], const float (&A)[VW], const float (&B)[VW], float (&h)[VW]) {
+                                     int wave, int lane, int W, Exchange<VW, MW>& x, const float (&A)[VW], const float (&B)[VW],
+                                     float (&h)[VW], End end) {
+  bool small = false;
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    sA[wave][lane * VW + e] = A[e];
-    sB[wave][lane * VW + e] = B[e];
+    x.A[wave][lane * VW + e] = A[e];
+    x.B[wave][lane * VW + e] = B[e];
+    small |= live && !clean(A[e]);
   }
+  const bool risk = __any(small);
+  if (lane == 0) x.risk[wave] = risk;
   __syncthreads();
+  const bool ends = pos % SUPER == SUPER - 1, more = pos + 1 < p.chunks;
   if (wave == 0) {
-    float tA[VW], tB[VW];
+    float tA[VW], tB[VW], low[VW];
+    bool grew[VW];
+    const bool look = __any(lane < W && x.risk[lane & (MW - 1)]);
 #pragma unroll
     for (int e = 0; e < VW; ++e) {
       tA[e] = A[e];
       tB[e] = B[e];
+      low[e] = fabsf(A[e]);
+      grew[e] = low[e] > 1.f;
     }
     for (int w = 1; w < W; ++w)
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        const float a = sA[w][lane * VW + e];
+        const float a = x.A[w][lane * VW + e];
         tA[e] *= a;
-        tB[e] = apply(a, tB[e], sB[w][lane * VW + e]);
+        tB[e] = fmaf(a, tB[e], x.B[w][lane * VW + e]);
+        if constexpr (MODE == SCAN_LINEAR) {
+          grew[e] |= fabsf(a) > 1.f;
+          low[e] = fminf(low[e], fabsf(tA[e]));
+        }
       }
-    const bool ends = pos % SUPER == SUPER - 1, more = pos + 1 < p.chunks;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) tA[e] = mark(tA[e], tB[e], MODE == SCAN_LINEAR && grew[e], low[e]);
     perturb_pause(wave_tag(), pos, 4u);
     if (more && !ends && live)
 #pragma unroll
       for (int e = 0; e < VW; ++e) publish2(p.maps + (long long)pos * C + c + e, tA[e], tB[e]);
+    float gA[VW], gB[VW], s[VW], r[VW];
+    bool unclean[VW], dirty = false;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      unclean[e] = live && more && !clean(tA[e]);
+      dirty |= unclean[e];
+      gA[e] = 1.f;
+      gB[e] = 0.f;
+      s[e] = 0.f;
+    }
+    if (pos == 0) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        if (first && live) s[e] = first[c + e];
+        if (more && live) publish(p.state + c + e, s[e]);
+      }
+    }
+    dirty = __any(dirty);
+    if (pos > 0) wait_state<MODE, VW, SUPER>(p, pos, C, c, live, gA, gB, s);
+    perturb_pause(wave_tag(), pos, 5u);
+    float* const next = (ends ? p.state + (long long)(pos / SUPER + 1) * C : p.ends + (long long)pos * C) + c;
+    bool again[VW], out[VW] = {}, any = false;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      h[e] = fmaf(gA[e], s[e], gB[e]);
+      r[e] = fmaf(tA[e], h[e], tB[e]);
+      again[e] = live && strays(s[e], h[e]);
+      any |= again[e];
+    }
+    if (dirty) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) out[e] = unclean[e] && strays(h[e], r[e]);
+    }
+    // both channels' before the stores: a wait for the second's word among them would be one for the first's store
+    if constexpr (VW == 2) asm volatile("" : "+v"(r[0]), "+v"(r[VW - 1]));
 #pragma unroll
     for (int e = 0; e < VW; ++e)
-      h[e] = !live ? 0.f : p.chunks > 1 ? __uint_as_float(peek(p.state + c + e)) : first ? first[c + e] : 0.f;
-    if (pos > 0) wait_state<VW, SUPER>(p, pos, C, c, live, h);
-    perturb_pause(wave_tag(), pos, 5u);
-    if (more && ends && live)
+      if (more && live && (ends || unclean[e]) && !again[e] && !out[e]) publish(next + e, r[e]);
+    if (__builtin_expect(__any(any), 0)) {
 #pragma unroll
-      for (int e = 0; e < VW; ++e) publish(p.state + (long long)(pos / SUPER + 1) * C + c + e, apply(tA[e], h[e], tB[e]));
+      for (int e = 0; e < VW; ++e)
+        if (again[e]) h[e] = s[e];
+      step_by_step<VW, SUPER>(p, pos, C, c, again, h);
 #pragma unroll
-    for (int e = 0; e < VW; ++e) sh[lane * VW + e] = h[e];
+      for (int e = 0; e < VW; ++e)
+        if (again[e]) {
+          r[e] = fmaf(tA[e], h[e], tB[e]);
+          out[e] = unclean[e] && strays(h[e], r[e]);
+          if (more && (ends || unclean[e]) && !out[e]) publish(next + e, r[e]);
+        }
+    }
+    any = false;
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      x.h[0][lane * VW + e] = h[e];
+      any |= out[e];
+    }
+    const bool slow = look || __any(any);
+    if (lane == 0) x.any = slow;
+    if (__builtin_expect(slow, 0)) {
+      any = false;
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        float v = h[e];
+        bool walk = out[e];
+#pragma unroll 1
+        for (int w = 0; w < W - 1; ++w) {
+          const float to = fmaf(x.A[w][lane * VW + e], v, x.B[w][lane * VW + e]);
+          walk |= live && strays(v, to);
+          v = to;
+        }
+        const unsigned long long mw = __ballot(walk), mo = __ballot(out[e]);
+        any |= mw != 0;
+        if (lane == 0) {
+          x.slow[e] = mw;
+          x.out[e] = mo;
+        }
+      }
+      if (lane == 0) x.any = any;
+    }
   }
   __syncthreads();
+  const bool slow = x.any != 0;   // the same for every wave
 #pragma unroll
-  for (int e = 0; e < VW; ++e) h[e] = sh[lane * VW + e];
+  for (int e = 0; e < VW; ++e) h[e] = x.h[0][lane * VW + e];
   for (int w = 0; w < wave; ++w)
 #pragma unroll
-    for (int e = 0; e < VW; ++e) h[e] = apply(sA[w][lane * VW + e], h[e], sB[w][lane * VW + e]);
+    for (int e = 0; e < VW; ++e) h[e] = fmaf(x.A[w][lane * VW + e], h[e], x.B[w][lane * VW + e]);
+  if (__builtin_expect(!slow, 1)) return;
+#pragma unroll 1
+  for (int w = 0; w < W; ++w) {
+    if (w == wave) {
+      float s[VW];
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        s[e] = x.h[w][lane * VW + e];
+        if (x.slow[e] >> lane & 1) h[e] = s[e];
+      }
+      end(s);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        x.h[w + 1][lane * VW + e] = s[e];
+        if (w == W - 1 && x.out[e] >> lane & 1)
+          publish((ends ? p.state + (long long)(pos / SUPER + 1) * C : p.ends + (long long)pos * C) + c + e, s[e]);
+      }
+    }
+    __syncthreads();
+  }
 }
 
 // Where a lane's values lie in a step's row: the elements up to the
@@ -324,12 +481,30 @@ __device__ __forceinline__ T ld(const char* row, unsigned off) { return *reinter
 template <class T>
 __device__ __forceinline__ void st(char* row, unsigned off, T v) { *reinterpret_cast<T*>(row + off) = v; }
 
+// mark() of a wave's map; whether a coefficient was above 1 is looked up only
+// where a product came out small
+template <int MODE, int G, int VW>
+__device__ __forceinline__ void mark_piece(const float (&a)[G][VW], const float (&B)[VW], const float (&low)[VW], float (&A)[VW]) {
+  bool grew[VW] = {}, small = false;
+  if constexpr (MODE == SCAN_LINEAR) {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) small |= low[e] < 0x1p-102f;
+    if (__builtin_expect(__any(small), 0))
+#pragma unroll
+      for (int s = 0; s < G; ++s)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) grew[e] |= fabsf(a[s][e]) > 1.f;
+  }
+#pragma unroll
+  for (int e = 0; e < VW; ++e) A[e] = mark(A[e], B[e], grew[e], low[e]);
+}
+
 template <bool BF, int MODE, int VW>
 __global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(const ScanParams p) {
   using V = Vec<BF, VW>;
   using T = typename V::T;
   constexpr int ES = BF ? 2 : 4, G = kScanFwdSteps;
-  __shared__ float sA[kScanFwdWaves][64 * VW], sB[kScanFwdWaves][64 * VW], sh[64 * VW];
+  __shared__ Exchange<VW, kScanFwdWaves> x;
   __shared__ unsigned shared;
   const Place at = place(p, VW, shared);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
@@ -354,10 +529,10 @@ __global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(con
     rp[s] = ld<T>(row, l.g);
     rq[s] = ld<T>(row + half, l.g);
   }
-  float a[G][VW], b[G][VW], A[VW], B[VW], h[VW];
+  float a[G][VW], b[G][VW], A[VW], B[VW], h[VW], low[VW];
 #pragma unroll
   for (int e = 0; e < VW; ++e) {
-    A[e] = 1.f;
+    A[e] = low[e] = 1.f;
     B[e] = 0.f;
   }
   // WHOLE: every step of the piece belongs to every row; otherwise steps past
@@ -379,12 +554,19 @@ __global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(con
         if (!valid) a[s][e] = 1.f;
         A[e] *= a[s][e];
         B[e] = fmaf(a[s][e], B[e], b[s][e]);
+        if constexpr (MODE == SCAN_LINEAR) low[e] = fminf(low[e], fabsf(A[e]));
       }
     }
   };
   if (whole) compose(std::true_type{});
   else compose(std::false_type{});
-  join<VW, kScanFwdSuper, kScanFwdWaves>(p, at.pos, C, c, l.live, p.h0, wave, lane, W, sA, sB, sh, A, B, h);
+  mark_piece<MODE>(a, B, low, A);
+  join<MODE, VW, kScanFwdSuper, kScanFwdWaves>(p, at.pos, C, c, l.live, p.h0, wave, lane, W, x, A, B, h, [&](float (&s)[VW]) {
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+#pragma unroll
+      for (int e = 0; e < VW; ++e) s[e] = fmaf(a[i][e], s[e], b[i][e]);
+  });
   if (!l.live) return;
   auto walk = [&](auto w) {
     constexpr bool WHOLE = decltype(w)::value;
@@ -417,7 +599,7 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
   using V = Vec<BF, VW>;
   using T = typename V::T;
   constexpr int ES = BF ? 2 : 4, G = kScanBwdSteps;
-  __shared__ float sA[kScanBwdWaves][64 * VW], sB[kScanBwdWaves][64 * VW], sh[64 * VW];
+  __shared__ Exchange<VW, kScanBwdWaves> x;
   __shared__ unsigned shared;
   const Place at = place(p, VW, shared);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
@@ -449,7 +631,7 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
     rd[s] = ld<T>(dy + t * yrow, l.y);
   }
   // a, dp = f (dy + D), dq = f2 (dy + D)
-  float a[G][VW], f[G][VW], f2[G][VW], A[VW], B[VW], D[VW];
+  float a[G][VW], f[G][VW], f2[G][VW], A[VW], B[VW], D[VW], low[VW];
   auto compose = [&](auto w) {
     constexpr bool WHOLE = decltype(w)::value;
 #pragma unroll
@@ -485,6 +667,7 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
     for (int e = 0; e < VW; ++e) {
       A[e] = a[G - 1][e];
       B[e] = 0.f;
+      low[e] = fabsf(A[e]);
     }
     // B: dy + D of the step, D of nothing being 0
     V::get(rd[G - 1], B);
@@ -496,6 +679,7 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
       for (int e = 0; e < VW; ++e) {
         A[e] *= a[s][e];
         B[e] = fmaf(a[s + 1][e], B[e], v[e]);
+        if constexpr (MODE == SCAN_LINEAR) low[e] = fminf(low[e], fabsf(A[e]));
       }
     }
 #pragma unroll
@@ -503,7 +687,18 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
   };
   if (whole) compose(std::true_type{});
   else compose(std::false_type{});
-  join<VW, kScanBwdSuper, kScanBwdWaves>(p, at.pos, C, c, l.live, p.dhy, wave, lane, W, sA, sB, sh, A, B, D);
+  mark_piece<MODE>(a, B, low, A);
+  join<MODE, VW, kScanBwdSuper, kScanBwdWaves>(p, at.pos, C, c, l.live, p.dhy, wave, lane, W, x, A, B, D, [&](float (&s)[VW]) {
+#pragma unroll
+    for (int i = G - 1; i >= 0; --i) {
+      float v[VW];
+      V::get(rd[i], v);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) s[e] = i == G - 1 ? s[e] + v[e] : fmaf(a[i == G - 1 ? i : i + 1][e], s[e], v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < VW; ++e) s[e] *= a[0][e];
+  });
   if (!l.live) return;
   auto walk = [&](auto w) {
     constexpr bool WHOLE = decltype(w)::value;
@@ -566,10 +761,10 @@ hipError_t launch(const ScanParams& p, int mode, int bf16, hipStream_t s) {
   const long long BH = (long long)p.B * p.H, tiles = (BH + (two ? 127 : 63)) / (two ? 128 : 64) * p.D;
   if (tiles * p.chunks > 0x7fffffffLL) return hipErrorInvalidValue;
   if (p.chunks > 1) {
-    const long long words = (long long)(p.chunks * 2 + p.chunks / (BACK ? kScanBwdSuper : kScanFwdSuper) + 1) * C;
+    const long long words = (3LL * p.chunks + p.chunks / (BACK ? kScanBwdSuper : kScanFwdSuper) + 1) * C;
     const long long counters = ((char*)p.maps - (char*)p.counters) / 16, all = counters + (words + 3) / 4;
     const dim3 grid((unsigned)std::min<long long>((all + 255) / 256, 2048));
-    hipLaunchKernelGGL(clear_kernel, grid, dim3(256), 0, s, p.head, counters, all, 2LL * p.chunks * C, C, BACK ? p.dhy : p.h0);
+    hipLaunchKernelGGL(clear_kernel, grid, dim3(256), 0, s, p.head, counters, all);
   }
   const dim3 grid((unsigned)(tiles * p.chunks)), block(64 * p.waves);
   if (bf16 && mode == SCAN_GATED) start<BACK, true, SCAN_GATED>(p, two, grid, block, s);
