@@ -90,30 +90,33 @@ struct Vec {
   }
 };
 
-// a, 1 - a and the candidate n of a gated step.  1 - a from the same
-// exponential (no cancellation); tanh from one exponential of -2|q|, and from
-// its series q - q^3/3 + 2q^5/15 below 1/16, where 1 - e^(-2|q|) would cancel
-// (both are within 12 units in the last place).
-__device__ __forceinline__ void gate(float p, float q, float& a, float& na, float& n) {
+// a, 1 - a, the candidate n of a gated step and its slope 1 - n^2.  1 - a from
+// the same exponential (no cancellation); tanh from one exponential
+// t = e^(-2|q|), and from its series q - q^3/3 + 2q^5/15 below 1/16, where 1 - t
+// would cancel (both are within 12 units in the last place); the slope as
+// 4 t / (1 + t)^2 (1 - n^2 has lost all its digits at |q| = 9).
+__device__ __forceinline__ void gate(float p, float q, float& a, float& na, float& n, float& slope) {
   const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(p));
   const float x = fabsf(q), t = __builtin_amdgcn_exp2f(-2.8853900817779268f * x);
   const float e1 = 1.f + e, t1 = 1.f + t, r = __builtin_amdgcn_rcpf(e1 * t1);
-  const float big = r * t1, small = e * big;
+  const float big = r * t1, small = e * big, rt = r * e1;
   a = p >= 0.f ? big : small;
   na = p >= 0.f ? small : big;
-  const float far = (1.f - t) * (r * e1);
+  const float far = (1.f - t) * rt;
   const float z = q * q, near = fmaf(x * z, fmaf(z, 2.f / 15.f, -1.f / 3.f), x);
   n = copysignf(x < 0.0625f ? near : far, q);
+  slope = 4.f * t * (rt * rt);
 }
 
 template <int MODE>
-__device__ __forceinline__ void coeffs(float p, float q, float& a, float& na, float& n) {
+__device__ __forceinline__ void coeffs(float p, float q, float& a, float& na, float& n, float& slope) {
   if constexpr (MODE == SCAN_GATED) {
-    gate(p, q, a, na, n);
+    gate(p, q, a, na, n, slope);
   } else {
     a = p;
     na = 1.f;
     n = q;
+    slope = 1.f;
   }
 }
 
@@ -149,8 +152,8 @@ __global__ __launch_bounds__(256) void step_kernel(int B, int H, const void* gv,
   if (i >= (long long)B * H) return;
   const int b = (int)(i / H), u = (int)(i - (long long)b * H);
   const El<BF16>* g = (const El<BF16>*)gv + (long long)b * 2 * H + u;
-  float a, na, n;
-  coeffs<MODE>(el_load<BF16>(g), el_load<BF16>(g + H), a, na, n);
+  float a, na, n, slope;
+  coeffs<MODE>(el_load<BF16>(g), el_load<BF16>(g + H), a, na, n, slope);
   const float v = fmaf(a, h ? h[i] : 0.f, na * n);
   if (yv) el_store<BF16>((El<BF16>*)yv + i, v);
   hy[i] = v;
@@ -548,8 +551,8 @@ __global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(con
       const bool valid = WHOLE || (i < p.T && t < len);
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        float na, n;
-        coeffs<MODE>(vp[e], vq[e], a[s][e], na, n);
+        float na, n, slope;
+        coeffs<MODE>(vp[e], vq[e], a[s][e], na, n, slope);
         b[s][e] = valid ? na * n : 0.f;
         if (!valid) a[s][e] = 1.f;
         A[e] *= a[s][e];
@@ -643,11 +646,11 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
       const bool valid = WHOLE || (i < p.T && t < len);
 #pragma unroll
       for (int e = 0; e < VW; ++e) {
-        float na, n;
-        coeffs<MODE>(vp[e], vq[e], a[s][e], na, n);
+        float na, n, slope;
+        coeffs<MODE>(vp[e], vq[e], a[s][e], na, n, slope);
         if constexpr (MODE == SCAN_GATED) {
           f[s][e] = (h[e] - n) * (a[s][e] * na);
-          f2[s][e] = na * fmaf(-n, n, 1.f);
+          f2[s][e] = na * slope;
         } else {
           f[s][e] = h[e];
           f2[s][e] = 1.f;
