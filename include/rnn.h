@@ -410,8 +410,8 @@ rnn_status_t rnn_scan_step(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype
  * state carried from piece to piece).  The workspace then holds
  * what rnn_scan_backward reads.  The time axis is split among workgroups that
  * pass the state on; a workgroup whose bounded wait for the state expires
- * sets the workspace's first 32-bit word (0 after a pass in which none did)
- * and carries on with NaN, so that every workgroup ends. */
+ * notes that in the workspace and carries on with NaN, so that every workgroup
+ * ends (see rnn_scan_status). */
 rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
                               const void* g, const float* h0, const int* lengths, void* y, float* hy, void* ws,
                               size_t ws_bytes);
@@ -423,6 +423,13 @@ rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wt
 rnn_status_t rnn_scan_backward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
                                const void* g, const float* h0, const int* lengths, const void* dy, const float* dhy,
                                void* dg, float* dh0, void* ws, size_t ws_bytes);
+
+/* Synchronises `stream` and returns RNN_STATUS_DEVICE_TIMEOUT if a bounded wait
+ * of the last forward call on the workspace, or of the last backward call after
+ * it, expired; SUCCESS if none did.  (The workspace's first 32-bit word is not 0
+ * if forward's did, its second if backward's; a forward call clears both, a
+ * backward call its own.  Calls with B or H = 0 leave them alone.) */
+rnn_status_t rnn_scan_status(void* stream, const void* ws, size_t ws_bytes);
 
 /* Gated feed-forward block over M rows:
  *   y = (act(x Wg^T) * (x Wu^T)) w_out^T,   w_in = [Wg; Wu]

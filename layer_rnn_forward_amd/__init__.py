@@ -48,6 +48,7 @@ from ._binding import (  # noqa: F401
     rnn_scan_step,
     rnn_scan_forward,
     rnn_scan_backward,
+    rnn_scan_status,
     rnn_ffn_workspace_size,
     rnn_ffn_reserve_size,
     rnn_ffn_forward,

@@ -74,6 +74,7 @@ def load_library():
         "rnn_scan_step": [vp, i, i, i, i, vp, vp, vp, vp],
         "rnn_scan_forward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, sz],
         "rnn_scan_backward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, sz],
+        "rnn_scan_status": [vp, vp, sz],
         "rnn_ffn_workspace_size": [i, i, i, i, i, psz],
         "rnn_ffn_reserve_size": [i, i, i, i, i, psz],
         "rnn_ffn_forward": [vp, i, i, i, i, i, i, vp, vp, vp, vp, vp, sz, vp, sz],
@@ -481,6 +482,17 @@ def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
         _addr(dg, "dg", dev, dt, (T, B, D * 2 * H)), _addr(dh0, "dh0", dev, torch.float32, st), wp, wn)
     if status:
         _check(status, "rnn_scan_backward")
+
+
+def rnn_scan_status(ws) -> int:
+    """0, or -7 if a bounded device wait of the last rnn_scan_forward on ``ws``,
+    or of the last rnn_scan_backward after it, expired (their results are then
+    NaN); synchronises.  Raises on other errors."""
+    wp, wn = _room(ws, "ws", ws.get_device() if isinstance(ws, torch.Tensor) else -1)
+    s = load_library().rnn_scan_status(_on(ws.get_device()), wp, wn)
+    if s not in (0, STATUS_DEVICE_TIMEOUT):
+        raise RNNError(s, "rnn_scan_status")
+    return s
 
 
 def rnn_ffn_workspace_size(M: int, D: int, F: int, wtype: str, save: str = "none") -> int:

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "ffn_plan.h"
 #include "lm_common.h"
@@ -66,7 +67,15 @@ ScanPlan scan_plan(int T, int B, int H, int dirs) {
   return p;
 }
 
+// Polls of a wait before it expires: some seconds, or RNN_SPIN_LIMIT (as for
+// the recurrent kernels; 0 expires every wait whose words are not there).
+int scan_spin_limit() {
+  const char* v = std::getenv("RNN_SPIN_LIMIT");
+  return v && *v ? std::max(0, std::atoi(v)) : 1 << 22;
+}
+
 void scan_room(ScanParams& p, bool back, void* ws) {
+  p.spin_limit = scan_spin_limit();
   const ScanPlan q = scan_plan(p.T, p.B, p.H, p.D);
   p.waves = back ? q.bwaves : q.fwaves;
   p.chunks = back ? q.bchunks : q.fchunks;
@@ -241,6 +250,15 @@ rnn_status_t rnn_scan_backward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t w
   p.g = g; p.h0 = h0; p.lengths = lengths; p.dy = dy; p.dhy = dhy; p.dg = dg; p.dh0 = dh0;
   scan_room(p, true, ws);
   return dev(rnn_launch_scan_bwd(p, mode, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_scan_status(void* stream, const void* ws, size_t ws_bytes) {
+  if (!ws || !aligned(ws) || ws_bytes < kAlign) return RNN_STATUS_INVALID_ARG;
+  unsigned expired[2] = {};
+  if (hipStreamSynchronize(hs(stream)) != hipSuccess ||
+      hipMemcpy(expired, ws, sizeof(expired), hipMemcpyDeviceToHost) != hipSuccess)
+    return RNN_STATUS_DEVICE;
+  return expired[0] || expired[1] ? RNN_STATUS_DEVICE_TIMEOUT : RNN_STATUS_SUCCESS;
 }
 
 rnn_status_t rnn_ffn_workspace_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes) {

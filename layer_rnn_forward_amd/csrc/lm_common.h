@@ -32,7 +32,9 @@ struct ScanParams {
   void* dg;              // backward
   float* dh0;            // backward, or null
   int waves, chunks;     // chunks of `waves` pieces
-  // workspace, in this order: [0] a wait expired (256 bytes); started chunks
+  int spin_limit;        // polls of a wait before it expires
+  // workspace, in this order: [0], [1] a wait of the forward, of the backward
+  // pass expired (256 bytes); started chunks
   // of each workgroup's channels, 64 bytes apart; the chunks' maps (A, B), the
   // states before every group of chunks and the states after chunks that had
   // to be walked, contiguous; the state before every kScanKeep-th step

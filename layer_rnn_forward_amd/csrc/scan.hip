@@ -31,8 +31,8 @@
 // Published words are their own flags: a kernel sets them beforehand to a
 // pattern that no published value has (kUnset, a NaN pattern replaced by
 // another NaN when a result has it), so a wait costs one round trip.  Waits
-// are bounded; one that expires sets the workspace's first word and carries on
-// with NaN.
+// are bounded; one that expires sets its pass's word at the workspace's start
+// and carries on with NaN.
 //
 // The backward pass is the same recurrence walked the other way
 // (D_(t-1) = a_t (dy_t + D_t)).  It composes the states again from the gates
@@ -67,7 +67,6 @@ using namespace rnnk;
 namespace {
 
 constexpr unsigned kUnset = 0xffffffffu;
-constexpr int kWaitLimit = 1 << 22;
 
 template <bool BF, int VW>
 struct Vec {
@@ -159,9 +158,21 @@ __global__ __launch_bounds__(256) void step_kernel(int B, int H, const void* gv,
   hy[i] = v;
 }
 
+// Words for waits that expired: forward's, then backward's.  A forward pass
+// clears both, a backward pass its own: what forward noted stays to be read
+// after the step.
+template <bool BACK>
+__device__ __forceinline__ void clear_expired(unsigned* head) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (!BACK) head[0] = 0;
+    head[1] = 0;
+  }
+}
+
 // counters to zero, published words to kUnset, 16 bytes a lane
+template <bool BACK>
 __global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long counters, long long all) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) head[0] = 0;
+  clear_expired<BACK>(head);
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
     const unsigned v = i < counters ? 0u : kUnset;
     reinterpret_cast<uint4*>(head + 64)[i] = make_uint4(v, v, v, v);
@@ -169,7 +180,7 @@ __global__ __launch_bounds__(256) void clear_kernel(unsigned* head, long long co
 }
 
 // Read `count` words at once, and those again that were unset.
-template <int N, int VW, class Load, class Word>
+template <bool BACK, int N, int VW, class Load, class Word>
 __device__ __forceinline__ void wait_words(const ScanParams& p, int count, Word (&v)[N][VW], Load load) {
   unsigned need = (1u << count) - 1u;
   for (int spin = 0; need; ++spin) {
@@ -187,8 +198,8 @@ __device__ __forceinline__ void wait_words(const ScanParams& p, int count, Word 
         if (__all(ok)) need &= ~(1u << j);
       }
     if (!need) break;
-    if (spin == kWaitLimit) {
-      flag_store(p.head, 1u);
+    if (spin >= p.spin_limit) {
+      flag_store(p.head + BACK, 1u);
       break;                             // the unset words are NaNs
     }
     __builtin_amdgcn_s_sleep(1);
@@ -198,7 +209,7 @@ __device__ __forceinline__ void wait_words(const ScanParams& p, int count, Word 
 // The state that chunk `pos` (in walking order) starts from: the wave's VW
 // channels at `c` of `C`.  The maps since the last published state are composed
 // (A, B) first, then that state (s) is waited for.
-template <int MODE, int VW, int SUPER>
+template <bool BACK, int MODE, int VW, int SUPER>
 __device__ __forceinline__ void wait_state(const ScanParams& p, int pos, long long C, long long c, bool live, float (&A)[VW],
                                            float (&B)[VW], float (&s)[VW]) {
   const int sup = pos / SUPER, n = pos - sup * SUPER;
@@ -214,7 +225,7 @@ __device__ __forceinline__ void wait_state(const ScanParams& p, int pos, long lo
     unsigned long long m[N][VW];
     const unsigned long long* from = p.maps + (long long)(sup * SUPER + j0) * C + c;
     const int count = min(N, n - j0);
-    wait_words<N, VW>(p, count, m, [&](int j, int e) { return live ? peek2(from + j * C + e) : 0ull; });
+    wait_words<BACK, N, VW>(p, count, m, [&](int j, int e) { return live ? peek2(from + j * C + e) : 0ull; });
 #pragma unroll
     for (int j = 0; j < N; ++j)
       if (j < count)
@@ -232,7 +243,7 @@ __device__ __forceinline__ void wait_state(const ScanParams& p, int pos, long lo
 #pragma unroll
   for (int e = 0; e < VW; ++e) A[e] = mark(A[e], B[e], grew[e], low[e]);
   unsigned u[1][VW];
-  wait_words<1, VW>(p, 1, u, [&](int, int e) { return live ? peek(p.state + (long long)sup * C + c + e) : 0u; });
+  wait_words<BACK, 1, VW>(p, 1, u, [&](int, int e) { return live ? peek(p.state + (long long)sup * C + c + e) : 0u; });
 #pragma unroll
   for (int e = 0; e < VW; ++e) s[e] = __uint_as_float(u[0][e]);
 }
@@ -240,7 +251,7 @@ __device__ __forceinline__ void wait_state(const ScanParams& p, int pos, long lo
 // For the channels `again`, whose composed maps stray: the chunks' maps once
 // more, one after the other from the group's first state; a chunk whose map is
 // not clean publishes the state after it, too.
-template <int VW, int SUPER>
+template <bool BACK, int VW, int SUPER>
 __device__ __forceinline__ void step_by_step(const ScanParams& p, int pos, long long C, long long c, const bool (&again)[VW],
                                              float (&h)[VW]) {
   const int sup = pos / SUPER, n = pos - sup * SUPER;
@@ -258,7 +269,7 @@ __device__ __forceinline__ void step_by_step(const ScanParams& p, int pos, long 
     }
     if (!__any(any)) continue;
     unsigned u[1][VW];
-    wait_words<1, VW>(p, 1, u, [&](int, int e) { return wait[e] ? peek(p.ends + at + e) : 0u; });
+    wait_words<BACK, 1, VW>(p, 1, u, [&](int, int e) { return wait[e] ? peek(p.ends + at + e) : 0u; });
 #pragma unroll
     for (int e = 0; e < VW; ++e)
       if (wait[e]) h[e] = __uint_as_float(u[0][e]);
@@ -270,6 +281,7 @@ struct Place {
   int pos;           // chunk, in walking order
   int d, c0;         // direction, first channel (of B * H)
 };
+template <bool BACK>
 __device__ __forceinline__ Place place(const ScanParams& p, int VW, unsigned& shared) {
   const int per = (p.B * p.H + 64 * VW - 1) / (64 * VW), tile = (int)(blockIdx.x % (unsigned)(per * p.D));
   Place r;
@@ -279,8 +291,8 @@ __device__ __forceinline__ Place place(const ScanParams& p, int VW, unsigned& sh
     if (threadIdx.x == 0) shared = atomicAdd(p.counters + tile * 16LL, 1u);
     __syncthreads();
     r.pos = __builtin_amdgcn_readfirstlane(shared);
-  } else if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.head[0] = 0;
+  } else {
+    clear_expired<BACK>(p.head);
   }
   r.d = tile / per;
   r.c0 = (tile - r.d * per) * 64 * VW;
@@ -300,7 +312,7 @@ struct Exchange {
 // compose the waves' maps to the chunk's, find the state before the chunk,
 // pass it on; returns the state before this wave's piece.  end(x): the state x
 // before this wave's piece becomes the one after it.
-template <int MODE, int VW, int SUPER, int MW, class End>
+template <bool BACK, int MODE, int VW, int SUPER, int MW, class End>
 __device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, long long c, bool live, const float* first,
                                      int wave, int lane, int W, Exchange<VW, MW>& x, const float (&A)[VW], const float (&B)[VW],
                                      float (&h)[VW], End end) {
@@ -361,7 +373,7 @@ __device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, 
       }
     }
     dirty = __any(dirty);
-    if (pos > 0) wait_state<MODE, VW, SUPER>(p, pos, C, c, live, gA, gB, s);
+    if (pos > 0) wait_state<BACK, MODE, VW, SUPER>(p, pos, C, c, live, gA, gB, s);
     perturb_pause(wave_tag(), pos, 5u);
     float* const next = (ends ? p.state + (long long)(pos / SUPER + 1) * C : p.ends + (long long)pos * C) + c;
     bool again[VW], out[VW] = {}, any = false;
@@ -385,7 +397,7 @@ __device__ __forceinline__ void join(const ScanParams& p, int pos, long long C, 
 #pragma unroll
       for (int e = 0; e < VW; ++e)
         if (again[e]) h[e] = s[e];
-      step_by_step<VW, SUPER>(p, pos, C, c, again, h);
+      step_by_step<BACK, VW, SUPER>(p, pos, C, c, again, h);
 #pragma unroll
       for (int e = 0; e < VW; ++e)
         if (again[e]) {
@@ -509,7 +521,7 @@ __global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(con
   constexpr int ES = BF ? 2 : 4, G = kScanFwdSteps;
   __shared__ Exchange<VW, kScanFwdWaves> x;
   __shared__ unsigned shared;
-  const Place at = place(p, VW, shared);
+  const Place at = place<false>(p, VW, shared);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const long long C = (long long)p.D * p.B * p.H;
   long long gbase, ybase;
@@ -564,7 +576,7 @@ __global__ __launch_bounds__(64 * kScanFwdWaves, kScanFwdEu) void fwd_kernel(con
   if (whole) compose(std::true_type{});
   else compose(std::false_type{});
   mark_piece<MODE>(a, B, low, A);
-  join<MODE, VW, kScanFwdSuper, kScanFwdWaves>(p, at.pos, C, c, l.live, p.h0, wave, lane, W, x, A, B, h, [&](float (&s)[VW]) {
+  join<false, MODE, VW, kScanFwdSuper, kScanFwdWaves>(p, at.pos, C, c, l.live, p.h0, wave, lane, W, x, A, B, h, [&](float (&s)[VW]) {
 #pragma unroll
     for (int i = 0; i < G; ++i)
 #pragma unroll
@@ -604,7 +616,7 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
   constexpr int ES = BF ? 2 : 4, G = kScanBwdSteps;
   __shared__ Exchange<VW, kScanBwdWaves> x;
   __shared__ unsigned shared;
-  const Place at = place(p, VW, shared);
+  const Place at = place<true>(p, VW, shared);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
   const long long C = (long long)p.D * p.B * p.H;
   long long gbase, ybase;
@@ -691,7 +703,7 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
   if (whole) compose(std::true_type{});
   else compose(std::false_type{});
   mark_piece<MODE>(a, B, low, A);
-  join<MODE, VW, kScanBwdSuper, kScanBwdWaves>(p, at.pos, C, c, l.live, p.dhy, wave, lane, W, x, A, B, D, [&](float (&s)[VW]) {
+  join<true, MODE, VW, kScanBwdSuper, kScanBwdWaves>(p, at.pos, C, c, l.live, p.dhy, wave, lane, W, x, A, B, D, [&](float (&s)[VW]) {
 #pragma unroll
     for (int i = G - 1; i >= 0; --i) {
       float v[VW];
@@ -732,9 +744,11 @@ __global__ __launch_bounds__(64 * kScanBwdWaves, kScanBwdEu) void bwd_kernel(con
 }
 
 // T == 0: the states pass through
-__global__ __launch_bounds__(256) void pass_kernel(long long n, const float* from, float* to) {
+template <bool BACK>
+__global__ __launch_bounds__(256) void pass_kernel(unsigned* head, long long n, const float* from, float* to) {
+  clear_expired<BACK>(head);
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) to[i] = from ? from[i] : 0.f;
+  if (to && i < n) to[i] = from ? from[i] : 0.f;
 }
 
 template <bool BACK, bool BF, int MODE>
@@ -754,7 +768,7 @@ hipError_t launch(const ScanParams& p, int mode, int bf16, hipStream_t s) {
   if (C == 0) return hipSuccess;
   if (p.T == 0) {
     float* to = BACK ? p.dh0 : p.hy;
-    if (to) hipLaunchKernelGGL(pass_kernel, dim3((unsigned)((C + 255) / 256)), dim3(256), 0, s, C, BACK ? p.dhy : p.h0, to);
+    hipLaunchKernelGGL(pass_kernel<BACK>, dim3((unsigned)((C + 255) / 256)), dim3(256), 0, s, p.head, C, BACK ? p.dhy : p.h0, to);
     return hipGetLastError();
   }
   // bf16: two channels (4 bytes) a lane where they never straddle two rows of
@@ -767,7 +781,7 @@ hipError_t launch(const ScanParams& p, int mode, int bf16, hipStream_t s) {
     const long long words = (3LL * p.chunks + p.chunks / (BACK ? kScanBwdSuper : kScanFwdSuper) + 1) * C;
     const long long counters = ((char*)p.maps - (char*)p.counters) / 16, all = counters + (words + 3) / 4;
     const dim3 grid((unsigned)std::min<long long>((all + 255) / 256, 2048));
-    hipLaunchKernelGGL(clear_kernel, grid, dim3(256), 0, s, p.head, counters, all);
+    hipLaunchKernelGGL(clear_kernel<BACK>, grid, dim3(256), 0, s, p.head, counters, all);
   }
   const dim3 grid((unsigned)(tiles * p.chunks)), block(64 * p.waves);
   if (bf16 && mode == SCAN_GATED) start<BACK, true, SCAN_GATED>(p, two, grid, block, s);
