@@ -1,9 +1,10 @@
-"""ctypes binding of include/rnn.h.  Argument marshalling only."""
+"""ctypes binding of include/rnn.h: argument checks and marshalling."""
 
 from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import numpy as np
 import torch
@@ -19,7 +20,7 @@ KERNEL_NAMES = ["gemm_input", "recurrent_fwd", "recurrent_bwd", "gemm_dx", "gemm
 STATUS_DEVICE_TIMEOUT = -7
 
 _LIB = None
-_CALL = None      # the compiled entries of the language-model operators (csrc/call.cpp)
+_CALL = None      # the compiled entries of the language-model operators (csrc/call.cpp), or _Interpreted
 
 
 class RNNError(RuntimeError):
@@ -93,14 +94,27 @@ def load_library():
     lib.rnn_static_workspace_bytes.restype = ctypes.c_size_t
     try:
         from . import _call
-    except ImportError as e:
-        raise RuntimeError(f"{os.path.dirname(path)}/_call.so cannot be loaded ({e}): build the extension first "
-                           "(python -m layer_rnn_forward_amd.build)") from e
-    _call.bind(*(ctypes.cast(getattr(lib, n), vp).value for n in (
-        "rnn_scan_step", "rnn_scan_forward", "rnn_scan_backward", "rnn_ffn_forward", "rnn_ffn_backward",
-        "rnn_checkpoint_size", "rnn_checkpoint_store", "rnn_checkpoint_load")))
+        _call.bind(*(ctypes.cast(getattr(lib, n), vp).value for n in (
+            "rnn_scan_step", "rnn_scan_forward", "rnn_scan_backward", "rnn_ffn_forward", "rnn_ffn_backward",
+            "rnn_checkpoint_size", "rnn_checkpoint_store", "rnn_checkpoint_load")))
+    except ImportError as e:      # built for another Python or torch: nothing else needs it
+        _call = _Interpreted(e)
     _LIB, _CALL = lib, _call
     return lib
+
+
+class _Interpreted:
+    """In the place of the compiled entries: every call goes on to its ctypes path."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        if self.why is not None:
+            warnings.warn(f"_call.so cannot be loaded ({self.why}): calls of the language-model operators take a few "
+                          "microseconds longer; python -m layer_rnn_forward_amd.build makes it", RuntimeWarning, stacklevel=3)
+            self.why = None
+        return lambda *args: None
 
 
 def rnn_status_string(s: int) -> str:
@@ -322,7 +336,8 @@ def rnn_profile_read(h, kernel: int):
 # ------------------------------------------------- language-model operators
 # Each call goes to its compiled entry (_call), which checks its arguments and
 # returns the status, or None where a check failed; the code after it then
-# finds the failing check and raises.
+# finds the failing check and raises (or, without the compiled entries, makes
+# the call).
 _WTYPE_OF = {torch.float32: 0, torch.bfloat16: 1}
 
 
