@@ -62,12 +62,12 @@ __device__ __forceinline__ int job_of(const Jobs& j, int b) {
 
 template <bool BF, int T, int OCC>
 __global__ __launch_bounds__(256, OCC) void store_kernel(const Jobs j) {
-  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds<BF, T, T>()];
+  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds(64 * T, 64 * T)];
   ffn_product<BF, true, true, T, T, FFN_STORE, SAVE_NONE, 0>(j.p[0], smem, (int)blockIdx.x, j.blocks[0]);
 }
 template <bool BF, int T, int OCC>
 __global__ __launch_bounds__(256, OCC) void grads_kernel(const Jobs j) {
-  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds<BF, T, T>()];
+  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds(64 * T, 64 * T)];
   const int b = (int)blockIdx.x, i = job_of(j, b);
   const FfnGemm p = j.p[i];
   if (i == 0) ffn_product<BF, true, false, T, T, FFN_STORE, SAVE_NONE, 0>(p, smem, b - j.begin[0], j.blocks[0]);

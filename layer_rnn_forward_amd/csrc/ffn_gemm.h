@@ -58,7 +58,6 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kStagesA = 3, kStagesB = 2;
 constexpr unsigned kOutside = 0x80000000u;   // byte offset past any operand tile: reads zeros
 
 // s_waitcnt immediate (gfx9 encoding), export count not waited on.
@@ -451,10 +450,6 @@ __device__ __forceinline__ void tile_at(int lin, int tm, int tn, int& m, int& n)
   n = in / gm;
 }
 
-// LDS of one product
-template <bool BF, int MT, int NT>
-constexpr int ffn_lds() { return (kStagesA * 64 * MT + kStagesB * 64 * NT) * kStep; }
-
 // Piece `block` of a product that has `blocks` (a multiple of 8) workgroups: a
 // tile, or a split of a tile's k, whose sums go to p.part.
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT>
@@ -690,7 +685,7 @@ __device__ __forceinline__ void ffn_product(const FfnGemm& p, char* smem, int bl
 
 template <bool BF, bool AROWS, bool BROWS, int MT, int NT, int EPI, int SAVE, int ACT, int OCC>
 __global__ __launch_bounds__(256, OCC) void ffn_gemm_kernel(const FfnGemm p) {
-  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds<BF, MT, NT>()];
+  __shared__ __attribute__((aligned(1024))) char smem[ffn_lds(64 * MT, 64 * NT)];
   ffn_product<BF, AROWS, BROWS, MT, NT, EPI, SAVE, ACT>(p, smem, (int)blockIdx.x, (int)gridDim.x);
 }
 
@@ -748,14 +743,14 @@ template <bool AROWS, bool BROWS, int EPI, int SAVE, int ACT>
 hipError_t ffn_pick(const FfnGemm& p, int tile, int bf16, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
   const long long tiles = ffn_tiles(p, tile, EPI == FFN_GLU);
-  constexpr int N64 = EPI == FFN_GLU ? 2 : 1;
+  constexpr int N64 = EPI == FFN_GLU ? 2 : 1, OCC64 = ffn_places(TILE_64, EPI == FFN_GLU);
   if (!bf16) {
     if (tile == TILE_128) return ffn_launch<false, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, tiles, s);
-    return ffn_launch<false, AROWS, BROWS, 1, N64, EPI, SAVE, ACT, 3>(p, tiles, s);
+    return ffn_launch<false, AROWS, BROWS, 1, N64, EPI, SAVE, ACT, OCC64>(p, tiles, s);
   }
   if (tile == TILE_256) return ffn_launch<true, AROWS, BROWS, 4, 4, EPI, SAVE, ACT, 1>(p, tiles, s);
   if (tile == TILE_128) return ffn_launch<true, AROWS, BROWS, 2, 2, EPI, SAVE, ACT, 2>(p, tiles, s);
-  return ffn_launch<true, AROWS, BROWS, 1, N64, EPI, SAVE, ACT, 3>(p, tiles, s);
+  return ffn_launch<true, AROWS, BROWS, 1, N64, EPI, SAVE, ACT, OCC64>(p, tiles, s);
 }
 
 }  // namespace rnnk

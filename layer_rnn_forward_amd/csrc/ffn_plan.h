@@ -8,11 +8,21 @@
 namespace rnnk {
 
 constexpr int kStep = 128;     // bytes of k in a step
+constexpr int kStagesA = 3, kStagesB = 2;   // steps of each operand in LDS
+constexpr int kLds = 160 * 1024;            // of a CU
 
-// Tiles: 256 x 256 (one workgroup a CU), 128 x 128 (two), 64 x 64 (three; of
-// the gated product 64 x 128).
+// Tiles: 256 x 256, 128 x 128, 64 x 64 (of the gated product 64 x 128).
 enum FfnTile { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
 constexpr int kTile[3] = {256, 128, 64};
+
+// LDS of a workgroup, and workgroups that a CU holds: as many as fit its LDS
+// (one of 256 x 256, two of 128 x 128 and of 64 x 128), three of 64 x 64 (its
+// registers).
+constexpr int ffn_lds(int rows, int cols) { return (kStagesA * rows + kStagesB * cols) * kStep; }
+constexpr int ffn_places(int tile, bool glu) {
+  const int fit = kLds / ffn_lds(kTile[tile], glu && tile == TILE_64 ? 128 : kTile[tile]);
+  return fit < 3 ? fit : 3;
+}
 
 inline long long ffn_tiles(const FfnGemm& p, int tile, bool glu) {
   if (p.M <= 0 || p.N <= 0) return 0;
@@ -36,10 +46,11 @@ struct FfnChoice {
 // CU to itself and with all of its places taken (in between: linear):
 //   bf16   256: 1.45 us   128: 0.50 us, two a CU 0.86 us   64: 0.31 us, three a CU 0.54 us
 //   fp32                  128: 1.9 us,  two a CU 3.8 us    64: 0.5 us,  three a CU 1.44 us
-// A step of the gated product's 64 x 128 takes 2 of a 64 x 64's (bf16, alone: 1.3).
+// of the gated product, fp32 128: 2.08 us, two a CU 3.7 us; 64 x 128: 1.22 and 2.18 us (bf16: 0.46 and 0.63 us).
 inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const FfnChoice& c) {
-  static constexpr double alone[2][3] = {{0, 190, 50}, {145, 50, 31}}, full[2][3] = {{0, 380, 144}, {145, 86, 54}};
-  static constexpr int most[3] = {1, 2, 3};
+  static constexpr double alone[2][5] = {{0, 190, 50, 208, 122}, {145, 50, 31, 50, 46}},
+                          full[2][5] = {{0, 380, 144, 370, 218}, {145, 86, 54, 86, 63}};
+  const int t = glu && c.tile != TILE_256 ? 2 + c.tile : c.tile, most = ffn_places(c.tile, glu);
   long long all = 0;
   double after = 0;
   for (int i = 0; i < n; ++i) {
@@ -48,10 +59,20 @@ inline double ffn_time(const FfnGemm* const* p, int n, int bf16, bool glu, const
     // a second launch, and the partial sums' way out and back at about 3 TB/s
     if (c.splits[i] > 1) after = std::max(after, 500.0) + (double)pieces * ffn_area(c.tile, glu) * 8 / 3e4;
   }
-  const int occ = (int)std::max(1LL, std::min<long long>(most[c.tile], (all + 255) / 256)), places = 256 * occ;
-  const double share = occ > 1 ? (occ - 1.0) / (most[c.tile] - 1) : 0;
-  double step = alone[bf16][c.tile] + share * (full[bf16][c.tile] - alone[bf16][c.tile]);
-  if (glu && c.tile == TILE_64) step *= bf16 ? 1.3 + 0.7 * share : 2;
+  const int occ = (int)std::max(1LL, std::min<long long>(most, (all + 255) / 256)), places = 256 * occ;
+  auto step_of = [&](int held) {
+    const double share = held > 1 ? (held - 1.0) / (most - 1) : 0;
+    return alone[bf16][t] + share * (full[bf16][t] - alone[bf16][t]);
+  };
+  const double step = step_of(occ);
+  // The gated product: full rounds, and the rest of the pieces on fewer places a
+  // CU.  (Not for bf16's larger tiles, where a last round of one a CU takes as
+  // long as one of two: 4187 x 2392 x 1224 on 128 x 128 107 us, on 256 x 256 88.)
+  if (glu && (!bf16 || c.tile == TILE_64)) {
+    const double steps = (double)((ffn_steps(*p[0], bf16) + c.splits[0] - 1) / c.splits[0]) + 4;
+    const long long whole = all / (256 * most), rest = all - whole * 256 * most;
+    return after + steps * ((double)whole * step_of(most) + (rest ? step_of((int)((rest + 255) / 256)) : 0));
+  }
   struct Group {
     double time;
     long long count;
