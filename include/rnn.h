@@ -449,7 +449,8 @@ typedef enum RNN_ENUM_BASE { RNN_SAVE_NONE = 0, RNN_SAVE_FULL = 1, RNN_SAVE_INT8
 
 /* The workspace holds padded copies of operands whose rows are not whole,
  * aligned 16-byte pieces, the gated product or its gradients, and partial sums
- * of products that split k; nothing in it outlives a call.
+ * of products that split k; nothing in it outlives a call.  Its size does for
+ * fewer rows, too (as the reserve's does).
  * UNSUPPORTED: D or F >= 2^20, or M >= 2^30. */
 rnn_status_t rnn_ffn_workspace_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);
 rnn_status_t rnn_ffn_reserve_size(int M, int D, int F, rnn_wtype_t wtype, rnn_save_t save, size_t* bytes);

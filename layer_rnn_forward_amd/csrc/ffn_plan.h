@@ -156,6 +156,48 @@ inline size_t ffn_part(const FfnGemm& p, const FfnChoice& c, int i, bool glu) {
   return (size_t)ffn_tiles(p, c.tile, glu) * c.splits[i] * ffn_area(c.tile, glu) * 4;
 }
 
+// Bounds of the partial sums over all numbers of rows up to some M, so that a
+// workspace of M rows does for fewer.  With pieces of at least work / 1024 and 8
+// steps, a product alone is split while it has at most 512 tiles, into 1024
+// pieces at most; of several, one that is split has at least 3 work / 2048
+// steps, and the pieces are at most 1024 and one a tile of theirs.
+inline long long ffn_pieces(const FfnGemm& p, int tile, int bf16, bool glu) {
+  const long long steps = ffn_steps(p, bf16);
+  return steps < 12 ? 0 : ffn_tiles(p, tile, glu) * std::min(64LL, (steps + 7) / 8);
+}
+// Forward's product p: its bound, and the rows m <= p.M at which it is reached.
+inline size_t ffn_part_bound(const FfnGemm& p, int tile, int bf16, bool glu, int& m) {
+  FfnGemm q = p;
+  q.M = 1;
+  const long long across = ffn_tiles(q, tile, glu);
+  m = across ? (int)std::min<long long>(p.M, 512 / across * kTile[tile]) : 0;
+  q.M = m;
+  return (size_t)std::min(1024LL, ffn_pieces(q, tile, bf16, glu)) * ffn_area(tile, glu) * 4;
+}
+// Backward's: dx has more tiles with more rows, and the others more steps.
+inline size_t ffn_part_bound(const FfnGemm (&p)[3], int tile, int bf16, int& m) {
+  FfnGemm q = p[0], one = p[1];
+  const long long fixed = ffn_tiles(p[1], tile, false) + ffn_tiles(p[2], tile, false), deep = ffn_steps(p[0], bf16);
+  auto splits = [&](int rows) {   // whether dx may be
+    q.M = one.K = rows;
+    return 3 * (ffn_tiles(q, tile, false) * deep + fixed * ffn_steps(one, bf16)) <= 2048 * deep;
+  };
+  int lo = 0, hi = p[0].M;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (splits(mid)) lo = mid;
+    else hi = mid - 1;
+  }
+  q.M = m = lo;
+  long long pieces = ffn_pieces(q, tile, bf16, false), tiles = ffn_tiles(q, tile, false);
+  if (fixed <= 682 && ffn_pieces(p[1], tile, bf16, false) + ffn_pieces(p[2], tile, bf16, false) > 0) {
+    pieces += ffn_pieces(p[1], tile, bf16, false) + ffn_pieces(p[2], tile, bf16, false);
+    tiles += fixed;
+    m = p[0].M;
+  }
+  return (size_t)std::min(1024 + tiles, pieces) * ffn_area(tile, false) * 4;
+}
+
 // The products that may be split, by their sizes alone: forward's two, and
 // backward's last three, longest first (the order that ffn_choose_backward
 // gives).

@@ -104,7 +104,7 @@ size_t ckpt_bytes(size_t rows, size_t cols) { return rows * cols + rows * ((cols
 struct FfnPlan {
   int es = 0, Dp = 0, Fo = 0, Fp = 0;
   // workspace: padded copies (used where rows or addresses are not 16-byte
-  // aligned), the gated product, its gradients
+  // aligned, which the size does not know), the gated product, its gradients
   size_t x = 0, w_in = 0, w_out = 0, dy = 0, h = 0, dgu = 0, ws = 0;
   // and the partial sums of split products; the choices do not depend on which
   // gradients are wanted
@@ -130,14 +130,25 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
     o += align_up(bytes);
     return at;
   };
-  p.x = take(m * p.Dp * es);
-  p.w_in = take(2 * (size_t)F * p.Dp * es);
-  p.w_out = take((size_t)D * p.Fo * es);
-  if (save != RNN_SAVE_FULL) p.h = take((save == RNN_SAVE_NONE && M <= kFfnRows ? 2 : 1) * m * p.Fp * es);   // few rows: and the rests
-  if (save != RNN_SAVE_NONE) {
-    p.dy = take(m * p.Dp * es);
-    p.dgu = take(m * 2 * p.Fp * es);
+  // the block for few rows needs the gated product and the rests of its rounding, and nothing else
+  auto few = [&](size_t rows) { return align_up(2 * rows * p.Fp * es); };
+  if (save == RNN_SAVE_NONE && M <= kFfnRows) {
+    p.ws = std::max(few(m), kAlign);
+    return p;
   }
+  // copies, the gated product, its gradients; returns where they end for `rows` rows
+  auto layout = [&](size_t rows) {
+    o = 0;
+    p.x = take(rows * p.Dp * es);
+    p.w_in = take(2 * (size_t)F * p.Dp * es);
+    p.w_out = take((size_t)D * p.Fo * es);
+    if (save != RNN_SAVE_FULL) p.h = take(rows * p.Fp * es);
+    if (save != RNN_SAVE_NONE) {
+      p.dy = take(rows * p.Dp * es);
+      p.dgu = take(rows * 2 * p.Fp * es);
+    }
+    return o;
+  };
   const int bf = wtype == RNN_W_BF16;
   ffn_forward_product(M, D, F, p.out);
   p.out_choice = ffn_choose_forward(p.out, bf, false);
@@ -145,19 +156,32 @@ FfnPlan ffn_plan(int M, int D, int F, int wtype, int save) {
   ffn_gated_product(M, D, F, p.gated);
   p.gated_choice = ffn_choose_forward(p.gated, bf, true);
   p.gated.splits = p.gated_choice.splits[0];
-  const size_t parts = o;
+  if (save != RNN_SAVE_NONE) ffn_backward_products(M, D, F, p.Fp, p.grads);
+  // room for every smaller M as well
+  if (save == RNN_SAVE_NONE) p.ws = few(kFfnRows);
+  for (int tile : {TILE_128, TILE_64}) {
+    int rows = 0;
+    size_t part = ffn_part_bound(p.out, tile, bf, false, rows);
+    p.ws = std::max(p.ws, layout(rows) + part);
+    part = ffn_part_bound(p.gated, tile, bf, true, rows);
+    p.ws = std::max(p.ws, layout(rows) + part);
+    if (save != RNN_SAVE_NONE) {
+      part = ffn_part_bound(p.grads, tile, bf, rows);
+      p.ws = std::max(p.ws, layout(rows) + part);
+    }
+  }
+  const size_t parts = layout(m);   // the passes' partial sums share their place
   p.part = take(std::max(ffn_part(p.out, p.out_choice, 0, false), ffn_part(p.gated, p.gated_choice, 0, true)));
-  const size_t forward = o;
-  o = parts;              // the passes' partial sums share their place
+  p.ws = std::max({p.ws, o, kAlign});
   if (save != RNN_SAVE_NONE) {
-    ffn_backward_products(M, D, F, p.Fp, p.grads);
+    o = parts;
     p.grads_choice = ffn_choose_backward(p.grads, bf, p.order);
     for (int i = 0; i < 3; ++i) {
       p.grads[i].splits = p.grads_choice.splits[i];
       p.grads_part[i] = take(ffn_part(p.grads[i], p.grads_choice, i, false));
     }
+    p.ws = std::max(p.ws, o);
   }
-  p.ws = std::max({o, forward, kAlign});
   o = 0;
   if (save != RNN_SAVE_NONE) {
     const size_t vs = save == RNN_SAVE_INT8 ? 1 : wtype == RNN_W_BF16 ? 2 : 4;
@@ -291,7 +315,7 @@ rnn_status_t rnn_ffn_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, rnn
     FfnRows r{};
     r.M = M; r.R = F; r.K = D;
     r.x = x; r.ldx = D; r.w = w_in;
-    r.out = at<void>(ws, p.h); r.ldo = p.Fp;
+    r.out = ws; r.ldo = p.Fp;
     r.act = act;
     LM_TRY(dev(rnn_launch_ffn_rows(r, bf, 1, s)));
     r.R = D; r.K = F;
