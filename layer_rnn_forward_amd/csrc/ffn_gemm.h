@@ -214,6 +214,19 @@ __device__ __forceinline__ void store_row(El<BF>* row, const float (&v)[16], int
       if (8 * j + 4 * h + e < left) el_store<BF>(row + 8 * j + 4 * h + e, v[4 * j + e]);
 }
 
+// Zeros after the last column of a row that is an operand of the next product
+// with its columns as k: that product reads whole 16-byte pieces against zeros,
+// and an infinity or a NaN of the row's own (times this product's zeros) must
+// not be there.  `row` points at the row's last 32 columns; the lane that
+// stored a piece clears its end.
+template <bool BF>
+__device__ __forceinline__ void clear_end(El<BF>* row, int left, int h) {
+  constexpr int P = BF ? 8 : 4;
+  if (left >= 32 || (left / P & 1) != h) return;
+#pragma unroll 1
+  for (int c = left; c % P; ++c) row[c] = 0;
+}
+
 // The two lanes of a row agree on the bit pattern of the group's largest
 // magnitude.
 __device__ __forceinline__ unsigned group_top(const float (&v)[16]) {
@@ -369,7 +382,9 @@ __device__ __forceinline__ void glu_tile(const f32x16& gv, const f32x16& uv, con
     o[i] = a[i] * uv[i];
     da[i] *= uv[i];
   }
-  store_row<BF>((El<BF>*)p.C + m * p.ldc + f, o, lane >> 5, 32, true);
+  El<BF>* row = (El<BF>*)p.C + m * p.ldc + f;
+  store_row<BF>(row, o, lane >> 5, 32, true);
+  clear_end<BF>(row, p.N - f, lane >> 5);
   if constexpr (SAVE != SAVE_NONE) {
     const long long tile = (m >> 5) * p.lds + (f >> 5);
     Saved<BF, SAVE> s0, s1;
@@ -436,6 +451,8 @@ __device__ __forceinline__ void dglu_tile(const f32x16& dh, const Saved<BF, SAVE
   El<BF>* row = (El<BF>*)p.C + m * p.ldc + f;
   store_row<BF>(row, b, h, 32, true);
   store_row<BF>(row + p.ldc / 2, a, h, 32, true);
+  clear_end<BF>(row, p.N - f, h);
+  clear_end<BF>(row + p.ldc / 2, p.N - f, h);
 }
 
 }  // namespace
