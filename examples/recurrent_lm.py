@@ -21,7 +21,7 @@ def room(n):
 
 
 class Scan(torch.autograd.Function):
-    """y, hy = scan(x W^T, h0) over x [T, B, D]; x is kept in 8 bits, the gates are made again for backward."""
+    """y, hy = scan(x W^T, h0) over x [T, B, D]; x is kept in 8 bits, the gates as they are."""
 
     @staticmethod
     def forward(ctx, x, w, h0):

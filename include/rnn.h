@@ -367,7 +367,12 @@ rnn_status_t rnn_profile_read(rnn_handle_t h, int kernel, long long* launches, d
  * model.  They keep no state on the host and need no handle.  `wtype` is the
  * element type of the activations and weights they take and write
  * (RNN_W_F32 or RNN_W_BF16); recurrent states are always fp32, and every sum,
- * state and activation is computed in fp32.  All tensors are contiguous.
+ * state and activation is computed in fp32.  With RNN_W_BF16 the feed-forward
+ * block rounds what one of its products passes on to the next to bf16: the
+ * gated product, and in backward its two factors' gradients (without saving, up
+ * to 64 rows, the gated product is passed on as two bf16 numbers instead).
+ * All tensors are contiguous.  Outputs overlap neither inputs nor each other,
+ * except where a call allows it.
  * Buffers may have any alignment that their element type allows (workspaces,
  * reserves and checkpoints: 256 bytes).  Two calls that share a workspace
  * must not run at the same time.  Every call only enqueues on `stream`, can
@@ -418,7 +423,7 @@ rnn_status_t rnn_scan_forward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wt
 
 /* Gradients of a forward call with the same mode, sizes, g, h0, lengths and
  * workspace (which may have been followed by other backward calls, but by no
- * other forward call).  dy [T, B, dirs * H]; dhy [dirs, B, H] fp32 or NULL
+ * other forward call).  h0 itself is not read: the workspace has the states.  dy [T, B, dirs * H]; dhy [dirs, B, H] fp32 or NULL
  * (zeros); dg as g; dh0 as h0 or NULL, and may be dhy itself. */
 rnn_status_t rnn_scan_backward(void* stream, rnn_scan_mode_t mode, rnn_wtype_t wtype, int T, int B, int H, int dirs,
                                const void* g, const float* h0, const int* lengths, const void* dy, const float* dhy,

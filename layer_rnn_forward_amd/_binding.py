@@ -476,7 +476,7 @@ def rnn_scan_forward(mode, g, h0, lengths, y, hy, ws):
 
 def rnn_scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws):
     """Gradients of the rnn_scan_forward call that filled ``ws`` (same mode, g,
-    h0 and lengths): ``dy`` [T, B, dirs*H], ``dhy`` as hy or None (zeros);
+    h0, which is checked but not read, and lengths): ``dy`` [T, B, dirs*H], ``dhy`` as hy or None (zeros);
     ``dg`` as g, ``dh0`` [dirs, B, H] float32 (its shape gives dirs and H; it
     may be the same tensor as dhy)."""
     status = (_CALL or _entries()).scan_backward(mode, g, h0, lengths, dy, dhy, dg, dh0, ws)
