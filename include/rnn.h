@@ -486,6 +486,113 @@ rnn_status_t rnn_checkpoint_store(void* stream, rnn_wtype_t wtype, int rows, int
 rnn_status_t rnn_checkpoint_load(void* stream, rnn_wtype_t wtype, int rows, int cols, const void* kept,
                                  size_t kept_bytes, void* x);
 
+/* ------------------------------------------- state-space language models
+ * The three operators of a selective state-space block: normalisation of rows
+ * with the residual addition before it, a short causal convolution, and the
+ * state-space scan.  Rules and errors as for the language-model operators
+ * above, with these differences: parameters (weights, biases, A, D) and their
+ * gradients are always fp32, and states that a scan carries, too; and where an
+ * `ld` is given, the rows of a time-major tensor [T, B, width] (row t * B + b)
+ * lie ld elements apart, so that it may be a slice of a wider one (ld >=
+ * width, else INVALID_ARG).  Sums are fp32 with a fixed order.  Outputs past a
+ * row's length are 0 and inputs there are not used, whatever they hold. */
+
+/* y = (s - m) * rstd * weight + bias  for each of M rows of D values, with
+ *   RNN_NORM_LAYER  m = mean(s), rstd = 1 / sqrt(mean((s - m)^2) + eps)
+ *   RNN_NORM_RMS    m = 0
+ * where s is x, or with a residual x + residual rounded to the element type
+ * (the next residual: written to `total` unless NULL; `total` may be x or
+ * residual itself).  weight, bias [D]: NULL stands for 1 and 0.  stats (or
+ * NULL) [M, 2]: m and rstd for the backward call.  INVALID_ARG for an eps
+ * that is negative or not finite.  UNSUPPORTED: D >= 2^20 or M >= 2^30. */
+typedef enum RNN_ENUM_BASE { RNN_NORM_LAYER = 0, RNN_NORM_RMS = 1 } rnn_norm_t;
+
+rnn_status_t rnn_norm_forward(void* stream, rnn_norm_t kind, rnn_wtype_t wtype, int M, int D, const void* x,
+                              const void* residual, const float* weight, const float* bias, float eps, void* y,
+                              void* total, float* stats);
+
+/* Gradients.  s: what the forward call normalised (x, or `total`); stats: its.
+ * dtotal (or NULL): a gradient that reaches s on another way (the residual
+ * stream's), added to dx, which is the gradient of x and of the residual; dx
+ * may be dtotal itself.  dx, dweight, dbias: each may be NULL (not wanted);
+ * the workspace is needed for dweight and dbias only. */
+rnn_status_t rnn_norm_workspace_size(int M, int D, size_t* bytes);
+rnn_status_t rnn_norm_backward(void* stream, rnn_norm_t kind, rnn_wtype_t wtype, int M, int D, const void* s,
+                               const float* weight, const float* stats, const void* dy, const void* dtotal, void* dx,
+                               float* dweight, float* dbias, void* ws, size_t ws_bytes);
+
+/* Depthwise causal convolution over time, 1 <= K <= 8 (else UNSUPPORTED):
+ *   v_t = bias + sum_k w[c, k] x_(t - K + 1 + k),   y = v or silu(v)
+ * x, y [T, B, C]; w [C, K]; bias [C] or NULL; s0 [K - 1, B, C] (element type;
+ * NULL: zeros): the inputs before the first step, the last of them x_(-1).
+ * sy as s0, or NULL: the inputs before the step that follows the row's last;
+ * it may be s0 itself.  `lengths` as for the scan.  act: RNN_ACT_NONE or
+ * RNN_ACT_SILU.  UNSUPPORTED: B * C >= 2^30 or T >= 2^30. */
+#define RNN_ACT_NONE ((rnn_act_t)3)
+
+rnn_status_t rnn_conv_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, int T, int B, int C, int K,
+                              const void* x, long long ldx, const float* w, const float* bias, const void* s0,
+                              const int* lengths, void* y, long long ldy, void* sy);
+
+/* One step (a generated token): x, y [B, C] with rows ldx and ldy apart. */
+rnn_status_t rnn_conv_step(void* stream, rnn_act_t act, rnn_wtype_t wtype, int B, int C, int K, const void* x,
+                           long long ldx, const float* w, const float* bias, const void* s, void* y, long long ldy,
+                           void* sy);
+
+/* Gradients.  dsy (as sy) NULL: zeros.  dx, dw, dbias, ds0: each may be NULL
+ * (not wanted); the workspace is needed for dw and dbias only. */
+rnn_status_t rnn_conv_workspace_size(int T, int B, int C, int K, size_t* bytes);
+rnn_status_t rnn_conv_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, int T, int B, int C, int K,
+                               const void* x, long long ldx, const float* w, const float* bias, const void* s0,
+                               const int* lengths, const void* dy, long long lddy, const void* dsy, void* dx,
+                               long long lddx, float* dw, float* dbias, void* ds0, void* ws, size_t ws_bytes);
+
+/* Selective state-space scan: channel e of E carries N states h,
+ *   d_t = softplus(delta_t + delta_bias)  (RNN_DELTA_LINEAR: the sum itself)
+ *   h_t[n] = exp(d_t A[e, n]) h_(t-1)[n] + d_t u_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D[e] u_t) * silu(z_t)
+ * u, delta, z, y [T, B, E]; Bm, Cm [T, B, groups * N], shared by the E / groups
+ * neighbouring channels of a group; A [E, N]; D, delta_bias [E].  D, z and
+ * delta_bias may be NULL (the term or factor is left out).  States h0, hy
+ * [B, E, N]; h0 NULL: zeros, hy NULL: not wanted; hy may be h0 itself.
+ * INVALID_ARG where groups < 1 or does not divide E; UNSUPPORTED: N > 64,
+ * B * E >= 2^24, T >= 2^30 or groups * N >= 2^20.  A state's decay over any
+ * number of steps may leave fp32's range; the states themselves may not. */
+typedef enum RNN_ENUM_BASE { RNN_DELTA_SOFTPLUS = 0, RNN_DELTA_LINEAR = 1 } rnn_delta_t;
+
+typedef struct rnn_ssm_inputs {
+  const void *u, *delta, *z, *Bm, *Cm;
+  long long ldu, lddelta, ldz, ldB, ldC;
+  const float *A, *D, *delta_bias;
+} rnn_ssm_inputs_t;
+
+/* What backward is asked for; NULL: not wanted. */
+typedef struct rnn_ssm_grads {
+  void *du, *ddelta, *dz, *dBm, *dCm;
+  long long lddu, ldddelta, lddz, lddB, lddC;
+  float *dA, *dD, *ddelta_bias, *dh0;
+} rnn_ssm_grads_t;
+
+/* One step (a generated token): rows [B, ...] of every tensor. */
+rnn_status_t rnn_ssm_step(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int B, int E, int N, int groups,
+                          const rnn_ssm_inputs_t* in, const float* h, void* y, long long ldy, float* hy);
+
+/* save: RNN_SAVE_NONE (inference) or RNN_SAVE_FULL (the workspace then holds
+ * the states that rnn_ssm_backward starts from). */
+rnn_status_t rnn_ssm_workspace_size(int T, int B, int E, int N, int groups, rnn_save_t save, size_t* bytes);
+rnn_status_t rnn_ssm_forward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, rnn_save_t save, int T, int B, int E,
+                             int N, int groups, const rnn_ssm_inputs_t* in, const float* h0, const int* lengths,
+                             void* y, long long ldy, float* hy, void* ws, size_t ws_bytes);
+
+/* Gradients of a forward call with RNN_SAVE_FULL and the same mode, sizes,
+ * inputs, lengths and workspace (which may have been followed by other
+ * backward calls, but by no other forward call).  dhy [B, E, N] or NULL
+ * (zeros); dh0 may be dhy itself. */
+rnn_status_t rnn_ssm_backward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int T, int B, int E, int N,
+                              int groups, const rnn_ssm_inputs_t* in, const int* lengths, const void* dy,
+                              long long lddy, const float* dhy, const rnn_ssm_grads_t* grads, void* ws,
+                              size_t ws_bytes);
+
 /* Static text for a status code. */
 const char* rnn_status_string(rnn_status_t s);
 

@@ -56,6 +56,17 @@ from ._binding import (  # noqa: F401
     rnn_checkpoint_size,
     rnn_checkpoint_store,
     rnn_checkpoint_load,
+    rnn_norm_workspace_size,
+    rnn_norm_forward,
+    rnn_norm_backward,
+    rnn_conv_workspace_size,
+    rnn_conv_forward,
+    rnn_conv_step,
+    rnn_conv_backward,
+    rnn_ssm_workspace_size,
+    rnn_ssm_forward,
+    rnn_ssm_step,
+    rnn_ssm_backward,
     pack_weights,
     unpack_weights,
     SCHED_AUTO,

@@ -14,6 +14,10 @@ WTYPES = {"f32": 0, "bf16": 1}
 SCAN_MODES = {"gated": 0, "linear": 1}
 ACTS = {"sigmoid": 0, "silu": 1, "gelu": 2}
 SAVES = {"none": 0, "full": 1, "int8": 2}
+NORMS = {"layer": 0, "rms": 1}
+CONV_ACTS = {"none": 3, "silu": 1}
+DELTAS = {"softplus": 0, "linear": 1}
+SSM_SAVES = {"none": 0, "full": 1}
 SCHED_AUTO, SCHED_PERSISTENT, SCHED_STEPPED = 0, 1, 2
 KERNEL_NAMES = ["gemm_input", "recurrent_fwd", "recurrent_bwd", "gemm_dx", "gemm_dw", "fill", "prep",
                 "exchange_probe", "dropout"]
@@ -21,6 +25,18 @@ STATUS_DEVICE_TIMEOUT = -7
 
 _LIB = None
 _CALL = None      # the compiled entries of the language-model operators (csrc/call.cpp), or _Interpreted
+
+
+class _SsmInputs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("u", "delta", "z", "Bm", "Cm")] + [
+        (n, ctypes.c_longlong) for n in ("ldu", "lddelta", "ldz", "ldB", "ldC")] + [
+        (n, ctypes.c_void_p) for n in ("A", "D", "delta_bias")]
+
+
+class _SsmGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("du", "ddelta", "dz", "dBm", "dCm")] + [
+        (n, ctypes.c_longlong) for n in ("lddu", "ldddelta", "lddz", "lddB", "lddC")] + [
+        (n, ctypes.c_void_p) for n in ("dA", "dD", "ddelta_bias", "dh0")]
 
 
 class RNNError(RuntimeError):
@@ -47,7 +63,7 @@ def load_library():
             f"{path} is missing: build the HIP extension first "
             "(python -m layer_rnn_forward_amd.build)")
     lib = ctypes.CDLL(path)
-    vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, i, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
     psz = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "rnn_create": [ctypes.POINTER(vp), i, i, i, i, i, i],
@@ -83,6 +99,18 @@ def load_library():
         "rnn_checkpoint_size": [i, i, psz],
         "rnn_checkpoint_store": [vp, i, i, i, vp, vp, sz],
         "rnn_checkpoint_load": [vp, i, i, i, vp, sz, vp],
+        "rnn_norm_workspace_size": [i, i, psz],
+        "rnn_norm_forward": [vp, i, i, i, i, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp],
+        "rnn_norm_backward": [vp, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz],
+        "rnn_conv_workspace_size": [i, i, i, i, psz],
+        "rnn_conv_forward": [vp, i, i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, ll, vp],
+        "rnn_conv_step": [vp, i, i, i, i, i, vp, ll, vp, vp, vp, vp, ll, vp],
+        "rnn_conv_backward": [vp, i, i, i, i, i, i, vp, ll, vp, vp, vp, vp, vp, ll, vp, vp, ll, vp, vp, vp, vp, sz],
+        "rnn_ssm_workspace_size": [i, i, i, i, i, i, psz],
+        "rnn_ssm_step": [vp, i, i, i, i, i, i, ctypes.POINTER(_SsmInputs), vp, vp, ll, vp],
+        "rnn_ssm_forward": [vp, i, i, i, i, i, i, i, i, ctypes.POINTER(_SsmInputs), vp, vp, vp, ll, vp, vp, sz],
+        "rnn_ssm_backward": [vp, i, i, i, i, i, i, i, ctypes.POINTER(_SsmInputs), vp, vp, ll, vp,
+                             ctypes.POINTER(_SsmGrads), vp, sz],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -96,7 +124,9 @@ def load_library():
         from . import _call
         _call.bind(*(ctypes.cast(getattr(lib, n), vp).value for n in (
             "rnn_scan_step", "rnn_scan_forward", "rnn_scan_backward", "rnn_ffn_forward", "rnn_ffn_backward",
-            "rnn_checkpoint_size", "rnn_checkpoint_store", "rnn_checkpoint_load")))
+            "rnn_checkpoint_size", "rnn_checkpoint_store", "rnn_checkpoint_load", "rnn_norm_forward", "rnn_norm_backward",
+            "rnn_conv_forward", "rnn_conv_step", "rnn_conv_backward", "rnn_ssm_forward", "rnn_ssm_step",
+            "rnn_ssm_backward")))
     except ImportError as e:      # built for another Python or torch: nothing else needs it
         _call = _Interpreted(e)
     _LIB, _CALL = lib, _call
@@ -610,6 +640,275 @@ def rnn_checkpoint_load(kept, x):
                                               _addr(x, "x", dev, dt, x.shape))
     if status:
         _check(status, "rnn_checkpoint_load")
+
+
+# ---------------------------------------- operators of a state-space block
+def _rows(t, name, dev, dtype, shape, optional=False):
+    """Address of ``t`` [T, B, width] or [B, width] and the elements between its
+    rows, which may lie apart (a slice of a wider tensor)."""
+    if t is None and optional:
+        return None, shape[-1]
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor" + (" or None" if optional else ""))
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor, on the same device as the others")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    width, st = shape[-1], t.stride()
+    if t.numel() == 0:
+        return t.data_ptr() or None, width
+    steps = [(n, s) for n, s in zip(shape[:-1], st[:-1]) if n > 1]
+    ld = width
+    if steps:
+        ld = steps[-1][1]
+        if len(steps) == 2 and steps[0][1] != steps[1][0] * ld:
+            raise ValueError(f"{name}'s rows must lie equally far apart")
+    if (width > 1 and st[-1] != 1) or ld < width:
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return t.data_ptr(), ld
+
+
+def rnn_norm_workspace_size(M: int, D: int) -> int:
+    """Bytes of the workspace of rnn_norm_backward."""
+    _ints(M, D)
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_norm_workspace_size(M, D, ctypes.byref(n)), "rnn_norm_workspace_size")
+    return n.value
+
+
+def rnn_norm_forward(kind, x, residual, weight, bias, y, total=None, stats=None, eps=1e-5):
+    """y = (s - m) * rstd * weight + bias for the rows of ``x`` [M, D]: kind
+    "layer" or "rms" (m = 0); s is x, or with ``residual`` x + residual rounded
+    to x's type, which ``total`` (or None; it may be x or residual itself) is
+    set to.  ``weight`` and ``bias`` [D] float32 or None; ``stats`` [M, 2]
+    float32 (or None): m and rstd, for rnn_norm_backward."""
+    status = (_CALL or _entries()).norm_forward(kind, x, residual, weight, bias, y, total, stats, eps)
+    if status == 0 or _done(status, "rnn_norm_forward"):
+        return
+    k = _choice(NORMS, kind, "kind")
+    dt, w, dev = _elements(x, "x", 2)
+    M, D = x.shape
+    f32 = torch.float32
+    status = (_LIB or load_library()).rnn_norm_forward(
+        _on(dev), k, w, M, D, _addr(x, "x", dev, dt, (M, D)), _addr(residual, "residual", dev, dt, (M, D), True),
+        _addr(weight, "weight", dev, f32, (D,), True), _addr(bias, "bias", dev, f32, (D,), True), float(eps),
+        _addr(y, "y", dev, dt, (M, D)), _addr(total, "total", dev, dt, (M, D), True),
+        _addr(stats, "stats", dev, f32, (M, 2), True))
+    if status:
+        _check(status, "rnn_norm_forward")
+
+
+def rnn_norm_backward(kind, s, weight, stats, dy, dtotal, dx, dweight, dbias, ws=None):
+    """Gradients of the rnn_norm_forward call that normalised ``s`` (its x, or
+    its total) and made ``stats``: ``dtotal`` (or None) is added to ``dx`` and
+    may be the same tensor; ``dx``, ``dweight`` and ``dbias`` may be None (not
+    wanted); ``ws`` is needed for the last two."""
+    status = (_CALL or _entries()).norm_backward(kind, s, weight, stats, dy, dtotal, dx, dweight, dbias, ws)
+    if status == 0 or _done(status, "rnn_norm_backward"):
+        return
+    k = _choice(NORMS, kind, "kind")
+    dt, w, dev = _elements(s, "s", 2)
+    M, D = s.shape
+    f32 = torch.float32
+    wp, wn = _room(ws, "ws", dev, True)
+    status = (_LIB or load_library()).rnn_norm_backward(
+        _on(dev), k, w, M, D, _addr(s, "s", dev, dt, (M, D)), _addr(weight, "weight", dev, f32, (D,), True),
+        _addr(stats, "stats", dev, f32, (M, 2)), _addr(dy, "dy", dev, dt, (M, D)),
+        _addr(dtotal, "dtotal", dev, dt, (M, D), True), _addr(dx, "dx", dev, dt, (M, D), True),
+        _addr(dweight, "dweight", dev, f32, (D,), True), _addr(dbias, "dbias", dev, f32, (D,), True), wp, wn)
+    if status:
+        _check(status, "rnn_norm_backward")
+
+
+def _conv_call(act, x, w, dims):
+    """The checks that the convolution's calls share: codes, sizes, device."""
+    a = _choice(CONV_ACTS, act, "act")
+    dt, wt, dev = _elements(x, "x", dims)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a tensor [C, K]")
+    C, K = x.shape[-1], w.shape[1]
+    _ints(K)
+    return a, dt, wt, dev, x.shape[-2], C, K, _addr(w, "w", dev, torch.float32, (C, K))
+
+
+def rnn_conv_forward(act, x, w, bias, s0, lengths, y, sy):
+    """Depthwise causal convolution over time, v[t] = bias + sum_k w[:, k] x[t - K + 1 + k],
+    y = v (act "none") or silu(v): ``x``, ``y`` [T, B, C] (rows may lie apart),
+    ``w`` [C, K] and ``bias`` [C] (or None) float32; ``s0`` (or None: zeros)
+    [K - 1, B, C]: the inputs before the first step; ``sy`` (or None) likewise
+    those before the step after the last, and may be s0 itself; ``lengths``
+    int32 [B] or None."""
+    status = (_CALL or _entries()).conv_forward(act, x, w, bias, s0, lengths, y, sy)
+    if status == 0 or _done(status, "rnn_conv_forward"):
+        return
+    a, dt, wt, dev, B, C, K, wp = _conv_call(act, x, w, 3)
+    T, st = x.shape[0], (max(K - 1, 0), B, C)
+    xp, ldx = _rows(x, "x", dev, dt, (T, B, C))
+    yp, ldy = _rows(y, "y", dev, dt, (T, B, C))
+    status = (_LIB or load_library()).rnn_conv_forward(
+        _on(dev), a, wt, T, B, C, K, xp, ldx, wp, _addr(bias, "bias", dev, torch.float32, (C,), True),
+        _addr(s0, "s0", dev, dt, st, True), _addr(lengths, "lengths", dev, torch.int32, (B,), True), yp, ldy,
+        _addr(sy, "sy", dev, dt, st, True))
+    if status:
+        _check(status, "rnn_conv_forward")
+
+
+def rnn_conv_step(act, x, w, bias, s, y, sy):
+    """One step of the convolution (a generated token): ``x``, ``y`` [B, C] (rows
+    may lie apart); ``s`` (or None: zeros) and ``sy`` [K - 1, B, C], which may be
+    the same tensor."""
+    status = (_CALL or _entries()).conv_step(act, x, w, bias, s, y, sy)
+    if status == 0 or _done(status, "rnn_conv_step"):
+        return
+    a, dt, wt, dev, B, C, K, wp = _conv_call(act, x, w, 2)
+    st = (max(K - 1, 0), B, C)
+    xp, ldx = _rows(x, "x", dev, dt, (B, C))
+    yp, ldy = _rows(y, "y", dev, dt, (B, C))
+    status = (_LIB or load_library()).rnn_conv_step(
+        _on(dev), a, wt, B, C, K, xp, ldx, wp, _addr(bias, "bias", dev, torch.float32, (C,), True),
+        _addr(s, "s", dev, dt, st, True), yp, ldy, _addr(sy, "sy", dev, dt, st, True))
+    if status:
+        _check(status, "rnn_conv_step")
+
+
+def rnn_conv_workspace_size(T: int, B: int, C: int, K: int) -> int:
+    """Bytes of the workspace of rnn_conv_backward."""
+    _ints(T, B, C, K)
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_conv_workspace_size(T, B, C, K, ctypes.byref(n)), "rnn_conv_workspace_size")
+    return n.value
+
+
+def rnn_conv_backward(act, x, w, bias, s0, lengths, dy, dsy, dx, dw, dbias, ds0, ws=None):
+    """Gradients of rnn_conv_forward: ``dy`` as y, ``dsy`` as sy or None (zeros);
+    ``dx``, ``dw``, ``dbias`` and ``ds0`` may be None (not wanted); ``ws`` is
+    needed for dw and dbias."""
+    status = (_CALL or _entries()).conv_backward(act, x, w, bias, s0, lengths, dy, dsy, dx, dw, dbias, ds0, ws)
+    if status == 0 or _done(status, "rnn_conv_backward"):
+        return
+    a, dt, wt, dev, B, C, K, wp = _conv_call(act, x, w, 3)
+    T, st, f32 = x.shape[0], (max(K - 1, 0), B, C), torch.float32
+    xp, ldx = _rows(x, "x", dev, dt, (T, B, C))
+    gp, ldg = _rows(dy, "dy", dev, dt, (T, B, C))
+    dp, ldd = _rows(dx, "dx", dev, dt, (T, B, C), True)
+    rp, rn = _room(ws, "ws", dev, True)
+    status = (_LIB or load_library()).rnn_conv_backward(
+        _on(dev), a, wt, T, B, C, K, xp, ldx, wp, _addr(bias, "bias", dev, f32, (C,), True),
+        _addr(s0, "s0", dev, dt, st, True), _addr(lengths, "lengths", dev, torch.int32, (B,), True), gp, ldg,
+        _addr(dsy, "dsy", dev, dt, st, True), dp, ldd, _addr(dw, "dw", dev, f32, (C, K), True),
+        _addr(dbias, "dbias", dev, f32, (C,), True), _addr(ds0, "ds0", dev, dt, st, True), rp, rn)
+    if status:
+        _check(status, "rnn_conv_backward")
+
+
+def _ssm_call(mode, u, delta, A, Bm, Cm, D, z, delta_bias, dims):
+    """The checks that the state-space calls share: codes, sizes, device, inputs."""
+    m = _choice(DELTAS, mode, "mode")
+    dt, wt, dev = _elements(u, "u", dims)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a tensor [E, N]")
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != dims:
+        raise ValueError(f"Bm must be a tensor of {dims} dimensions")
+    lead, E, N, GN, f32 = tuple(u.shape[:-1]), u.shape[-1], A.shape[1], Bm.shape[-1], torch.float32
+    if N < 1 or GN < 1 or GN % N:
+        raise ValueError("Bm must have a whole number of A's N columns")
+    _ints(N, GN)
+    args = _SsmInputs()
+    args.u, args.ldu = _rows(u, "u", dev, dt, lead + (E,))
+    args.delta, args.lddelta = _rows(delta, "delta", dev, dt, lead + (E,))
+    args.z, args.ldz = _rows(z, "z", dev, dt, lead + (E,), True)
+    args.Bm, args.ldB = _rows(Bm, "Bm", dev, dt, lead + (GN,))
+    args.Cm, args.ldC = _rows(Cm, "Cm", dev, dt, lead + (GN,))
+    args.A = _addr(A, "A", dev, f32, (E, N))
+    args.D = _addr(D, "D", dev, f32, (E,), True)
+    args.delta_bias = _addr(delta_bias, "delta_bias", dev, f32, (E,), True)
+    return m, dt, wt, dev, lead[-1], E, N, GN // N, args
+
+
+def rnn_ssm_workspace_size(T: int, B: int, E: int, N: int, groups: int = 1, save: str = "none") -> int:
+    """Bytes of the workspace of rnn_ssm_forward and, with save "full", of the
+    rnn_ssm_backward calls after it."""
+    _ints(T, B, E, N, groups)
+    n = ctypes.c_size_t()
+    _check(load_library().rnn_ssm_workspace_size(T, B, E, N, groups, _choice(SSM_SAVES, save, "save"), ctypes.byref(n)),
+           "rnn_ssm_workspace_size")
+    return n.value
+
+
+def rnn_ssm_forward(mode, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, hy, ws, save="none"):
+    """The selective state-space scan over ``u``, ``delta``, ``z`` [T, B, E]:
+    d = softplus(delta + delta_bias) (mode "linear": the sum itself),
+    h[n] = exp(d A[:, n]) h[n] + d u B[n], y = (sum_n C[n] h[n] + D u) silu(z).
+    ``Bm``, ``Cm`` [T, B, groups * N] (rows of these five and of ``y`` may lie
+    apart); ``A`` [E, N], ``D`` and ``delta_bias`` [E] float32; D, z and
+    delta_bias may be None; states ``h0`` (or None: zeros) and ``hy`` (or None)
+    [B, E, N] float32, which may be the same tensor; ``lengths`` int32 [B] or
+    None; save "full" where rnn_ssm_backward follows."""
+    status = (_CALL or _entries()).ssm_forward(mode, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, hy, ws, save)
+    if status == 0 or _done(status, "rnn_ssm_forward"):
+        return
+    sv = _choice(SSM_SAVES, save, "save")
+    m, dt, wt, dev, B, E, N, groups, args = _ssm_call(mode, u, delta, A, Bm, Cm, D, z, delta_bias, 3)
+    T, st = u.shape[0], (B, E, N)
+    yp, ldy = _rows(y, "y", dev, dt, (T, B, E))
+    wp, wn = _room(ws, "ws", dev)
+    status = (_LIB or load_library()).rnn_ssm_forward(
+        _on(dev), m, wt, sv, T, B, E, N, groups, ctypes.byref(args), _addr(h0, "h0", dev, torch.float32, st, True),
+        _addr(lengths, "lengths", dev, torch.int32, (B,), True), yp, ldy, _addr(hy, "hy", dev, torch.float32, st, True), wp, wn)
+    if status:
+        _check(status, "rnn_ssm_forward")
+
+
+def rnn_ssm_step(mode, u, delta, A, Bm, Cm, D, z, delta_bias, h, y, hy):
+    """One step of the state-space scan (a generated token): ``u``, ``delta``,
+    ``z``, ``y`` [B, E], ``Bm``, ``Cm`` [B, groups * N]; ``h`` (or None: zeros)
+    and ``hy`` [B, E, N] float32, which may be the same tensor."""
+    status = (_CALL or _entries()).ssm_step(mode, u, delta, A, Bm, Cm, D, z, delta_bias, h, y, hy)
+    if status == 0 or _done(status, "rnn_ssm_step"):
+        return
+    m, dt, wt, dev, B, E, N, groups, args = _ssm_call(mode, u, delta, A, Bm, Cm, D, z, delta_bias, 2)
+    yp, ldy = _rows(y, "y", dev, dt, (B, E))
+    status = (_LIB or load_library()).rnn_ssm_step(
+        _on(dev), m, wt, B, E, N, groups, ctypes.byref(args), _addr(h, "h", dev, torch.float32, (B, E, N), True), yp, ldy,
+        _addr(hy, "hy", dev, torch.float32, (B, E, N), True))
+    if status:
+        _check(status, "rnn_ssm_step")
+
+
+def rnn_ssm_backward(mode, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, dy, dhy, du, ddelta, dA, dBm, dCm, dD, dz,
+                     ddelta_bias, dh0, ws):
+    """Gradients of the rnn_ssm_forward call with save "full" that filled ``ws``
+    (same mode, inputs, h0, which is checked but not read, and lengths): ``dy``
+    as y, ``dhy`` as hy or None (zeros); each gradient has its input's shape
+    and type and may be None (not wanted); dh0 may be dhy itself."""
+    status = (_CALL or _entries()).ssm_backward(mode, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, dy, dhy, du, ddelta,
+                                                dA, dBm, dCm, dD, dz, ddelta_bias, dh0, ws)
+    if status == 0 or _done(status, "rnn_ssm_backward"):
+        return
+    m, dt, wt, dev, B, E, N, groups, args = _ssm_call(mode, u, delta, A, Bm, Cm, D, z, delta_bias, 3)
+    T, st, f32 = u.shape[0], (B, E, N), torch.float32
+    _addr(h0, "h0", dev, f32, st, True)
+    gp, ldg = _rows(dy, "dy", dev, dt, (T, B, E))
+    if dz is not None and z is None:
+        raise ValueError("dz without z")
+    g = _SsmGrads()
+    g.du, g.lddu = _rows(du, "du", dev, dt, (T, B, E), True)
+    g.ddelta, g.ldddelta = _rows(ddelta, "ddelta", dev, dt, (T, B, E), True)
+    g.dz, g.lddz = _rows(dz, "dz", dev, dt, (T, B, E), True)
+    g.dBm, g.lddB = _rows(dBm, "dBm", dev, dt, (T, B, groups * N), True)
+    g.dCm, g.lddC = _rows(dCm, "dCm", dev, dt, (T, B, groups * N), True)
+    g.dA = _addr(dA, "dA", dev, f32, (E, N), True)
+    g.dD = _addr(dD, "dD", dev, f32, (E,), True)
+    g.ddelta_bias = _addr(ddelta_bias, "ddelta_bias", dev, f32, (E,), True)
+    g.dh0 = _addr(dh0, "dh0", dev, f32, st, True)
+    wp, wn = _room(ws, "ws", dev)
+    status = (_LIB or load_library()).rnn_ssm_backward(
+        _on(dev), m, wt, T, B, E, N, groups, ctypes.byref(args), _addr(lengths, "lengths", dev, torch.int32, (B,), True), gp, ldg,
+        _addr(dhy, "dhy", dev, f32, st, True), ctypes.byref(g), wp, wn)
+    if status:
+        _check(status, "rnn_ssm_backward")
 
 
 # ------------------------------------------------------------ weight packing

@@ -16,8 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "librnn_mi355x.so")
-SOURCES = ["checkpoint.hip", "dropout.hip", "ffn.hip", "ffn_dglu.hip", "ffn_glu.hip", "ffn_rows.hip", "gemm.hip", "layout.hip", "lm_api.cpp", "recurrent.hip",
-           "recurrent_gru2.hip", "rnn_api.cpp", "scan.hip",
+SOURCES = ["checkpoint.hip", "conv.hip", "dropout.hip", "ffn.hip", "ffn_dglu.hip", "ffn_glu.hip", "ffn_rows.hip", "gemm.hip", "layout.hip", "lm_api.cpp", "norm.hip", "recurrent.hip",
+           "recurrent_gru2.hip", "rnn_api.cpp", "scan.hip", "ssm.hip", "ssm_api.cpp", "ssm_bwd.hip",
            *[f"recurrent_{m}_{k}.hip" for m in ("tanh", "lstm", "gru") for k in ("fwd", "bwd")]]
 CALL_LIB = os.path.join(PKG, "_call.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

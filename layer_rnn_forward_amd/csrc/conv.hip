@@ -1,0 +1,318 @@
+// Depthwise causal convolution over time (gfx950): v_t = bias +
+// sum_k w[c, k] x_(t - K + 1 + k), y = v or silu(v), its gradients, and its
+// form for single steps.
+//
+// A lane holds VW neighbouring channels and walks a piece of the time axis with
+// the last K inputs in registers, so an input is read once, and again only by
+// the piece that follows (K - 1 steps).  Backward walks K - 1 steps further
+// than its piece, which makes the v' that its last inputs need, keeps the last
+// K of them, and sums the weights' gradients over its own steps; pieces' sums
+// are added in a second launch, in a fixed order.
+#include <algorithm>
+
+#include "ssm_common.h"
+
+using namespace rnnk;
+
+namespace {
+
+constexpr int kWidth = 4;     // channels of a lane
+constexpr int kAhead = 4;     // steps whose loads are asked for at once
+
+// silu and its slope
+__device__ __forceinline__ float silu(float v) {
+  float a, da;
+  act_pair<ACT_SILU>(v, a, da);
+  return a;
+}
+
+struct Place {
+  int c, left;               // first channel, channels from there on
+  int b, len;
+  int t0, t1;                // steps of the piece
+};
+template <int VW>
+__device__ __forceinline__ Place place(const ConvParams& p) {
+  Place r;
+  const int tiles = (p.C + 64 * VW - 1) / (64 * VW), groups = (p.pieces + kConvWaves - 1) / kConvWaves;
+  int i = blockIdx.x;
+  const int tile = i % tiles;
+  i /= tiles;
+  r.b = i % p.B;
+  const int piece = i / p.B * kConvWaves + (int)(threadIdx.x >> 6);
+  (void)groups;
+  r.c = (tile * 64 + (int)(threadIdx.x & 63)) * VW;
+  r.left = p.C - r.c;
+  r.t0 = piece * p.piece;
+  r.t1 = min(r.t0 + p.piece, p.T);
+  if (piece >= p.pieces) r.t0 = r.t1 = -1;
+  r.len = p.lengths ? min(max(p.lengths[r.b], 0), p.T) : p.T;
+  return r;
+}
+
+template <int K, int VW>
+__device__ __forceinline__ void load_weights(const ConvParams& p, const Place& at, float (&w)[K][VW], float (&bias)[VW]) {
+#pragma unroll
+  for (int j = 0; j < VW; ++j) {
+    const bool on = j < at.left;
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][j] = on ? p.w[(long long)(at.c + j) * K + k] : 0.f;
+    bias[j] = on && p.bias ? p.bias[at.c + j] : 0.f;
+  }
+}
+
+// input of step t >= -(K - 1); steps past the row's length are not used
+template <bool BF, int K, int VW>
+__device__ __forceinline__ void input(const ConvParams& p, const Place& at, int t, float (&v)[VW]) {
+  if (t >= 0) {
+    load_piece<BF, VW>((const El<BF>*)p.x + ((long long)t * p.B + at.b) * p.ldx + at.c, t < at.len ? at.left : 0, v);
+  } else {
+    load_piece<BF, VW>((const El<BF>*)p.s0 + ((long long)(t + K - 1) * p.B + at.b) * p.C + at.c, p.s0 ? at.left : 0, v);
+  }
+}
+
+// the inputs before the step that follows the row's last
+template <bool BF, int K, int VW>
+__device__ __forceinline__ void last_inputs(const ConvParams& p, const Place& at) {
+  if constexpr (K > 1) {
+    float v[K - 1][VW];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) input<BF, K, VW>(p, at, at.len - (K - 1) + j, v[j]);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) store_piece<BF, VW>((El<BF>*)p.sy + ((long long)j * p.B + at.b) * p.C + at.c, at.left, v[j]);
+  }
+}
+
+template <bool BF, int K>
+__global__ __launch_bounds__(64 * kConvWaves) void fwd_kernel(const ConvParams p) {
+  constexpr int VW = kWidth;
+  const Place at = place<VW>(p);
+  if (at.t0 < 0 || at.left <= 0) return;
+  float w[K][VW], bias[VW], x[K][VW];
+  load_weights<K, VW>(p, at, w, bias);
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) input<BF, K, VW>(p, at, at.t0 - (K - 1) + k, x[k + 1]);
+  for (int t = at.t0; t < at.t1; t += kAhead) {
+    float in[kAhead][VW];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (t + i < at.t1) input<BF, K, VW>(p, at, t + i, in[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (t + i >= at.t1) break;
+      float v[VW];
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k) x[k][j] = x[k + 1][j];
+        x[K - 1][j] = in[i][j];
+        v[j] = bias[j];
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[j] = fmaf(w[k][j], x[k][j], v[j]);
+        if (p.silu) v[j] = silu(v[j]);
+        if (t + i >= at.len) v[j] = 0.f;
+      }
+      store_piece<BF, VW>((El<BF>*)p.y + ((long long)(t + i) * p.B + at.b) * p.ldy + at.c, at.left, v);
+    }
+  }
+  // s0 is read by the first piece alone, so sy may take its place
+  if (p.sy && at.t0 == 0) last_inputs<BF, K, VW>(p, at);
+}
+
+template <bool BF, int K>
+__global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p) {
+  constexpr int VW = kWidth;
+  const Place at = place<VW>(p);
+  __shared__ float sums[kConvWaves][K + 1][64 * VW];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float dw[K][VW], db[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) {
+    db[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) dw[k][j] = 0.f;
+  }
+  if (at.t0 >= 0 && at.left > 0) {
+    float w[K][VW], bias[VW], x[K][VW], dv[K][VW];
+    load_weights<K, VW>(p, at, w, bias);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < VW; ++j) dv[k][j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) input<BF, K, VW>(p, at, at.t0 - (K - 1) + k, x[k + 1]);
+    // after step t the gradient of input t - K + 1 is whole
+    const int end = at.t1 + K - 1;
+    for (int t = at.t0; t < end; t += kAhead) {
+      float in[kAhead][VW], dy[kAhead][VW];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i < p.T && t + i < end) {
+          input<BF, K, VW>(p, at, t + i, in[i]);
+          load_piece<BF, VW>((const El<BF>*)p.dy + ((long long)(t + i) * p.B + at.b) * p.lddy + at.c, t + i < at.len ? at.left : 0, dy[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VW; ++j) in[i][j] = dy[i][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i >= end) break;
+        const int s = t + i - (K - 1);      // the input whose gradient is whole
+        const bool mine = t + i < at.t1;
+        float dx[VW], more[VW];
+        const int j0 = s - at.len + K - 1;
+        const bool last = p.dsy && j0 >= 0 && j0 < K - 1 && (s >= at.t0 || at.t0 == 0);
+        if (last) load_piece<BF, VW>((const El<BF>*)p.dsy + ((long long)j0 * p.B + at.b) * p.C + at.c, at.left, more);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) x[k][j] = x[k + 1][j];
+          x[K - 1][j] = in[i][j];
+          float d = dy[i][j];
+          if (p.silu) {
+            float v = bias[j], a, da;
+#pragma unroll
+            for (int k = 0; k < K; ++k) v = fmaf(w[k][j], x[k][j], v);
+            act_pair<ACT_SILU>(v, a, da);
+            d = t + i < at.len ? d * da : 0.f;
+          }
+#pragma unroll
+          for (int k = K - 1; k > 0; --k) dv[k][j] = dv[k - 1][j];
+          dv[0][j] = d;
+          if (mine) {
+            db[j] += d;
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k][j] = fmaf(d, x[k][j], dw[k][j]);
+          }
+          dx[j] = last ? more[j] : 0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) dx[j] = fmaf(w[k][j], dv[k][j], dx[j]);
+        }
+        if (s >= at.t0) {
+          if (p.dx) store_piece<BF, VW>((El<BF>*)p.dx + ((long long)s * p.B + at.b) * p.lddx + at.c, at.left, dx);
+        } else if (at.t0 == 0 && p.ds0) {
+          store_piece<BF, VW>((El<BF>*)p.ds0 + ((long long)(s + K - 1) * p.B + at.b) * p.C + at.c, at.left, dx);
+        }
+      }
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int j = 0; j < VW; ++j) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) sums[wave][k][lane * VW + j] = dw[k][j];
+    sums[wave][K][lane * VW + j] = db[j];
+  }
+  __syncthreads();
+  const int tiles = (p.C + 64 * VW - 1) / (64 * VW), tile = blockIdx.x % tiles;
+  float* to = p.part + (long long)(blockIdx.x / tiles) * (K + 1) * p.C;
+  for (int i = threadIdx.x; i < (K + 1) * 64 * VW; i += 64 * kConvWaves) {
+    const int k = i / (64 * VW), c = i - k * (64 * VW);
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kConvWaves; ++q) s += sums[q][k][c];
+    if (tile * 64 * VW + c < p.C) to[(long long)k * p.C + tile * 64 * VW + c] = s;
+  }
+}
+
+// the pieces' sums: 64 channels a workgroup, a quarter of the pieces a wave
+__global__ __launch_bounds__(256) void sum_kernel(const ConvParams p, int rows) {
+  __shared__ float lds[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long long n = (long long)(p.K + 1) * p.C, i = (long long)blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (i < n)
+    for (int r = wave; r < rows; r += 4) s += p.part[r * n + i];
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave || i >= n) return;
+  s = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+  const int k = (int)(i / p.C), c = (int)(i - (long long)k * p.C);
+  if (k == p.K) {
+    if (p.dbias) p.dbias[c] = s;
+  } else if (p.dw) {
+    p.dw[(long long)c * p.K + k] = s;
+  }
+}
+
+template <bool BF, int K>
+__global__ __launch_bounds__(256) void step_kernel(const ConvParams p) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)p.B * p.C) return;
+  const int b = (int)(i / p.C), c = (int)(i - (long long)b * p.C);
+  const long long n = (long long)p.B * p.C;
+  El<BF> x[K];
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) x[k] = p.s0 ? ((const El<BF>*)p.s0)[k * n + i] : El<BF>(0);
+  x[K - 1] = ((const El<BF>*)p.x)[b * p.ldx + c];
+  float v = p.bias ? p.bias[c] : 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v = fmaf(p.w[(long long)c * K + k], el_load<BF>(&x[k]), v);
+  if (p.silu) v = silu(v);
+  if (p.sy)
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) ((El<BF>*)p.sy)[k * n + i] = x[k + 1];
+  el_store<BF>((El<BF>*)p.y + b * p.ldy + c, v);
+}
+
+enum Pass { FWD, BWD, STEP };
+template <bool BF, int K>
+void start(const ConvParams& p, Pass what, hipStream_t s) {
+  if (what == STEP) {
+    hipLaunchKernelGGL((step_kernel<BF, K>), dim3((unsigned)(((long long)p.B * p.C + 255) / 256)), dim3(256), 0, s, p);
+    return;
+  }
+  const long long tiles = (p.C + 64 * kWidth - 1) / (64 * kWidth), groups = (p.pieces + kConvWaves - 1) / kConvWaves;
+  const dim3 grid((unsigned)(tiles * p.B * groups)), block(64 * kConvWaves);
+  if (what == FWD) hipLaunchKernelGGL((fwd_kernel<BF, K>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((bwd_kernel<BF, K>), grid, block, 0, s, p);
+}
+
+template <bool BF>
+void pick(const ConvParams& p, Pass what, hipStream_t s) {
+  switch (p.K) {
+    case 1: return start<BF, 1>(p, what, s);
+    case 2: return start<BF, 2>(p, what, s);
+    case 3: return start<BF, 3>(p, what, s);
+    case 4: return start<BF, 4>(p, what, s);
+    case 5: return start<BF, 5>(p, what, s);
+    case 6: return start<BF, 6>(p, what, s);
+    case 7: return start<BF, 7>(p, what, s);
+    default: return start<BF, 8>(p, what, s);
+  }
+}
+
+hipError_t launch(const ConvParams& p, Pass what, int bf16, hipStream_t s) {
+  if (p.B == 0 || p.C == 0) return hipSuccess;
+  const long long tiles = (p.C + 64 * kWidth - 1) / (64 * kWidth), groups = (p.pieces + kConvWaves - 1) / kConvWaves;
+  if (what != STEP && tiles * p.B * groups > 0x7fffffffLL) return hipErrorInvalidValue;
+  if (bf16) pick<true>(p, what, s);
+  else pick<false>(p, what, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// steps of a wave's piece (at least K - 1 of them)
+int rnnk::conv_piece(int T, int B, int C, bool) {
+  const long long waves = (long long)B * ((C + 64 * kWidth - 1) / (64 * kWidth));
+  int piece = 32;
+  while (piece > 8 && waves * ((T + piece - 1) / piece) < 2048) piece /= 2;
+  return piece;
+}
+
+hipError_t rnn_launch_conv_fwd(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, FWD, bf16, s); }
+hipError_t rnn_launch_conv_step(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, STEP, bf16, s); }
+hipError_t rnn_launch_conv_bwd(const ConvParams& q, int bf16, hipStream_t s) {
+  ConvParams p = q;
+  const bool sums = p.dw || p.dbias;
+  if (!sums) p.part = nullptr;
+  if (p.B == 0 || p.C == 0) p.pieces = 0;
+  const hipError_t e = launch(p, BWD, bf16, s);
+  if (e != hipSuccess || !sums || p.C == 0) return e;
+  const int rows = p.B * ((p.pieces + kConvWaves - 1) / kConvWaves);
+  hipLaunchKernelGGL(sum_kernel, dim3((unsigned)(((long long)(p.K + 1) * p.C + 63) / 64)), dim3(256), 0, s, p, rows);
+  return hipGetLastError();
+}

@@ -1,0 +1,248 @@
+// C ABI of the operators of a state-space block (normalisation, causal
+// convolution, selective state-space scan): argument checks, workspace
+// layouts, launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "rnn.h"
+#include "ssm_common.h"
+
+using namespace rnnk;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+inline bool aligned(const void* p) { return ((uintptr_t)p & (kAlign - 1)) == 0; }
+
+rnn_status_t dev(hipError_t e) { return e == hipSuccess ? RNN_STATUS_SUCCESS : RNN_STATUS_DEVICE; }
+inline hipStream_t hs(void* s) { return reinterpret_cast<hipStream_t>(s); }
+
+#define LM_TRY(expr)                                 \
+  do {                                               \
+    const rnn_status_t st_ = (expr);                 \
+    if (st_ != RNN_STATUS_SUCCESS) return st_;       \
+  } while (0)
+
+bool wtype_ok(int w) { return w == RNN_W_F32 || w == RNN_W_BF16; }
+
+rnn_status_t room(const void* ws, size_t have, size_t need) {
+  if (!ws || !aligned(ws)) return RNN_STATUS_INVALID_ARG;
+  return have < need ? RNN_STATUS_WORKSPACE_TOO_SMALL : RNN_STATUS_SUCCESS;
+}
+
+// ------------------------------------------------------------------- norm
+rnn_status_t norm_sizes(int M, int D) {
+  if (M < 0 || D < 0) return RNN_STATUS_INVALID_ARG;
+  return D >= (1 << 20) || M >= (1 << 30) ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
+}
+bool norm_ok(int kind, int wtype) { return (kind == RNN_NORM_LAYER || kind == RNN_NORM_RMS) && wtype_ok(wtype); }
+size_t norm_bytes(int M, int D) { return std::max(kAlign, align_up((size_t)norm_parts(M, D) * 2 * D * 4)); }
+
+// ------------------------------------------------------------------- conv
+rnn_status_t conv_sizes(int T, int B, int C, int K) {
+  if (T < 0 || B < 0 || C < 0 || K < 1) return RNN_STATUS_INVALID_ARG;
+  if (K > kConvMost || (long long)B * C >= (1LL << 30) || T >= (1 << 30)) return RNN_STATUS_UNSUPPORTED;
+  // workgroups of a launch, and rows of partial sums
+  if ((long long)B * (C / 64 + 1) * (T / 32 + 1) >= (1LL << 31)) return RNN_STATUS_UNSUPPORTED;
+  return RNN_STATUS_SUCCESS;
+}
+bool conv_ok(int act, int wtype) { return (act == RNN_ACT_NONE || act == RNN_ACT_SILU) && wtype_ok(wtype); }
+
+ConvParams conv_params(int act, int T, int B, int C, int K, bool back) {
+  ConvParams p{};
+  p.T = T; p.B = B; p.C = C; p.K = K;
+  p.silu = act == RNN_ACT_SILU;
+  p.piece = conv_piece(T, B, C, back);
+  p.pieces = std::max(1, (T + p.piece - 1) / p.piece);
+  return p;
+}
+size_t conv_bytes(int T, int B, int C, int K) {
+  const ConvParams p = conv_params(RNN_ACT_NONE, T, B, C, K, true);
+  return std::max(kAlign, align_up((size_t)((p.pieces + kConvWaves - 1) / kConvWaves) * B * (K + 1) * C * 4));
+}
+
+// -------------------------------------------------------------------- ssm
+rnn_status_t ssm_sizes(int T, int B, int E, int N, int groups) {
+  if (T < 0 || B < 0 || E < 0 || N < 1 || groups < 1 || E % groups) return RNN_STATUS_INVALID_ARG;
+  if (N > kSsmStates || (long long)B * E >= (1 << 24) || T >= (1 << 30) || (long long)groups * N >= (1 << 20)) return RNN_STATUS_UNSUPPORTED;
+  // the launch over dB and dC
+  return (double)T * B * groups * N >= 0x1p37 ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
+}
+bool ssm_ok(int mode, int wtype) { return (mode == RNN_DELTA_SOFTPLUS || mode == RNN_DELTA_LINEAR) && wtype_ok(wtype); }
+
+size_t ssm_starts(int T, int B, int E, int N) { return align_up(ssm_start_floats(T, B, E, N) * 4); }
+size_t ssm_bytes(int T, int B, int E, int N, int groups, int save) {
+  if (save == RNN_SAVE_NONE) return kAlign;
+  return std::max(kAlign, ssm_starts(T, B, E, N) + align_up(ssm_part_floats(T, B, E, N, groups) * 4));
+}
+
+// the inputs' checks; they are needed where there are steps
+rnn_status_t ssm_inputs(SsmParams& p, const rnn_ssm_inputs_t* in, int mode, int T, int B, int E, int N, int groups) {
+  if (!in || !in->A) return RNN_STATUS_INVALID_ARG;
+  if (T > 0 && (!in->u || !in->delta || !in->Bm || !in->Cm)) return RNN_STATUS_INVALID_ARG;
+  const long long GN = (long long)groups * N;
+  if (in->ldu < E || in->lddelta < E || (in->z && in->ldz < E) || in->ldB < GN || in->ldC < GN) return RNN_STATUS_INVALID_ARG;
+  p.T = T; p.B = B; p.E = E; p.N = N; p.G = groups;
+  p.softplus = mode == RNN_DELTA_SOFTPLUS;
+  p.u = in->u; p.delta = in->delta; p.z = in->z; p.Bm = in->Bm; p.Cm = in->Cm;
+  p.ldu = in->ldu; p.lddelta = in->lddelta; p.ldz = in->ldz; p.ldB = in->ldB; p.ldC = in->ldC;
+  p.A = in->A; p.D = in->D; p.delta_bias = in->delta_bias;
+  return RNN_STATUS_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+rnn_status_t rnn_norm_workspace_size(int M, int D, size_t* bytes) {
+  if (!bytes) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(norm_sizes(M, D));
+  *bytes = norm_bytes(M, D);
+  return RNN_STATUS_SUCCESS;
+}
+
+rnn_status_t rnn_norm_forward(void* stream, rnn_norm_t kind, rnn_wtype_t wtype, int M, int D, const void* x,
+                              const void* residual, const float* weight, const float* bias, float eps, void* y,
+                              void* total, float* stats) {
+  if (!norm_ok(kind, wtype) || !(eps >= 0.f) || !std::isfinite(eps)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(norm_sizes(M, D));
+  if (M == 0 || D == 0) return RNN_STATUS_SUCCESS;
+  if (!x || !y) return RNN_STATUS_INVALID_ARG;
+  NormParams p{};
+  p.M = M; p.D = D; p.rms = kind == RNN_NORM_RMS; p.eps = eps;
+  p.x = x; p.residual = residual; p.weight = weight; p.bias = bias;
+  p.y = y; p.total = total; p.stats = stats;
+  return dev(rnn_launch_norm_fwd(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_norm_backward(void* stream, rnn_norm_t kind, rnn_wtype_t wtype, int M, int D, const void* s,
+                               const float* weight, const float* stats, const void* dy, const void* dtotal, void* dx,
+                               float* dweight, float* dbias, void* ws, size_t ws_bytes) {
+  if (!norm_ok(kind, wtype)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(norm_sizes(M, D));
+  if (dweight || dbias) LM_TRY(room(ws, ws_bytes, norm_bytes(M, D)));
+  if (D == 0) return RNN_STATUS_SUCCESS;
+  if (M > 0 && (!s || !stats || !dy)) return RNN_STATUS_INVALID_ARG;
+  NormParams p{};
+  p.M = M; p.D = D; p.rms = kind == RNN_NORM_RMS;
+  p.x = s; p.weight = weight; p.stats = const_cast<float*>(stats);   // read only
+  p.dy = dy; p.dtotal = dtotal; p.dx = dx; p.dweight = dweight; p.dbias = dbias;
+  p.part = (float*)ws;
+  return dev(rnn_launch_norm_bwd(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_conv_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, int T, int B, int C, int K,
+                              const void* x, long long ldx, const float* w, const float* bias, const void* s0,
+                              const int* lengths, void* y, long long ldy, void* sy) {
+  if (!conv_ok(act, wtype)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(conv_sizes(T, B, C, K));
+  if (ldx < C || ldy < C) return RNN_STATUS_INVALID_ARG;
+  if (B == 0 || C == 0) return RNN_STATUS_SUCCESS;
+  if (!w || (T > 0 && (!x || !y))) return RNN_STATUS_INVALID_ARG;
+  ConvParams p = conv_params(act, T, B, C, K, false);
+  p.x = x; p.ldx = ldx; p.w = w; p.bias = bias; p.s0 = s0; p.lengths = lengths;
+  p.y = y; p.ldy = ldy; p.sy = sy;
+  return dev(rnn_launch_conv_fwd(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_conv_step(void* stream, rnn_act_t act, rnn_wtype_t wtype, int B, int C, int K, const void* x,
+                           long long ldx, const float* w, const float* bias, const void* s, void* y, long long ldy,
+                           void* sy) {
+  if (!conv_ok(act, wtype)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(conv_sizes(1, B, C, K));
+  if (ldx < C || ldy < C) return RNN_STATUS_INVALID_ARG;
+  if (B == 0 || C == 0) return RNN_STATUS_SUCCESS;
+  if (!w || !x || !y) return RNN_STATUS_INVALID_ARG;
+  ConvParams p = conv_params(act, 1, B, C, K, false);
+  p.x = x; p.ldx = ldx; p.w = w; p.bias = bias; p.s0 = s;
+  p.y = y; p.ldy = ldy; p.sy = sy;
+  return dev(rnn_launch_conv_step(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_conv_workspace_size(int T, int B, int C, int K, size_t* bytes) {
+  if (!bytes) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(conv_sizes(T, B, C, K));
+  *bytes = conv_bytes(T, B, C, K);
+  return RNN_STATUS_SUCCESS;
+}
+
+rnn_status_t rnn_conv_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, int T, int B, int C, int K,
+                               const void* x, long long ldx, const float* w, const float* bias, const void* s0,
+                               const int* lengths, const void* dy, long long lddy, const void* dsy, void* dx,
+                               long long lddx, float* dw, float* dbias, void* ds0, void* ws, size_t ws_bytes) {
+  if (!conv_ok(act, wtype)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(conv_sizes(T, B, C, K));
+  if (ldx < C || lddy < C || (dx && lddx < C)) return RNN_STATUS_INVALID_ARG;
+  if (dw || dbias) LM_TRY(room(ws, ws_bytes, conv_bytes(T, B, C, K)));
+  if (C == 0) return RNN_STATUS_SUCCESS;
+  if (B > 0 && (!w || (T > 0 && (!x || !dy)))) return RNN_STATUS_INVALID_ARG;
+  ConvParams p = conv_params(act, T, B, C, K, true);
+  p.x = x; p.ldx = ldx; p.w = w; p.bias = bias; p.s0 = s0; p.lengths = lengths;
+  p.dy = dy; p.lddy = lddy; p.dsy = dsy;
+  p.dx = dx; p.lddx = lddx; p.dw = dw; p.dbias = dbias; p.ds0 = ds0;
+  p.part = (float*)ws;
+  return dev(rnn_launch_conv_bwd(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_ssm_step(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int B, int E, int N, int groups,
+                          const rnn_ssm_inputs_t* in, const float* h, void* y, long long ldy, float* hy) {
+  if (!ssm_ok(mode, wtype)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_sizes(1, B, E, N, groups));
+  if (B == 0 || E == 0) return RNN_STATUS_SUCCESS;
+  SsmParams p{};
+  LM_TRY(ssm_inputs(p, in, mode, 1, B, E, N, groups));
+  if (!y || ldy < E) return RNN_STATUS_INVALID_ARG;
+  p.h0 = h; p.y = y; p.ldy = ldy; p.hy = hy;
+  return dev(rnn_launch_ssm_step(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_ssm_workspace_size(int T, int B, int E, int N, int groups, rnn_save_t save, size_t* bytes) {
+  if (!bytes || (save != RNN_SAVE_NONE && save != RNN_SAVE_FULL)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_sizes(T, B, E, N, groups));
+  *bytes = ssm_bytes(T, B, E, N, groups, save);
+  return RNN_STATUS_SUCCESS;
+}
+
+rnn_status_t rnn_ssm_forward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, rnn_save_t save, int T, int B, int E,
+                             int N, int groups, const rnn_ssm_inputs_t* in, const float* h0, const int* lengths,
+                             void* y, long long ldy, float* hy, void* ws, size_t ws_bytes) {
+  if (!ssm_ok(mode, wtype) || (save != RNN_SAVE_NONE && save != RNN_SAVE_FULL)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_sizes(T, B, E, N, groups));
+  LM_TRY(room(ws, ws_bytes, ssm_bytes(T, B, E, N, groups, save)));
+  if (B == 0 || E == 0) return RNN_STATUS_SUCCESS;
+  SsmParams p{};
+  LM_TRY(ssm_inputs(p, in, mode, T, B, E, N, groups));
+  if (ldy < E || (T > 0 && !y)) return RNN_STATUS_INVALID_ARG;
+  p.h0 = h0; p.lengths = lengths; p.y = y; p.ldy = ldy; p.hy = hy;
+  p.starts = save == RNN_SAVE_FULL ? (float*)ws : nullptr;
+  return dev(rnn_launch_ssm_fwd(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+rnn_status_t rnn_ssm_backward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int T, int B, int E, int N,
+                              int groups, const rnn_ssm_inputs_t* in, const int* lengths, const void* dy,
+                              long long lddy, const float* dhy, const rnn_ssm_grads_t* grads, void* ws,
+                              size_t ws_bytes) {
+  if (!ssm_ok(mode, wtype) || !grads) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_sizes(T, B, E, N, groups));
+  LM_TRY(room(ws, ws_bytes, ssm_bytes(T, B, E, N, groups, RNN_SAVE_FULL)));
+  if (E == 0) return RNN_STATUS_SUCCESS;
+  SsmParams p{};
+  LM_TRY(ssm_inputs(p, in, mode, B > 0 ? T : 0, B, E, N, groups));
+  const long long GN = (long long)groups * N;
+  const rnn_ssm_grads_t& g = *grads;
+  if (lddy < E || (B > 0 && T > 0 && !dy) || (g.dz && !in->z) || (g.du && g.lddu < E) || (g.ddelta && g.ldddelta < E) ||
+      (g.dz && g.lddz < E) || (g.dBm && g.lddB < GN) || (g.dCm && g.lddC < GN))
+    return RNN_STATUS_INVALID_ARG;
+  p.lengths = lengths; p.dy = dy; p.lddy = lddy; p.dhy = dhy;
+  p.du = g.du; p.ddelta = g.ddelta; p.dz = g.dz; p.dBm = g.dBm; p.dCm = g.dCm;
+  p.lddu = g.lddu; p.ldddelta = g.ldddelta; p.lddz = g.lddz; p.lddB = g.lddB; p.lddC = g.lddC;
+  p.dA = g.dA; p.dD = g.dD; p.ddelta_bias = g.ddelta_bias; p.dh0 = g.dh0;
+  p.starts = (float*)ws;
+  p.part = (float*)((char*)ws + ssm_starts(T, B, E, N));
+  return dev(rnn_launch_ssm_bwd(p, wtype == RNN_W_BF16, hs(stream)));
+}
+
+}  // extern "C"

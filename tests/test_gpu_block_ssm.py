@@ -1,0 +1,150 @@
+"""Selective state-space scan on the GPU against the definition in 64 bits; tolerances are the oracle's bounds on an
+evaluation in fp32 and half a step of the output's type."""
+
+import pytest
+import torch
+
+import layer_rnn_forward_amd as R
+from oracle.bounds import check
+from tests.block_gpu import INPUTS, gpu, room, ssm_case, ssm_run, ssm_want
+
+pytestmark = pytest.mark.gpu
+FP32 = ("hy", "dA", "dD", "ddelta_bias", "dh0")
+
+
+def compare(mode, c, dtype, wide=0, backward=True):
+    got, want = ssm_run(mode, c, wide, backward), ssm_want(mode, c, backward)
+    assert set(got) == set(want)
+    for k, v in want.items():
+        check(k, got[k], v, "f32" if k in FP32 else dtype)
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,E,N,G", [(1, 1, 1, 1, 1), (3, 2, 5, 4, 1), (5, 2, 16, 16, 1), (64, 1, 17, 16, 1), (65, 2, 33, 16, 1), (130, 2, 20, 8, 1),
+                                       (100, 1, 70, 3, 1), (40, 2, 24, 13, 3), (70, 3, 12, 32, 2), (66, 1, 9, 64, 1), (63, 2, 40, 5, 4),
+                                       (200, 1, 64, 16, 2), (50, 1, 8, 41, 1)])
+def test_sequences(dtype, T, B, E, N, G):
+    print("CASE ssm", dtype, T, B, E, N, G, flush=True)
+    compare("softplus", ssm_case(T, B, E, N, G, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [2, 7, 16, 30, 50])
+def test_steps_as_given(dtype, N):
+    """Linear d, without the gate, and without bias and skip."""
+    compare("linear", ssm_case(90, 2, 19, N, 1, dtype, mode="linear"), dtype)
+    compare("linear", ssm_case(70, 2, 19, N, 1, dtype, mode="linear", gated=False), dtype)
+    compare("softplus", ssm_case(70, 2, 18, N, 2, dtype, extras=False, state=False), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,lengths", [(70, [70, 0, 1, 64]), (200, [128, 63, 200, 65]), (40, [-3, 99, 17, 40])])
+@pytest.mark.parametrize("N", [4, 16, 40])
+def test_ragged_rows(dtype, T, lengths, N):
+    """Lengths within, below and above the range; what lies past a row's length is not used."""
+    c = ssm_case(T, 4, 18, N, 1, dtype, lengths)
+    got = compare("softplus", c, dtype)
+    for b, n in enumerate(lengths):
+        for k in ("u", "delta", "z", "Bm", "Cm", "dy"):
+            c[k][max(n, 0):, b] = float("nan") if b % 2 else float("inf")
+    again = ssm_run("softplus", c)
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B", [1, 2])
+def test_slices_of_wider_tensors(dtype, B):
+    for T in (1, 70):
+        c = ssm_case(T, B, 21, 16, 1, dtype)
+        got, want = compare("softplus", c, dtype, wide=11), ssm_run("softplus", c)
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
+
+
+def test_no_steps():
+    c = ssm_case(0, 2, 10, 16, 1, "f32")
+    got = compare("softplus", c, "f32")
+    assert torch.equal(got["hy"].cpu(), c["h0"]) and torch.equal(got["dh0"].cpu(), c["dhy"])
+
+
+def test_inference_is_trainings_forward():
+    c = ssm_case(150, 3, 50, 16, 1, "bf16", [150, 20, 77])
+    a, b = ssm_run("softplus", c), ssm_run("softplus", c, backward=False)
+    assert torch.equal(a["y"], b["y"]) and torch.equal(a["hy"], b["hy"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,G", [(3, 1), (8, 2), (16, 1), (29, 1), (64, 2)])
+def test_single_steps(dtype, N, G):
+    """Every step by itself, the state updated in place, against the definition of the sequence."""
+    c = ssm_case(40, 3, 22, N, G, dtype)
+    want = ssm_want("softplus", c, backward=False)
+    g = {k: gpu(v) for k, v in c.items()}
+    h, y = g["h0"].clone(), torch.empty_like(g["u"])
+    for t in range(40):
+        at = [g[k] if k in ("A", "D", "delta_bias") else g[k][t] for k in INPUTS]
+        R.rnn_ssm_step("softplus", *at, h, y[t], h)
+    check("y", y, want["y"], dtype)
+    check("hy", h, want["hy"])
+
+
+def test_states_carried_in_place():
+    """A sequence in pieces, hy over h0; gradients with dh0 over dhy."""
+    c = ssm_case(150, 2, 40, 16, 1, "f32")
+    want = ssm_want("softplus", c)
+    g = {k: gpu(v) for k, v in c.items()}
+    h, y = g["h0"].clone(), torch.empty_like(g["u"])
+    ws = room(R.rnn_ssm_workspace_size(150, 2, 40, 16, 1))
+    for a, b in ((0, 70), (70, 71), (71, 150)):
+        at = [g[k] if k in ("A", "D", "delta_bias") else g[k][a:b] for k in INPUTS]
+        R.rnn_ssm_forward("softplus", *at, h, None, y[a:b], h, ws)
+    check("y", y, want["y"])
+    check("hy", h, want["hy"])
+    ws = room(R.rnn_ssm_workspace_size(150, 2, 40, 16, 1, "full"))
+    R.rnn_ssm_forward("softplus", *(g[k] for k in INPUTS), g["h0"], None, y, None, ws, "full")
+    d = g["dhy"].clone()
+    R.rnn_ssm_backward("softplus", *(g[k] for k in INPUTS), g["h0"], None, g["dy"], d, *[None] * 8, d, ws)
+    check("dh0", d, want["dh0"])
+
+
+def test_not_wanted_gradients():
+    c = ssm_case(80, 2, 30, 16, 1, "bf16")
+    want = ssm_run("softplus", c)
+    g = {k: gpu(v) for k, v in c.items()}
+    y, ws = torch.empty_like(g["u"]), room(R.rnn_ssm_workspace_size(80, 2, 30, 16, 1, "full"))
+    R.rnn_ssm_forward("softplus", *(g[k] for k in INPUTS), g["h0"], None, y, None, ws, "full")
+    names = ("du", "ddelta", "dA", "dBm", "dCm", "dD", "dz", "ddelta_bias", "dh0")
+    for name in names:
+        out = [torch.empty_like(want[k]) if k == name else None for k in names]
+        R.rnn_ssm_backward("softplus", *(g[k] for k in INPUTS), g["h0"], None, g["dy"], g["dhy"], *out, ws)
+        assert torch.equal(out[names.index(name)], want[name]), name
+
+
+def test_strong_decay_and_large_states():
+    """Decays far below fp32's range: a state of 1e30 that the steps carry down to the inputs' size, and resets."""
+    c = ssm_case(96, 1, 16, 4, 1, "f32", seed=5, mode="linear", gated=False, extras=False)
+    c["A"][:] = torch.tensor([-1.0, -40.0, -0.001, -700.0])
+    c["delta"][:] = 1.0
+    c["h0"][:] = 1e30
+    c["dhy"][:] = 1e-30
+    compare("linear", c, "f32")
+    c["delta"][20:28] = 30.0
+    compare("linear", c, "f32")
+
+
+def test_large_and_small_deltas():
+    """softplus at both ends: e^x far below 0, x far above."""
+    c = ssm_case(70, 2, 20, 16, 1, "f32", seed=6)
+    c["delta"][:20] = -60.0
+    c["delta"][20:30] = -100.0
+    c["delta"][30:40] = 40.0
+    compare("softplus", c, "f32")
+
+
+def test_no_rows():
+    c = ssm_case(5, 0, 6, 4, 1, "f32")
+    got = ssm_run("softplus", c)
+    for k in ("dA", "dD", "ddelta_bias"):
+        assert not got[k].any()
