@@ -556,7 +556,7 @@ rnn_status_t rnn_conv_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, i
  * delta_bias may be NULL (the term or factor is left out).  States h0, hy
  * [B, E, N]; h0 NULL: zeros, hy NULL: not wanted; hy may be h0 itself.
  * INVALID_ARG where groups < 1 or does not divide E; UNSUPPORTED: N > 64,
- * B * E >= 2^24, T >= 2^30 or groups * N >= 2^20.  A state's decay over any
+ * B * E >= 2^24, T >= 2^30, groups * N >= 2^20 or B * ld > 2^26.  A state's decay over any
  * number of steps may leave fp32's range; the states themselves may not. */
 typedef enum RNN_ENUM_BASE { RNN_DELTA_SOFTPLUS = 0, RNN_DELTA_LINEAR = 1 } rnn_delta_t;
 

@@ -1,12 +1,10 @@
 // Selective state-space scan (gfx950), forward and single steps:
 //   h_t[n] = exp(d_t A[n]) h_(t-1)[n] + d_t u_t B_t[n],  y_t = (C_t . h_t + D u_t) silu(z_t)
 //
-// A workgroup holds 64 / S channels of one row and walks their steps in blocks
-// of 64.  Its waves hold consecutive pieces of a block: each composes its piece
-// from a state of zero (h = P h' + Q with P = exp(A sum d)), the maps go
-// through LDS, and each wave walks its piece again from the true state with the
-// exponentials still in registers.  P is kept as its square root: applied
-// twice, it carries a state through a decay of up to 2^-252 without loss.
+// A wave walks the steps of 16 channels (16 states each) one after the other,
+// the states in registers: each step and state takes a product, an
+// exponential (a quarter of the rate), a product and two fused ones, and that
+// bounds the pass, at 8 issue slots a step and state.
 #include <algorithm>
 
 #include "ssm_util.h"
@@ -15,14 +13,10 @@ using namespace rnnk;
 
 namespace {
 
-constexpr int kSteps = 16, kWaves = kSsmBlock / kSteps;   // of a wave's piece, of a block
-
 template <bool BF, int S>
-__global__ __launch_bounds__(256) void step_kernel(const SsmParams p, int waves) {
+__global__ __launch_bounds__(64 * kSsmTiles) void step_kernel(const SsmParams p) {
   constexpr int R = kSsmPer;
-  const int wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (wave >= waves) return;
-  const SsmPlace q = ssm_place<S>(p, wave);
+  const SsmPlace q = ssm_place<S>(p, blockIdx.x, threadIdx.x >> 6);
   if (!q.live) return;
   const int left = p.N - q.n;
   const long long st = ((long long)q.b * p.E + q.e) * p.N + q.n;
@@ -44,8 +38,8 @@ __global__ __launch_bounds__(256) void step_kernel(const SsmParams p, int waves)
     o = fmaf(C[r], h[r], o);
   }
   if (p.hy) store_states(p.hy + st, left, h);
-  o = sum_channel<S>(o);
-  if (q.j) return;
+  o = sum_channel<1, S>(o);
+  if (q.n) return;
   o = fmaf(D, u, o);
   if (p.z) {
     float a, da;
@@ -55,141 +49,155 @@ __global__ __launch_bounds__(256) void step_kernel(const SsmParams p, int waves)
   el_store<BF>((El<BF>*)p.y + q.b * p.ldy + q.e, o);
 }
 
-template <bool BF, int S>
-__global__ __launch_bounds__(64 * kWaves) void fwd_kernel(const SsmParams p) {
-  constexpr int R = kSsmPer, G = kSteps, W = kWaves, NP = S * R, I = G / S, PER = kSsmBlock * 2 * NP / (64 * W);
-  __shared__ __align__(16) float bc[3][kSsmBlock][2][NP];
-  __shared__ __align__(16) float maps[2][W][2][64 * R];
-  const SsmPlace q = ssm_place<S>(p, blockIdx.x);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// LOCAL: the segments' maps (but the last one's), no outputs
+template <bool BF, int S, bool LOCAL>
+__global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) {
+  constexpr int R = kSsmPer, G = ssm_chunk(S), NP = S * R, Q = S < 4 ? S : 4, I = G / Q;
+  __shared__ __align__(16) float bc[kSsmTiles][G][2][NP];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const SsmPlace q = ssm_place<S>(p, blockIdx.x, wave);
+  if (!__any(q.live)) return;
   const int left = q.live ? p.N - q.n : 0;
-  const long long st = ((long long)q.b * p.E + q.e) * p.N + q.n;
-  float A2[R], carry[R] = {};
-  load_states(p.A + (long long)q.e * p.N + q.n, left, A2);
-  if (p.h0) load_states(p.h0 + st, left, carry);
+  const long long at = (long long)q.b * p.E + q.e;
+  float A[R], h[R] = {};
+  load_states(p.A + (long long)q.e * p.N + q.n, left, A);
+  if (p.segs == 1 || LOCAL) {
+    if (p.h0) load_states(p.h0 + at * p.N + q.n, left, h);
+    if (LOCAL) {                       // the states may be written over by the last segment
+      if (q.seg == 0 && q.live) store_states(p.seg_first + at * NP + q.n, R, h);
 #pragma unroll
-  for (int r = 0; r < R; ++r) A2[r] *= kLog2e;
-  const float bias = p.delta_bias && q.live ? p.delta_bias[q.e] : 0.f, D = p.D && q.live ? p.D[q.e] : 0.f;
-  const int blocks = (q.len + kSsmBlock - 1) / kSsmBlock;
-
-  float ru[I], rd[I], rz[I], rbc[PER];
-  auto load = [&](int k) {
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int t = k * kSsmBlock + wave * G + i * S + q.j;
-      const bool on = t < q.len && q.live;
-      const long long row = (long long)t * p.B + q.b;
-      ru[i] = on ? el_load<BF>((const El<BF>*)p.u + row * p.ldu + q.e) : 0.f;
-      rd[i] = on ? el_load<BF>((const El<BF>*)p.delta + row * p.lddelta + q.e) : 0.f;
-      rz[i] = on && p.z ? el_load<BF>((const El<BF>*)p.z + row * p.ldz + q.e) : 0.f;
+      for (int r = 0; r < R; ++r) h[r] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int x = threadIdx.x + i * 64 * W, n = x % NP, c = x / NP % 2, t = k * kSsmBlock + x / (2 * NP);
-      const long long row = (long long)t * p.B + q.b;
-      rbc[i] = 0.f;
-      if (t < q.len && n < p.N)
-        rbc[i] = c ? el_load<BF>((const El<BF>*)p.Cm + row * p.ldC + q.g * p.N + n) : el_load<BF>((const El<BF>*)p.Bm + row * p.ldB + q.g * p.N + n);
-    }
-  };
-  auto stage = [&](int k) {
-    float* to = &bc[k % 3][0][0][0];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) to[threadIdx.x + i * 64 * W] = rbc[i];
-  };
-  if (blocks) {
-    load(0);
-    stage(0);
-    __syncthreads();
-  }
-  for (int k = 0; k < blocks; ++k) {
-    float u[I], d[I], du[I], z[I], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const bool on = k * kSsmBlock + wave * G + i * S + q.j < q.len && q.live;
-      u[i] = ru[i];
-      z[i] = rz[i];
-      d[i] = rd[i] + bias;
-      if (p.softplus) d[i] = softplus(d[i]);
-      if (!on) d[i] = 0.f;
-      du[i] = d[i] * u[i];
-      sum += d[i];
-    }
-    sum = sum_channel<S>(sum);
-    if (k + 1 < blocks) load(k + 1);
-    const float* from = &bc[k % 3][wave * G][0][q.n];
-    float a[G][R], h[R] = {};
-#pragma unroll
-    for (int s = 0; s < G; ++s) {
-      const float ds = from_lane<S>(d[s / S], s % S), dus = from_lane<S>(du[s / S], s % S);
-      float B[R];
-      lds_get(from + s * 2 * NP, B);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        a[s][r] = __builtin_amdgcn_exp2f(ds * A2[r]);
-        h[r] = fmaf(a[s][r], h[r], dus * B[r]);
-      }
-    }
-    float P[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) P[r] = __builtin_amdgcn_exp2f(fminf(0.5f * A2[r] * sum, 127.f));
-    lds_put(&maps[k & 1][wave][0][lane * R], P);
-    lds_put(&maps[k & 1][wave][1][lane * R], h);
-    // a wave may still walk block k - 1: its B and C are a third buffer's, its maps the other one's
-    if (k + 1 < blocks) stage(k + 1);
-    __syncthreads();
-    if (p.starts && wave == 0 && q.live)
-      store_states(p.starts + (((long long)k * p.B + q.b) * p.E + q.e) * NP + q.n, R, carry);
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
+  } else {
+    load_states(p.seg_first + at * NP + q.n, R, h);
+    for (int i = 0; i < q.seg; ++i) {
       float Q[R];
-      lds_get(&maps[k & 1][w][0][lane * R], P);
-      lds_get(&maps[k & 1][w][1][lane * R], Q);
+      const long long m = (long long)i * p.B * p.E + at;
+      load_states(p.seg_q + m * NP + q.n, R, Q);
+      const float sum = p.seg_d[m];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (w == wave) h[r] = carry[r];
-        carry[r] = fmaf(P[r], P[r] * carry[r], Q[r]);
-      }
+      for (int r = 0; r < R; ++r) h[r] = through(A[r], sum, Q[r], h[r]);
     }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) A[r] *= kLog2e;
+  const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
+  const int begin = q.seg * p.seg_steps, stop = min(begin + p.seg_steps, p.T), end = min(stop, q.len);
+  SsmRows xu = ssm_rows<BF, Q>(p, q, p.u, p.ldu, begin), xd = ssm_rows<BF, Q>(p, q, p.delta, p.lddelta, begin),
+          xz = ssm_rows<BF, Q>(p, q, p.z, p.ldz, begin), xy = ssm_rows<BF, Q>(p, q, p.y, p.ldy, begin);
+  El<BF> ru[I], rd[I], rz[I] = {};
+  RawFour<BF> rbc[bc_pieces<G, NP>()];
+  float total = 0.f;
+  auto load = [&](int t0) {
+    const int left = q.len - t0;
+    load_own<BF, Q, false, I>(xu, q, left, ru);
+    load_own<BF, Q, false, I>(xd, q, left, rd);
+    if (!LOCAL && p.z) load_own<BF, Q, false, I>(xz, q, left, rz);
+    load_bc<BF, G, NP>(p, q, t0, rbc);
+  };
+  if (begin < end) load(begin);
+  int t0 = begin;
+  float y[I] = {}, mid[R] = {};
+  for (; t0 < end; t0 += G) {
+    float u[I], d[I], du[I], gate[I];
+#pragma unroll
+    for (int i = 0; i < I; ++i) d[i] = el_load<BF>(&rd[i]) + bias;
+    if (p.softplus)
+#pragma unroll
+      for (int i = 0; i < I; ++i) d[i] = softplus(d[i]);
+#pragma unroll
+    for (int i = 0; i < I; ++i) gate[i] = 1.f;
+    if (!LOCAL && p.z)
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        float slope;
+        act_pair<ACT_SILU>(el_load<BF>(&rz[i]), gate[i], slope);
+      }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      float part[S];
+      const bool on = t0 + i * Q + q.j < end;
+      u[i] = on ? el_load<BF>(&ru[i]) : 0.f;
+      d[i] = on ? d[i] : 0.f;
+      du[i] = d[i] * u[i];
+      total += d[i];
+    }
+    float* own = &bc[wave][0][0][0];
+    put_bc<BF, G, NP>(own, rbc);
+    // what this and the last chunk have to store goes before the next loads: a
+    // wait for those then has no young stores to wait for
+    if constexpr (!LOCAL) {
+      if (t0 > begin) store_own<BF, Q, false, I>(xy, q, G, y);
+      if (p.starts && q.live) {
+        float* to = p.starts + ((long long)(t0 / kSsmKeep) * p.B * p.E + at) * NP + q.n;
+        if (G > kSsmKeep && t0 > begin) store_states(to - (long long)p.B * p.E * NP, R, mid);
+        store_states(to, R, h);
+      }
+    }
+    if (t0 + G < end) load(t0 + G);
+    // B and C of Q steps are read while the Q steps before them are walked (the
+    // empty asm statement holds the reads there)
+    float B[2][Q][R], C[2][Q][R];
+    auto read = [&](int i) {
 #pragma unroll
-      for (int l = 0; l < S; ++l) {
-        const int s = i * S + l;
-        const float dus = from_lane<S>(du[i], l);
-        float B[R], C[R];
-        lds_get(from + s * 2 * NP, B);
-        lds_get(from + s * 2 * NP + NP, C);
+      for (int l = 0; l < Q; ++l) {
+        const float* row = own + (i * Q + l) * 2 * NP + q.n;
+        lds_get(row, B[i & 1][l]);
+        if constexpr (!LOCAL) lds_get(row + NP, C[i & 1][l]);
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      if (i + 1 < I) read(i + 1);
+      if (G > kSsmKeep && i * Q == kSsmKeep)
+#pragma unroll
+        for (int r = 0; r < R; ++r) mid[r] = h[r];
+      asm volatile("" ::: "memory");
+      float part[Q];
+#pragma unroll
+      for (int l = 0; l < Q; ++l) {
+        const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
         part[l] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          h[r] = fmaf(a[s][r], h[r], dus * B[r]);
-          part[l] = fmaf(C[r], h[r], part[l]);
+          h[r] = fmaf(__builtin_amdgcn_exp2f(ds * A[r]), h[r], dus * B[i & 1][l][r]);
+          if constexpr (!LOCAL) part[l] = fmaf(C[i & 1][l][r], h[r], part[l]);
         }
       }
-      float o = fmaf(D, u[i], sum_to_lane<S>(part));
-      if (p.z) {
-        float g, slope;
-        act_pair<ACT_SILU>(z[i], g, slope);
-        o *= g;
+      if constexpr (!LOCAL) {
+        y[i] = fmaf(D, u[i], sum_to_lane<S, Q>(part)) * gate[i];
+        if (t0 + i * Q + q.j >= end) y[i] = 0.f;
       }
-      const int t = k * kSsmBlock + wave * G + i * S + q.j;
-      if (q.live && t < p.T) el_store<BF>((El<BF>*)p.y + ((long long)t * p.B + q.b) * p.ldy + q.e, t < q.len ? o : 0.f);
     }
   }
-  if (!q.live) return;
-  for (int t = blocks * kSsmBlock + wave * S + q.j; t < p.T; t += W * S)
-    el_store<BF>((El<BF>*)p.y + ((long long)t * p.B + q.b) * p.ldy + q.e, 0.f);
-  if (p.hy && wave == 0) store_states(p.hy + st, left, carry);
+  if constexpr (LOCAL) {
+    if (!q.live) return;
+    const long long m = (long long)q.seg * p.B * p.E + at;
+    store_states(p.seg_q + m * NP + q.n, R, h);
+    total = sum_channel<1, Q>(total);
+    if (q.owner && q.j == 0) p.seg_d[m] = total;
+  } else {
+    const float none[I] = {};
+    if (t0 > begin) {
+      store_own<BF, Q, false, I>(xy, q, stop - (t0 - G), y);
+      if (G > kSsmKeep && p.starts && q.live && t0 - G + kSsmKeep < end)
+        store_states(p.starts + ((long long)((t0 - G) / kSsmKeep + 1) * p.B * p.E + at) * NP + q.n, R, mid);
+    }
+    for (; t0 < stop; t0 += G) store_own<BF, Q, false, I>(xy, q, stop - t0, none);
+    if (q.live && p.hy && q.seg == p.segs - 1) store_states(p.hy + at * p.N + q.n, left, h);
+  }
 }
 
 template <bool BF, int S>
 hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
-  constexpr int CH = 64 / S;
-  const long long tiles = (p.E / p.G + CH - 1) / CH, all = tiles * p.G * p.B;   // at most B * E
-  if (step) hipLaunchKernelGGL((step_kernel<BF, S>), dim3((unsigned)((all + 3) / 4)), dim3(256), 0, s, p, (int)all);
-  else hipLaunchKernelGGL((fwd_kernel<BF, S>), dim3((unsigned)all), dim3(64 * kWaves), 0, s, p);
+  const unsigned tiles = (unsigned)ssm_groups(p, S) * p.G * p.B;   // at most B * E
+  const dim3 block(64 * kSsmTiles);
+  if (step) {
+    hipLaunchKernelGGL((step_kernel<BF, S>), dim3(tiles), block, 0, s, p);
+    return hipGetLastError();
+  }
+  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1)), block, 0, s, p);
+  hipLaunchKernelGGL((fwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -206,6 +214,44 @@ hipError_t launch(const SsmParams& p, bool step, hipStream_t s) {
 }
 
 }  // namespace
+
+// Segments of a pass with `tiles` waves a segment: one where a device's worth
+// of waves (1024: one a SIMD) walks alone, else as many as fill it with `fill`
+// waves, of 32 steps at least.  `alone`: where one segment begins to win.
+static int segments(long long tiles, int T, int alone, int fill) {
+  if (tiles == 0 || tiles >= alone) return 1;
+  return (int)std::max(1LL, std::min<long long>(fill / tiles, T / 32));
+}
+
+SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
+  SsmPlan r{};
+  const int S = ssm_lanes(N), CH = 64 / S, step = ssm_chunk(S), NP = S * kSsmPer;
+  const long long tiles = (long long)(E / G + CH - 1) / CH * G * B;
+  for (int back = 0; back < 2; ++back) {
+    const int segs = back ? segments(tiles, T, 1300, 2048) : segments(tiles, T, 800, 4096);
+    r.seg_steps[back] = std::max(step, ((T + segs - 1) / segs + step - 1) / step * step);
+    r.segs[back] = std::max(1, (T + r.seg_steps[back] - 1) / r.seg_steps[back]);
+  }
+  const size_t C = (size_t)B * E, segs = std::max(r.segs[0], save ? r.segs[1] : 1);
+  size_t o = 0;
+  auto take = [&o](size_t floats) {
+    const size_t at = o;
+    o += (floats + 63) & ~(size_t)63;
+    return at;
+  };
+  if (save) r.starts = take(((size_t)T + kSsmKeep - 1) / kSsmKeep * C * NP);
+  if (segs > 1) {
+    r.first = take(C * NP);
+    r.q = take(segs * C * NP);
+    r.d = take(segs * C);
+  }
+  if (save) {
+    const size_t groups = (size_t)(E / G + CH * kSsmTiles - 1) / (CH * kSsmTiles);
+    r.part = take((groups > 1 ? groups * T * B * G * 2 * NP : 0) + r.segs[1] * C * (NP + 2));
+  }
+  r.all = o;
+  return r;
+}
 
 hipError_t rnn_launch_ssm_step(const SsmParams& p, int bf16, hipStream_t s) {
   return bf16 ? launch<true>(p, true, s) : launch<false>(p, true, s);

@@ -68,15 +68,30 @@ size_t conv_bytes(int T, int B, int C, int K) {
 rnn_status_t ssm_sizes(int T, int B, int E, int N, int groups) {
   if (T < 0 || B < 0 || E < 0 || N < 1 || groups < 1 || E % groups) return RNN_STATUS_INVALID_ARG;
   if (N > kSsmStates || (long long)B * E >= (1 << 24) || T >= (1 << 30) || (long long)groups * N >= (1 << 20)) return RNN_STATUS_UNSUPPORTED;
-  // the launch over dB and dC
+  // the launch over dB and dC, and its partial sums
   return (double)T * B * groups * N >= 0x1p37 ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
 }
 bool ssm_ok(int mode, int wtype) { return (mode == RNN_DELTA_SOFTPLUS || mode == RNN_DELTA_LINEAR) && wtype_ok(wtype); }
 
-size_t ssm_starts(int T, int B, int E, int N) { return align_up(ssm_start_floats(T, B, E, N) * 4); }
-size_t ssm_bytes(int T, int B, int E, int N, int groups, int save) {
-  if (save == RNN_SAVE_NONE) return kAlign;
-  return std::max(kAlign, ssm_starts(T, B, E, N) + align_up(ssm_part_floats(T, B, E, N, groups) * 4));
+size_t ssm_bytes(const SsmPlan& q) { return std::max(kAlign, q.all * 4); }
+
+// a pass's segments and its parts of the workspace
+void ssm_room(SsmParams& p, const SsmPlan& q, bool back, void* ws) {
+  float* f = (float*)ws;
+  p.segs = q.segs[back];
+  p.seg_steps = q.seg_steps[back];
+  p.seg_first = f + q.first;
+  p.seg_q = f + q.q;
+  p.seg_d = f + q.d;
+  p.starts = f + q.starts;
+  p.part = f + q.part;
+}
+
+// rows `ld` elements apart; a step's lie within 32 bits of each other
+rnn_status_t ssm_rows(int B, const void* x, long long ld, long long width) {
+  if (!x) return RNN_STATUS_SUCCESS;
+  if (ld < width) return RNN_STATUS_INVALID_ARG;
+  return ld > (1 << 26) / std::max(B, 1) ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
 }
 
 // the inputs' checks; they are needed where there are steps
@@ -84,7 +99,11 @@ rnn_status_t ssm_inputs(SsmParams& p, const rnn_ssm_inputs_t* in, int mode, int 
   if (!in || !in->A) return RNN_STATUS_INVALID_ARG;
   if (T > 0 && (!in->u || !in->delta || !in->Bm || !in->Cm)) return RNN_STATUS_INVALID_ARG;
   const long long GN = (long long)groups * N;
-  if (in->ldu < E || in->lddelta < E || (in->z && in->ldz < E) || in->ldB < GN || in->ldC < GN) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_rows(B, in->u, in->ldu, E));
+  LM_TRY(ssm_rows(B, in->delta, in->lddelta, E));
+  LM_TRY(ssm_rows(B, in->z, in->ldz, E));
+  LM_TRY(ssm_rows(B, in->Bm, in->ldB, GN));
+  LM_TRY(ssm_rows(B, in->Cm, in->ldC, GN));
   p.T = T; p.B = B; p.E = E; p.N = N; p.G = groups;
   p.softplus = mode == RNN_DELTA_SOFTPLUS;
   p.u = in->u; p.delta = in->delta; p.z = in->z; p.Bm = in->Bm; p.Cm = in->Cm;
@@ -194,7 +213,8 @@ rnn_status_t rnn_ssm_step(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int
   if (B == 0 || E == 0) return RNN_STATUS_SUCCESS;
   SsmParams p{};
   LM_TRY(ssm_inputs(p, in, mode, 1, B, E, N, groups));
-  if (!y || ldy < E) return RNN_STATUS_INVALID_ARG;
+  if (!y) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_rows(B, y, ldy, E));
   p.h0 = h; p.y = y; p.ldy = ldy; p.hy = hy;
   return dev(rnn_launch_ssm_step(p, wtype == RNN_W_BF16, hs(stream)));
 }
@@ -202,7 +222,7 @@ rnn_status_t rnn_ssm_step(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int
 rnn_status_t rnn_ssm_workspace_size(int T, int B, int E, int N, int groups, rnn_save_t save, size_t* bytes) {
   if (!bytes || (save != RNN_SAVE_NONE && save != RNN_SAVE_FULL)) return RNN_STATUS_INVALID_ARG;
   LM_TRY(ssm_sizes(T, B, E, N, groups));
-  *bytes = ssm_bytes(T, B, E, N, groups, save);
+  *bytes = ssm_bytes(ssm_plan(T, B, E, N, groups, save == RNN_SAVE_FULL));
   return RNN_STATUS_SUCCESS;
 }
 
@@ -211,13 +231,16 @@ rnn_status_t rnn_ssm_forward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, 
                              void* y, long long ldy, float* hy, void* ws, size_t ws_bytes) {
   if (!ssm_ok(mode, wtype) || (save != RNN_SAVE_NONE && save != RNN_SAVE_FULL)) return RNN_STATUS_INVALID_ARG;
   LM_TRY(ssm_sizes(T, B, E, N, groups));
-  LM_TRY(room(ws, ws_bytes, ssm_bytes(T, B, E, N, groups, save)));
+  const SsmPlan plan = ssm_plan(T, B, E, N, groups, save == RNN_SAVE_FULL);
+  LM_TRY(room(ws, ws_bytes, ssm_bytes(plan)));
   if (B == 0 || E == 0) return RNN_STATUS_SUCCESS;
   SsmParams p{};
   LM_TRY(ssm_inputs(p, in, mode, T, B, E, N, groups));
-  if (ldy < E || (T > 0 && !y)) return RNN_STATUS_INVALID_ARG;
+  if (T > 0 && !y) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_rows(B, y, ldy, E));
   p.h0 = h0; p.lengths = lengths; p.y = y; p.ldy = ldy; p.hy = hy;
-  p.starts = save == RNN_SAVE_FULL ? (float*)ws : nullptr;
+  ssm_room(p, plan, false, ws);
+  if (save == RNN_SAVE_NONE) p.starts = nullptr;
   return dev(rnn_launch_ssm_fwd(p, wtype == RNN_W_BF16, hs(stream)));
 }
 
@@ -227,21 +250,25 @@ rnn_status_t rnn_ssm_backward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype,
                               size_t ws_bytes) {
   if (!ssm_ok(mode, wtype) || !grads) return RNN_STATUS_INVALID_ARG;
   LM_TRY(ssm_sizes(T, B, E, N, groups));
-  LM_TRY(room(ws, ws_bytes, ssm_bytes(T, B, E, N, groups, RNN_SAVE_FULL)));
+  const SsmPlan plan = ssm_plan(T, B, E, N, groups, true);
+  LM_TRY(room(ws, ws_bytes, ssm_bytes(plan)));
   if (E == 0) return RNN_STATUS_SUCCESS;
   SsmParams p{};
   LM_TRY(ssm_inputs(p, in, mode, B > 0 ? T : 0, B, E, N, groups));
   const long long GN = (long long)groups * N;
   const rnn_ssm_grads_t& g = *grads;
-  if (lddy < E || (B > 0 && T > 0 && !dy) || (g.dz && !in->z) || (g.du && g.lddu < E) || (g.ddelta && g.ldddelta < E) ||
-      (g.dz && g.lddz < E) || (g.dBm && g.lddB < GN) || (g.dCm && g.lddC < GN))
-    return RNN_STATUS_INVALID_ARG;
+  if ((B > 0 && T > 0 && !dy) || (g.dz && !in->z)) return RNN_STATUS_INVALID_ARG;
+  LM_TRY(ssm_rows(B, dy, lddy, E));
+  LM_TRY(ssm_rows(B, g.du, g.lddu, E));
+  LM_TRY(ssm_rows(B, g.ddelta, g.ldddelta, E));
+  LM_TRY(ssm_rows(B, g.dz, g.lddz, E));
+  LM_TRY(ssm_rows(B, g.dBm, g.lddB, GN));
+  LM_TRY(ssm_rows(B, g.dCm, g.lddC, GN));
   p.lengths = lengths; p.dy = dy; p.lddy = lddy; p.dhy = dhy;
   p.du = g.du; p.ddelta = g.ddelta; p.dz = g.dz; p.dBm = g.dBm; p.dCm = g.dCm;
   p.lddu = g.lddu; p.ldddelta = g.ldddelta; p.lddz = g.lddz; p.lddB = g.lddB; p.lddC = g.lddC;
   p.dA = g.dA; p.dD = g.dD; p.ddelta_bias = g.ddelta_bias; p.dh0 = g.dh0;
-  p.starts = (float*)ws;
-  p.part = (float*)((char*)ws + ssm_starts(T, B, E, N));
+  ssm_room(p, plan, true, ws);
   return dev(rnn_launch_ssm_bwd(p, wtype == RNN_W_BF16, hs(stream)));
 }
 

@@ -4,14 +4,12 @@
 //   dC_t = sum_e do h_t     dB_t = sum_e g d u     du = d (g . B) + D do
 //   dd = sum_n A g a h_(t-1) + u (g . B)           dA = sum_t d g a h_(t-1)
 //
-// A workgroup walks the blocks of 64 steps backwards.  Forward left the state
-// before every block; each wave holds 8 steps (16 with 16 lanes a channel), composes its forward
-// map and its map of g (which has the same decay), and after one exchange
-// through LDS walks its steps forwards for the states and backwards for the
-// gradients, with exponentials and states in registers.  The sums over
-// channels of dB and dC are made within a wave, written for each tile of
-// channels, and added in a second launch; parameters' gradients stay in
-// registers over all steps and are added over rows there, too.  All in a fixed
+// A wave walks the chunks of its 16 channels (16 states each) backwards: from
+// the state that forward left before a chunk it walks the chunk forwards, keeps
+// the exponentials and the states, and walks it back.  The sums over channels
+// of dB and dC are made within a wave, then over the workgroup's waves through
+// the LDS, then (where a group has more channels) in a second launch, which
+// adds the parameters' gradients of the rows and segments, too.  All in a fixed
 // order.
 #include <algorithm>
 
@@ -21,20 +19,20 @@ using namespace rnnk;
 
 namespace {
 
-// steps of a wave's piece (a lane of a channel owns at least one)
-constexpr int steps_of(int S) { return S < 8 ? 8 : S; }
-
-// Partial sums in the workspace: [tiles][T][B][G][2][NP] of dB and dC, then
-// [B][E][NP] of dA and [B][E] of dD and ddelta_bias.
+// Partial sums in the workspace: [workgroups of a group][T][B][G][2][NP] of dB and
+// dC (where there are several), then [segs * B][E][NP] of dA and [segs * B][E]
+// of dD and ddelta_bias.
 struct Parts {
   float *bc, *A, *D, *bias;
+  int groups;
 };
-Parts parts_of(const SsmParams& p, int tiles, int NP) {
+Parts parts_of(const SsmParams& p, int groups, int NP) {
   Parts r;
+  r.groups = groups;
   r.bc = p.part;
-  r.A = r.bc + (size_t)tiles * p.T * p.B * p.G * 2 * NP;
-  r.D = r.A + (size_t)p.B * p.E * NP;
-  r.bias = r.D + (size_t)p.B * p.E;
+  r.A = r.bc + (groups > 1 ? (size_t)groups * p.T * p.B * p.G * 2 * NP : 0);
+  r.D = r.A + (size_t)p.segs * p.B * p.E * NP;
+  r.bias = r.D + (size_t)p.segs * p.B * p.E;
   return r;
 }
 
@@ -59,257 +57,260 @@ __device__ __forceinline__ void sum_channels(float (&v)[V]) {
   }
 }
 
-template <bool BF, int S>
-__global__ __launch_bounds__(64 * (kSsmBlock / steps_of(S))) void bwd_kernel(const SsmParams p, const Parts out) {
-  constexpr int R = kSsmPer, G = steps_of(S), W = kSsmBlock / G, NP = S * R, I = G / S, PER = kSsmBlock * 2 * NP / (64 * W), CH = 64 / S;
-  __shared__ __align__(16) float bc[3][kSsmBlock][2][NP];
-  __shared__ __align__(16) float maps[2][W][3][64 * R];
-  const SsmPlace q = ssm_place<S>(p, blockIdx.x);
+// LOCAL: the segments' maps of g (but the first one's), no outputs
+template <bool BF, int S, bool LOCAL>
+__global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams p, const Parts out) {
+  constexpr int R = kSsmPer, G = kSsmKeep, NP = S * R, Q = S < 4 ? S : 4, I = G / Q, CH = 64 / S, W = kSsmTiles;
+  __shared__ __align__(16) float bc[W][G][2][NP];
+  __shared__ float sums[LOCAL ? 1 : 2][W][G][2][NP];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  SsmPlace q = ssm_place<S>(p, blockIdx.x, wave);
+  if (LOCAL) ++q.seg;
+  if (LOCAL && !__any(q.live)) return;
   const int left = q.live ? p.N - q.n : 0;
-  const long long st = ((long long)q.b * p.E + q.e) * p.N + q.n;
-  float A[R], carry[R] = {}, dA[R] = {}, dD = 0.f, dbias = 0.f;
+  const bool whole = __all(q.live);
+  const long long at = (long long)q.b * p.E + q.e;
+  float A[R], e[R] = {}, dA[R] = {}, dD = 0.f, dbias = 0.f, total = 0.f;
   load_states(p.A + (long long)q.e * p.N + q.n, left, A);
-  if (p.dhy) load_states(p.dhy + st, left, carry);
-  const float bias = p.delta_bias && q.live ? p.delta_bias[q.e] : 0.f, D = p.D && q.live ? p.D[q.e] : 0.f;
-  const int blocks = (q.len + kSsmBlock - 1) / kSsmBlock;
-
-  float ru[I], rd[I], rz[I], rdy[I], rbc[PER], start[R];
-  auto load = [&](int k) {
+  if (p.segs == 1 || LOCAL) {
+    if (p.dhy) load_states(p.dhy + at * p.N + q.n, left, e);
+    if (LOCAL) {                       // dhy may be written over by the first segment
+      if (q.seg == p.segs - 1 && q.live) store_states(p.seg_first + at * NP + q.n, R, e);
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int t = k * kSsmBlock + wave * G + i * S + q.j;
-      const bool on = t < q.len && q.live;
-      const long long row = (long long)t * p.B + q.b;
-      ru[i] = on ? el_load<BF>((const El<BF>*)p.u + row * p.ldu + q.e) : 0.f;
-      rd[i] = on ? el_load<BF>((const El<BF>*)p.delta + row * p.lddelta + q.e) : 0.f;
-      rz[i] = on && p.z ? el_load<BF>((const El<BF>*)p.z + row * p.ldz + q.e) : 0.f;
-      rdy[i] = on ? el_load<BF>((const El<BF>*)p.dy + row * p.lddy + q.e) : 0.f;
+      for (int r = 0; r < R; ++r) e[r] = 0.f;
     }
+  } else if (q.live) {
+    load_states(p.seg_first + at * NP + q.n, R, e);
+    for (int i = p.segs - 1; i > q.seg; --i) {
+      float Q[R];
+      const long long m = (long long)i * p.B * p.E + at;
+      load_states(p.seg_q + m * NP + q.n, R, Q);
+      const float sum = p.seg_d[m];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int x = threadIdx.x + i * 64 * W, n = x % NP, c = x / NP % 2, t = k * kSsmBlock + x / (2 * NP);
-      const long long row = (long long)t * p.B + q.b;
-      rbc[i] = 0.f;
-      if (t < q.len && n < p.N)
-        rbc[i] = c ? el_load<BF>((const El<BF>*)p.Cm + row * p.ldC + q.g * p.N + n) : el_load<BF>((const El<BF>*)p.Bm + row * p.ldB + q.g * p.N + n);
+      for (int r = 0; r < R; ++r) e[r] = through(A[r], sum, Q[r], e[r]);
     }
-    load_states(p.starts + (((long long)k * p.B + q.b) * p.E + q.e) * NP + q.n, q.live ? R : 0, start);
-  };
-  auto stage = [&](int k) {
-    float* to = &bc[k % 3][0][0][0];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) to[threadIdx.x + i * 64 * W] = rbc[i];
-  };
-  if (blocks) {
-    load(blocks - 1);
-    stage(blocks - 1);
-    __syncthreads();
   }
-  for (int k = blocks - 1; k >= 0; --k) {
-    float u[I], d[I], du[I], z[I], dy[I], go[I], slope[I], sum = 0.f, first[R];
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const bool on = k * kSsmBlock + wave * G + i * S + q.j < q.len && q.live;
-      u[i] = ru[i];
-      z[i] = rz[i];
-      dy[i] = rdy[i];
-      const float pre = rd[i] + bias;
-      d[i] = pre;
-      slope[i] = 1.f;                    // of d to delta
-      if (p.softplus) {
-        float neg;
-        d[i] = softplus(pre);
-        sigmoid_pair(pre, slope[i], neg);
-      }
-      if (!on) d[i] = slope[i] = 0.f;
-      du[i] = d[i] * u[i];
-      go[i] = dy[i];
-      if (p.z) {
-        float g, unused;
-        act_pair<ACT_SILU>(z[i], g, unused);
-        go[i] *= g;
-      }
-      sum += d[i];
+  const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
+  const int begin = q.seg * p.seg_steps, stop = min(begin + p.seg_steps, p.T), end = min(stop, q.len);
+  int t0 = begin + (end - begin + G - 1) / G * G - G;      // the last chunk with steps, if there is one
+  SsmRows xu = ssm_rows<BF, Q>(p, q, p.u, p.ldu, t0), xd = ssm_rows<BF, Q>(p, q, p.delta, p.lddelta, t0),
+          xz = ssm_rows<BF, Q>(p, q, p.z, p.ldz, t0), xdy = ssm_rows<BF, Q>(p, q, p.dy, p.lddy, t0);
+  SsmRows ydu = ssm_rows<BF, Q>(p, q, p.du, p.lddu, t0), ydd = ssm_rows<BF, Q>(p, q, p.ddelta, p.ldddelta, t0),
+          ydz = ssm_rows<BF, Q>(p, q, p.dz, p.lddz, t0);
+  El<BF> ru[I] = {}, rd[I], rz[I] = {}, rdy[I];
+  RawFour<BF> rbc[bc_pieces<G, NP>()];
+  float start[R] = {};
+  auto load = [&](int t0) {
+    const int left = q.len - t0;
+    load_own<BF, Q, true, I>(xd, q, left, rd);
+    if (p.z) load_own<BF, Q, true, I>(xz, q, left, rz);
+    load_own<BF, Q, true, I>(xdy, q, left, rdy);
+    if constexpr (!LOCAL) load_own<BF, Q, true, I>(xu, q, left, ru);
+    load_bc<BF, G, NP>(p, q, t0, rbc);
+    if constexpr (!LOCAL) {
+      load_states(p.starts + ((long long)(t0 / G) * p.B * p.E + at) * NP + q.n, q.live ? R : 0, start);
     }
-    sum = sum_channel<S>(sum);
-#pragma unroll
-    for (int r = 0; r < R; ++r) first[r] = start[r];
-    if (k > 0) load(k - 1);
-    const float* from = &bc[k % 3][wave * G][0][q.n];
-    float a[G][R], h[R] = {}, e[R] = {};
-#pragma unroll
-    for (int s = 0; s < G; ++s) {
-      const float ds = from_lane<S>(d[s / S], s % S), dus = from_lane<S>(du[s / S], s % S);
-      float B[R];
-      lds_get(from + s * 2 * NP, B);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        a[s][r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e));
-        h[r] = fmaf(a[s][r], h[r], dus * B[r]);
-      }
+  };
+  if (begin < end) load(t0);
+  if constexpr (!LOCAL) {                // the steps past the row's length
+    const float none[I] = {};
+    const int from = begin < end ? t0 + G : begin;
+    SsmRows zdu = ssm_rows<BF, Q>(p, q, p.du, p.lddu, from), zdd = ssm_rows<BF, Q>(p, q, p.ddelta, p.ldddelta, from),
+            zdz = ssm_rows<BF, Q>(p, q, p.dz, p.lddz, from);
+    for (int t = from; t < stop; t += G) {
+      if (p.du) store_own<BF, Q, false, I>(zdu, q, stop - t, none);
+      if (p.ddelta) store_own<BF, Q, false, I>(zdd, q, stop - t, none);
+      if (p.dz) store_own<BF, Q, false, I>(zdz, q, stop - t, none);
     }
-#pragma unroll
-    for (int s = G - 1; s >= 0; --s) {
-      const float gs = from_lane<S>(go[s / S], s % S);
-      float C[R];
-      lds_get(from + s * 2 * NP + NP, C);
-#pragma unroll
-      for (int r = 0; r < R; ++r) e[r] = a[s][r] * fmaf(C[r], gs, e[r]);
-    }
-    float P[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) P[r] = __builtin_amdgcn_exp2f(fminf(0.5f * kLog2e * A[r] * sum, 127.f));
-    lds_put(&maps[k & 1][wave][0][lane * R], P);
-    lds_put(&maps[k & 1][wave][1][lane * R], h);
-    lds_put(&maps[k & 1][wave][2][lane * R], e);
-    if (k > 0) stage(k - 1);
+  }
+  // A chunk's outputs are stored in the next one, before its loads: a wait for
+  // those then has no young stores to wait for.  The waves' sums of dB and dC
+  // are added there, too; the other half of `sums` is written meanwhile.
+  float rows[3][I] = {};
+  auto flush = [&](int t0) {
+    if (p.du) store_own<BF, Q, true, I>(ydu, q, stop - t0, rows[0]);
+    if (p.ddelta) store_own<BF, Q, true, I>(ydd, q, stop - t0, rows[1]);
+    if (p.dz) store_own<BF, Q, true, I>(ydz, q, stop - t0, rows[2]);
+    if (!p.dBm && !p.dCm) return;
     __syncthreads();
-    // the state before the wave's steps, and what of g its last step gets from the steps that follow
+    for (int x = threadIdx.x; x < G * 2 * NP; x += 64 * W) {
+      const int s = x / (2 * NP), c = x / NP % 2, n = x % NP, t = t0 + s;
+      float v = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) h[r] = first[r];
-    for (int w = 0; w < wave; ++w) {
-      float Q[R];
-      lds_get(&maps[k & 1][w][0][lane * R], P);
-      lds_get(&maps[k & 1][w][1][lane * R], Q);
-#pragma unroll
-      for (int r = 0; r < R; ++r) h[r] = fmaf(P[r], P[r] * h[r], Q[r]);
-    }
-#pragma unroll
-    for (int w = W - 1; w >= 0; --w) {
-      float Q[R];
-      lds_get(&maps[k & 1][w][0][lane * R], P);
-      lds_get(&maps[k & 1][w][2][lane * R], Q);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (w == wave) e[r] = carry[r];
-        carry[r] = fmaf(P[r], P[r] * carry[r], Q[r]);
+      for (int w = 0; w < W; ++w) v += sums[LOCAL ? 0 : t0 / G & 1][w][s][c][n];
+      const long long row = (long long)t * p.B + q.b;
+      if (t >= end) continue;
+      if (out.groups > 1) {
+        out.bc[((((long long)q.group * p.T * p.B + row) * p.G + q.g) * 2 + c) * NP + n] = v;
+      } else if (n < p.N && (c ? p.dCm : p.dBm)) {
+        el_store<BF>((El<BF>*)(c ? p.dCm : p.dBm) + row * (c ? p.lddC : p.lddB) + q.g * p.N + n, v);
       }
     }
-    // forwards: the state before every step, and what the gate multiplied
-    float hb[G][R], o[I];
+  };
+  const int top = t0;
+  if (begin < end)
+    for (; t0 >= begin; t0 -= G) {
+      float u[I], d[I], du[I], z[I], dy[I], go[I], slope[I], h[R];
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      float part[S];
-#pragma unroll
-      for (int l = 0; l < S; ++l) {
-        const int s = i * S + l;
-        const float dus = from_lane<S>(du[i], l);
-        float B[R], C[R];
-        lds_get(from + s * 2 * NP, B);
-        lds_get(from + s * 2 * NP + NP, C);
-        part[l] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          hb[s][r] = h[r];
-          h[r] = fmaf(a[s][r], h[r], dus * B[r]);
-          part[l] = fmaf(C[r], h[r], part[l]);
-        }
+      for (int i = 0; i < I; ++i) {
+        d[i] = el_load<BF>(&rd[i]) + bias;
+        slope[i] = 1.f;                    // of d to delta
       }
-      o[i] = fmaf(D, u[i], sum_to_lane<S>(part));
-    }
-    // backwards
-    float gB[I], gA[I];
+      if (p.softplus)
 #pragma unroll
-    for (int i = I - 1; i >= 0; --i) {
-      float pB[S], pA[S];
-#pragma unroll
-      for (int l = S - 1; l >= 0; --l) {
-        const int s = i * S + l;
-        const float ds = from_lane<S>(d[i], l), dus = from_lane<S>(du[i], l), gs = from_lane<S>(go[i], l);
-        float B[R], C[R], v[2 * R];
-        lds_get(from + s * 2 * NP, B);
-        lds_get(from + s * 2 * NP + NP, C);
-        pB[l] = pA[l] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float g = fmaf(C[r], gs, e[r]);
-          v[r] = g * dus;
-          v[R + r] = gs * (s == G - 1 ? h[r] : hb[s == G - 1 ? s : s + 1][r]);
-          pB[l] = fmaf(g, B[r], pB[l]);
-          e[r] = g * a[s][r];
-          const float x = e[r] * hb[s][r];
-          pA[l] = fmaf(x, A[r], pA[l]);
-          dA[r] = fmaf(x, ds, dA[r]);
+        for (int i = 0; i < I; ++i) {
+          float neg;
+          sigmoid_pair(d[i], slope[i], neg);
+          d[i] = softplus(d[i]);
         }
-        sum_channels<S, 32, 2 * R>(v);
-        // the values a lane has left: folds of the bits 32, 16, ... chose them
-        constexpr int LEFT = 2 * R > CH ? 2 * R / CH : 1;
-        int first_value = 0;
-        bool mine = true;
 #pragma unroll
-        for (int bit = 32, half = R; bit >= S; bit /= 2, half /= 2) {
-          if (half >= 1) first_value += lane & bit ? half : 0;
-          else mine = mine && !(lane & bit);
+      for (int i = 0; i < I; ++i) {
+        const bool on = t0 + i * Q + q.j < end && q.live;
+        u[i] = on ? el_load<BF>(&ru[i]) : 0.f;
+        z[i] = on ? el_load<BF>(&rz[i]) : 0.f;
+        dy[i] = on ? el_load<BF>(&rdy[i]) : 0.f;
+        d[i] = on ? d[i] : 0.f;
+        slope[i] = on ? slope[i] : 0.f;
+        du[i] = d[i] * u[i];
+        go[i] = dy[i];
+        total += d[i];
+      }
+      if (p.z)
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          float g, unused;
+          act_pair<ACT_SILU>(z[i], g, unused);
+          go[i] *= g;
         }
-        const int t = k * kSsmBlock + wave * G + s;
-        if (mine && t < q.len) {
-          float* to = out.bc + (((((long long)q.tile * p.T + t) * p.B + q.b) * p.G + q.g) * 2) * NP;
 #pragma unroll
-          for (int i2 = 0; i2 < LEFT; ++i2) {
-            const int x = first_value + i2;
-            to[(x / R) * NP + q.n + x % R] = v[i2];
+      for (int r = 0; r < R; ++r) h[r] = start[r];
+      float* own = &bc[wave][0][0][0];
+      put_bc<BF, G, NP>(own, rbc);
+      if (!LOCAL && t0 < top) flush(t0 + G);
+      if (t0 > begin) load(t0 - G);
+      if constexpr (LOCAL) {
+#pragma unroll
+        for (int s = G - 1; s >= 0; --s) {
+          const float ds = from_lane<Q>(d[s / Q], s % Q), gs = from_lane<Q>(go[s / Q], s % Q);
+          float C[R];
+          lds_get(own + s * 2 * NP + NP + q.n, C);
+#pragma unroll
+          for (int r = 0; r < R; ++r) e[r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e)) * fmaf(C[r], gs, e[r]);
+        }
+        continue;
+      }
+      // forwards: the exponentials, the state before every step, what the gate multiplied
+      float a[G][R], hb[G][R], o[I];
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        float part[Q];
+#pragma unroll
+        for (int l = 0; l < Q; ++l) {
+          const int s = i * Q + l;
+          const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
+          float B[R], C[R];
+          lds_get(own + s * 2 * NP + q.n, B);
+          lds_get(own + s * 2 * NP + NP + q.n, C);
+          part[l] = 0.f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            a[s][r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e));
+            hb[s][r] = h[r];
+            h[r] = fmaf(a[s][r], h[r], dus * B[r]);
+            part[l] = fmaf(C[r], h[r], part[l]);
           }
         }
+        o[i] = fmaf(D, u[i], sum_to_lane<S, Q>(part));
       }
-      gB[i] = sum_to_lane<S>(pB);
-      gA[i] = sum_to_lane<S>(pA);
-    }
+      // backwards
+      float (*const to)[2][NP] = sums[LOCAL ? 0 : t0 / G & 1][wave];
+      float gB[I], gA[I];
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int t = k * kSsmBlock + wave * G + i * S + q.j;
-      const float dd = slope[i] * fmaf(u[i], gB[i], gA[i]);
-      dD = fmaf(go[i], u[i], dD);
-      dbias += dd;
-      if (!q.live || t >= p.T) continue;
-      const long long row = (long long)t * p.B + q.b;
-      const bool on = t < q.len;
-      if (p.du) el_store<BF>((El<BF>*)p.du + row * p.lddu + q.e, on ? fmaf(D, go[i], d[i] * gB[i]) : 0.f);
-      if (p.ddelta) el_store<BF>((El<BF>*)p.ddelta + row * p.ldddelta + q.e, on ? dd : 0.f);
-      if (p.dz) {
+      for (int i = I - 1; i >= 0; --i) {
+        float pB[Q], pA[Q];
+#pragma unroll
+        for (int l = Q - 1; l >= 0; --l) {
+          const int s = i * Q + l;
+          const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l), gs = from_lane<Q>(go[i], l);
+          float B[R], C[R], v[2 * R];
+          lds_get(own + s * 2 * NP + q.n, B);
+          lds_get(own + s * 2 * NP + NP + q.n, C);
+          pB[l] = pA[l] = 0.f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float g = fmaf(C[r], gs, e[r]);
+            v[r] = g * dus;
+            v[R + r] = gs * (s == G - 1 ? h[r] : hb[s == G - 1 ? s : s + 1][r]);
+            pB[l] = fmaf(g, B[r], pB[l]);
+            e[r] = g * a[s][r];
+            const float x = e[r] * hb[s][r];
+            pA[l] = fmaf(x, A[r], pA[l]);
+            dA[r] = fmaf(x, ds, dA[r]);
+          }
+          if (!whole)                    // an infinite B or C must not reach the sums through channels that are not there
+#pragma unroll
+            for (int x = 0; x < 2 * R; ++x) v[x] = q.live ? v[x] : 0.f;
+          sum_channels<S, 32, 2 * R>(v);
+          // the values that a lane has left: folds of the bits 32, 16, ... chose them
+          constexpr int LEFT = 2 * R > CH ? 2 * R / CH : 1;
+          int first = 0;
+          bool mine = true;
+#pragma unroll
+          for (int bit = 32, half = R; bit >= S; bit /= 2, half /= 2) {
+            if (half >= 1) first += lane & bit ? half : 0;
+            else mine = mine && !(lane & bit);
+          }
+          if (mine)
+#pragma unroll
+            for (int x = 0; x < LEFT; ++x) to[s][(first + x) / R][q.n + (first + x) % R] = v[x];
+        }
+        gB[i] = sum_to_lane<S, Q>(pB);
+        gA[i] = sum_to_lane<S, Q>(pA);
+      }
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const float dd = slope[i] * fmaf(u[i], gB[i], gA[i]);
+        const bool on = t0 + i * Q + q.j < end;
+        dD = fmaf(go[i], u[i], dD);
+        dbias += on ? dd : 0.f;
+        rows[0][i] = on ? fmaf(D, go[i], d[i] * gB[i]) : 0.f;
+        rows[1][i] = on ? dd : 0.f;
         float g, dg;
         act_pair<ACT_SILU>(z[i], g, dg);
-        el_store<BF>((El<BF>*)p.dz + row * p.lddz + q.e, on ? dy[i] * o[i] * dg : 0.f);
+        rows[2][i] = on ? dy[i] * o[i] * dg : 0.f;
       }
     }
+  if (!LOCAL && begin < end) flush(begin);
+  if constexpr (LOCAL) {
+    if (!q.live) return;
+    const long long m = (long long)q.seg * p.B * p.E + at;
+    store_states(p.seg_q + m * NP + q.n, R, e);
+    total = sum_channel<1, Q>(total);
+    if (q.owner && q.j == 0) p.seg_d[m] = total;
+    return;
   }
-  if (q.live)
-    for (int t = blocks * kSsmBlock + wave * S + q.j; t < p.T; t += W * S) {
-      const long long row = (long long)t * p.B + q.b;
-      if (p.du) el_store<BF>((El<BF>*)p.du + row * p.lddu + q.e, 0.f);
-      if (p.ddelta) el_store<BF>((El<BF>*)p.ddelta + row * p.ldddelta + q.e, 0.f);
-      if (p.dz) el_store<BF>((El<BF>*)p.dz + row * p.lddz + q.e, 0.f);
+  if (out.groups == 1) {               // the steps past the row's length
+    for (long long x = threadIdx.x; x < (long long)(stop - max(begin, end)) * 2 * p.N; x += 64 * W) {
+      const int n = (int)(x % p.N), c = (int)(x / p.N % 2);
+      const long long row = (max(begin, end) + x / (2 * p.N)) * p.B + q.b;
+      if (c ? p.dCm : p.dBm) el_store<BF>((El<BF>*)(c ? p.dCm : p.dBm) + row * (c ? p.lddC : p.lddB) + q.g * p.N + n, 0.f);
     }
-  if (p.dh0 && wave == 0 && q.live) store_states(p.dh0 + st, left, carry);
-  // the waves' sums of the parameters' gradients
-  dD = sum_channel<S>(dD);
-  dbias = sum_channel<S>(dbias);
-  __syncthreads();
-  lds_put(&maps[0][wave][0][lane * R], dA);
-  maps[0][wave][1][lane] = dD;
-  maps[0][wave][2][lane] = dbias;
-  __syncthreads();
-  if (wave || !q.live) return;
-#pragma unroll
-  for (int w = 1; w < W; ++w) {
-    float v[R];
-    lds_get(&maps[0][w][0][lane * R], v);
-#pragma unroll
-    for (int r = 0; r < R; ++r) dA[r] += v[r];
-    dD += maps[0][w][1][lane];
-    dbias += maps[0][w][2][lane];
   }
-  const long long at = (long long)q.b * p.E + q.e;
-  store_states(out.A + at * NP + q.n, R, dA);
-  if (q.j == 0) {
-    out.D[at] = dD;
-    out.bias[at] = dbias;
+  dD = sum_channel<1, Q>(dD);
+  dbias = sum_channel<1, Q>(dbias);
+  if (!q.live) return;
+  if (p.dh0 && q.seg == 0) store_states(p.dh0 + at * p.N + q.n, left, e);
+  const long long m = (long long)q.seg * p.B * p.E + at;
+  store_states(out.A + m * NP + q.n, R, dA);
+  if (q.owner && q.j == 0) {
+    out.D[m] = dD;
+    out.bias[m] = dbias;
   }
 }
 
-// dB and dC: the tiles' sums
+// dB and dC: the workgroups' sums
 template <bool BF>
-__global__ __launch_bounds__(256) void channels_kernel(const SsmParams p, const Parts in, int tiles, int NP) {
+__global__ __launch_bounds__(256) void channels_kernel(const SsmParams p, const Parts in, int NP) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x, all = (long long)p.T * p.B * p.G * 2 * NP;
   if (i >= all) return;
   const int n = (int)(i % NP), c = (int)(i / NP % 2), g = (int)(i / (2 * NP) % p.G);
@@ -320,20 +321,27 @@ __global__ __launch_bounds__(256) void channels_kernel(const SsmParams p, const 
   if (!to) return;
   float s = 0.f;
   if (row / p.B < len)
-    for (int x = 0; x < tiles; ++x) s += in.bc[x * all + i];
+    for (int x = 0; x < in.groups; ++x) s += in.bc[x * all + i];
   el_store<BF>((El<BF>*)to + row * (c ? p.lddC : p.lddB) + g * p.N + n, s);
 }
 
-// dA, dD, ddelta_bias: the rows' sums
+// dA, dD, ddelta_bias: the sums over rows and segments; 64 values a workgroup, every fourth row a wave
 __global__ __launch_bounds__(256) void rows_kernel(const SsmParams p, const Parts in, int NP) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int per = NP + 2, e = (int)(i / per), n = (int)(i % per);
-  if (e >= p.E) return;
+  __shared__ float lds[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = NP + 2;
+  const long long i = (long long)blockIdx.x * 64 + lane;
+  const int e = (int)(i / per), n = (int)(i % per), rows = p.segs * p.B;
   float s = 0.f;
-  for (int b = 0; b < p.B; ++b) {
-    const long long at = (long long)b * p.E + e;
-    s += n < NP ? in.A[at * NP + n] : n == NP ? in.D[at] : in.bias[at];
+  if (e < p.E) {
+    const float* from = n < NP ? in.A + (long long)e * NP + n : (n == NP ? in.D : in.bias) + e;
+    const long long step = (long long)p.E * (n < NP ? NP : 1);
+#pragma unroll 4
+    for (int b = wave; b < rows; b += 4) s += from[b * step];
   }
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave || e >= p.E) return;
+  s = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
   if (n < p.N) {
     if (p.dA) p.dA[(long long)e * p.N + n] = s;
   } else if (n == NP) {
@@ -345,14 +353,20 @@ __global__ __launch_bounds__(256) void rows_kernel(const SsmParams p, const Part
 
 template <bool BF, int S>
 hipError_t start(const SsmParams& p, hipStream_t s) {
-  constexpr int CH = 64 / S, NP = S * kSsmPer;
-  const int tiles = (p.E / p.G + CH - 1) / CH;
-  const Parts parts = parts_of(p, tiles, NP);
-  if (p.B > 0) hipLaunchKernelGGL((bwd_kernel<BF, S>), dim3((unsigned)(tiles * p.G * p.B)), dim3(64 * (kSsmBlock / steps_of(S))), 0, s, p, parts);
+  constexpr int NP = S * kSsmPer;
+  const int groups = ssm_groups(p, S);
+  const Parts parts = parts_of(p, groups, NP);
+  const unsigned tiles = (unsigned)groups * p.G * p.B;
+  const dim3 block(64 * kSsmTiles);
+  if (p.B > 0) {
+    if (p.segs > 1) hipLaunchKernelGGL((bwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1)), block, 0, s, p, parts);
+    hipLaunchKernelGGL((bwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p, parts);
+  }
   const long long all = (long long)p.T * p.B * p.G * 2 * NP;
-  if ((p.dBm || p.dCm) && all) hipLaunchKernelGGL(channels_kernel<BF>, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, p, parts, tiles, NP);
+  if ((p.dBm || p.dCm) && all && groups > 1)
+    hipLaunchKernelGGL(channels_kernel<BF>, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, p, parts, NP);
   if (p.dA || p.dD || p.ddelta_bias)
-    hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(((long long)p.E * (NP + 2) + 255) / 256)), dim3(256), 0, s, p, parts, NP);
+    hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(((long long)p.E * (NP + 2) + 63) / 64)), dim3(256), 0, s, p, parts, NP);
   return hipGetLastError();
 }
 
@@ -368,14 +382,6 @@ hipError_t launch(const SsmParams& p, hipStream_t s) {
 }
 
 }  // namespace
-
-size_t rnnk::ssm_part_floats(int T, int B, int E, int N, int G) {
-  const size_t S = ssm_lanes(N), CH = 64 / S, NP = S * kSsmPer, tiles = (E / G + CH - 1) / CH;
-  return tiles * T * B * G * 2 * NP + (size_t)B * E * (NP + 2);
-}
-size_t rnnk::ssm_start_floats(int T, int B, int E, int N) {
-  return ((size_t)T + kSsmBlock - 1) / kSsmBlock * B * E * ssm_lanes(N) * kSsmPer;
-}
 
 hipError_t rnn_launch_ssm_bwd(const SsmParams& p, int bf16, hipStream_t s) {
   if (p.E == 0) return hipSuccess;

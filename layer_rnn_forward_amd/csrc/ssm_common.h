@@ -66,7 +66,13 @@ struct SsmParams {
   void* y;
   long long ldy;
   float* hy;
-  float* starts;         // the state before every block of steps, or null
+  float* starts;         // the state before every chunk of steps, or null
+  // segments of the time axis and their steps (a whole number of chunks); with
+  // more than one: the state that the first one starts from, the segments' maps
+  int segs, seg_steps;
+  float* seg_first;      // [B][E][NP]
+  float* seg_q;          // [segs][B][E][NP]
+  float* seg_d;          // [segs][B][E]
   const void* dy;        // backward, as what follows
   long long lddy;
   const float* dhy;
@@ -75,8 +81,12 @@ struct SsmParams {
   float *dA, *dD, *ddelta_bias, *dh0;
   float* part;           // workspace of the backward pass
 };
-size_t ssm_start_floats(int T, int B, int E, int N);
-size_t ssm_part_floats(int T, int B, int E, int N, int G);
+// A call's segments (forward's or backward's) and the parts of the workspace, in floats
+struct SsmPlan {
+  int segs[2], seg_steps[2];
+  size_t starts, first, q, d, part, all;   // offsets; all: the size
+};
+SsmPlan ssm_plan(int T, int B, int E, int N, int G, bool save);
 
 // 16 bytes of a row at any alignment
 template <bool BF>
