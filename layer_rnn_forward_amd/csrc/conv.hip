@@ -16,8 +16,9 @@ using namespace rnnk;
 
 namespace {
 
+constexpr int kAhead = 8;     // steps whose loads are asked for at once
+
 constexpr int kWidth = 4;     // channels of a lane
-constexpr int kAhead = 4;     // steps whose loads are asked for at once
 
 // silu and its slope
 __device__ __forceinline__ float silu(float v) {
@@ -34,13 +35,12 @@ struct Place {
 template <int VW>
 __device__ __forceinline__ Place place(const ConvParams& p) {
   Place r;
-  const int tiles = (p.C + 64 * VW - 1) / (64 * VW), groups = (p.pieces + kConvWaves - 1) / kConvWaves;
+  const int tiles = (p.C + 64 * VW - 1) / (64 * VW);
   int i = blockIdx.x;
   const int tile = i % tiles;
   i /= tiles;
   r.b = i % p.B;
   const int piece = i / p.B * kConvWaves + (int)(threadIdx.x >> 6);
-  (void)groups;
   r.c = (tile * 64 + (int)(threadIdx.x & 63)) * VW;
   r.left = p.C - r.c;
   r.t0 = piece * p.piece;
@@ -52,23 +52,28 @@ __device__ __forceinline__ Place place(const ConvParams& p) {
 
 template <int K, int VW>
 __device__ __forceinline__ void load_weights(const ConvParams& p, const Place& at, float (&w)[K][VW], float (&bias)[VW]) {
+  // the lane's weights are neighbours: 16 bytes a load
+  const float* from = p.w + (long long)at.c * K;
+  RawPiece<false, 4> raw[VW * K / 4];
 #pragma unroll
-  for (int j = 0; j < VW; ++j) {
-    const bool on = j < at.left;
+  for (int i = 0; i < VW * K / 4; ++i) raw[i] = load_raw<false, 4>(from + 4 * i, at.left * K - 4 * i);
+  load_piece<false, VW>(p.bias + at.c, p.bias ? at.left : 0, bias);
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][j] = on ? p.w[(long long)(at.c + j) * K + k] : 0.f;
-    bias[j] = on && p.bias ? p.bias[at.c + j] : 0.f;
-  }
+  for (int j = 0; j < VW; ++j)
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][j] = __uint_as_float(raw[(j * K + k) / 4].w[(j * K + k) % 4]);
 }
 
 // input of step t >= -(K - 1); steps past the row's length are not used
 template <bool BF, int K, int VW>
+__device__ __forceinline__ RawPiece<BF, VW> input(const ConvParams& p, const Place& at, int t) {
+  const El<BF>* from = t >= 0 ? (const El<BF>*)p.x + ((long long)t * p.B + at.b) * p.ldx + at.c
+                              : (const El<BF>*)p.s0 + ((long long)(t + K - 1) * p.B + at.b) * p.C + at.c;
+  return load_raw<BF, VW>(from, (t >= 0 ? t < at.len : p.s0 != nullptr) ? at.left : 0);
+}
+template <bool BF, int K, int VW>
 __device__ __forceinline__ void input(const ConvParams& p, const Place& at, int t, float (&v)[VW]) {
-  if (t >= 0) {
-    load_piece<BF, VW>((const El<BF>*)p.x + ((long long)t * p.B + at.b) * p.ldx + at.c, t < at.len ? at.left : 0, v);
-  } else {
-    load_piece<BF, VW>((const El<BF>*)p.s0 + ((long long)(t + K - 1) * p.B + at.b) * p.C + at.c, p.s0 ? at.left : 0, v);
-  }
+  unpack<BF, VW>(input<BF, K, VW>(p, at, t), v);
 }
 
 // the inputs before the step that follows the row's last
@@ -92,21 +97,26 @@ __global__ __launch_bounds__(64 * kConvWaves) void fwd_kernel(const ConvParams p
   load_weights<K, VW>(p, at, w, bias);
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) input<BF, K, VW>(p, at, at.t0 - (K - 1) + k, x[k + 1]);
-  for (int t = at.t0; t < at.t1; t += kAhead) {
-    float in[kAhead][VW];
+  RawPiece<BF, VW> raw[kAhead], next[kAhead];
+  auto load = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (t + i < at.t1) input<BF, K, VW>(p, at, t + i, in[i]);
-    }
+    for (int i = 0; i < kAhead; ++i) next[i] = input<BF, K, VW>(p, at, min(t + i, at.t1 - 1));
+  };
+  if (at.t0 < at.t1) load(at.t0);
+  for (int t = at.t0; t < at.t1; t += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
+    if (t + kAhead < at.t1) load(t + kAhead);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (t + i >= at.t1) break;
-      float v[VW];
+      float v[VW], in[VW];
+      unpack<BF, VW>(raw[i], in);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) x[k][j] = x[k + 1][j];
-        x[K - 1][j] = in[i][j];
+        x[K - 1][j] = in[j];
         v[j] = bias[j];
 #pragma unroll
         for (int k = 0; k < K; ++k) v[j] = fmaf(w[k][j], x[k][j], v[j]);
@@ -145,23 +155,22 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
     // after step t the gradient of input t - K + 1 is whole
     const int end = at.t1 + K - 1;
     for (int t = at.t0; t < end; t += kAhead) {
-      float in[kAhead][VW], dy[kAhead][VW];
+      RawPiece<BF, VW> rx[kAhead], rdy[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (t + i < p.T && t + i < end) {
-          input<BF, K, VW>(p, at, t + i, in[i]);
-          load_piece<BF, VW>((const El<BF>*)p.dy + ((long long)(t + i) * p.B + at.b) * p.lddy + at.c, t + i < at.len ? at.left : 0, dy[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < VW; ++j) in[i][j] = dy[i][j] = 0.f;
-        }
+        const int s = min(t + i, end - 1);
+        const int left = s < at.len ? at.left : 0;
+        rx[i] = load_raw<BF, VW>((const El<BF>*)p.x + ((long long)s * p.B + at.b) * p.ldx + at.c, left);
+        rdy[i] = load_raw<BF, VW>((const El<BF>*)p.dy + ((long long)s * p.B + at.b) * p.lddy + at.c, left);
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (t + i >= end) break;
         const int s = t + i - (K - 1);      // the input whose gradient is whole
         const bool mine = t + i < at.t1;
-        float dx[VW], more[VW];
+        float dx[VW], more[VW], in[VW], dy[VW];
+        unpack<BF, VW>(rx[i], in);
+        unpack<BF, VW>(rdy[i], dy);
         const int j0 = s - at.len + K - 1;
         const bool last = p.dsy && j0 >= 0 && j0 < K - 1 && (s >= at.t0 || at.t0 == 0);
         if (last) load_piece<BF, VW>((const El<BF>*)p.dsy + ((long long)j0 * p.B + at.b) * p.C + at.c, at.left, more);
@@ -169,8 +178,8 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
         for (int j = 0; j < VW; ++j) {
 #pragma unroll
           for (int k = 0; k < K - 1; ++k) x[k][j] = x[k + 1][j];
-          x[K - 1][j] = in[i][j];
-          float d = dy[i][j];
+          x[K - 1][j] = in[j];
+          float d = dy[j];
           if (p.silu) {
             float v = bias[j], a, da;
 #pragma unroll
@@ -217,18 +226,11 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
   }
 }
 
-// the pieces' sums: 64 channels a workgroup, a quarter of the pieces a wave
-__global__ __launch_bounds__(256) void sum_kernel(const ConvParams p, int rows) {
-  __shared__ float lds[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long long n = (long long)(p.K + 1) * p.C, i = (long long)blockIdx.x * 64 + lane;
-  float s = 0.f;
-  if (i < n)
-    for (int r = wave; r < rows; r += 4) s += p.part[r * n + i];
-  lds[wave][lane] = s;
-  __syncthreads();
-  if (wave || i >= n) return;
-  s = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+__global__ __launch_bounds__(64 * kSumWaves) void sum_kernel(const ConvParams p, int rows) {
+  __shared__ float lds[kSumWaves][64];
+  const long long n = (long long)(p.K + 1) * p.C, i = (long long)blockIdx.x * 64 + (threadIdx.x & 63);
+  const float s = column_sum(p.part, n, i, rows, lds);
+  if (threadIdx.x >= 64 || i >= n) return;
   const int k = (int)(i / p.C), c = (int)(i - (long long)k * p.C);
   if (k == p.K) {
     if (p.dbias) p.dbias[c] = s;
@@ -264,8 +266,8 @@ void start(const ConvParams& p, Pass what, hipStream_t s) {
     hipLaunchKernelGGL((step_kernel<BF, K>), dim3((unsigned)(((long long)p.B * p.C + 255) / 256)), dim3(256), 0, s, p);
     return;
   }
-  const long long tiles = (p.C + 64 * kWidth - 1) / (64 * kWidth), groups = (p.pieces + kConvWaves - 1) / kConvWaves;
-  const dim3 grid((unsigned)(tiles * p.B * groups)), block(64 * kConvWaves);
+  const long long width = 64 * kWidth, tiles = (p.C + width - 1) / width;
+  const dim3 grid((unsigned)(tiles * p.B * ((p.pieces + kConvWaves - 1) / kConvWaves))), block(64 * kConvWaves);
   if (what == FWD) hipLaunchKernelGGL((fwd_kernel<BF, K>), grid, block, 0, s, p);
   else hipLaunchKernelGGL((bwd_kernel<BF, K>), grid, block, 0, s, p);
 }
@@ -286,8 +288,6 @@ void pick(const ConvParams& p, Pass what, hipStream_t s) {
 
 hipError_t launch(const ConvParams& p, Pass what, int bf16, hipStream_t s) {
   if (p.B == 0 || p.C == 0) return hipSuccess;
-  const long long tiles = (p.C + 64 * kWidth - 1) / (64 * kWidth), groups = (p.pieces + kConvWaves - 1) / kConvWaves;
-  if (what != STEP && tiles * p.B * groups > 0x7fffffffLL) return hipErrorInvalidValue;
   if (bf16) pick<true>(p, what, s);
   else pick<false>(p, what, s);
   return hipGetLastError();
@@ -313,6 +313,6 @@ hipError_t rnn_launch_conv_bwd(const ConvParams& q, int bf16, hipStream_t s) {
   const hipError_t e = launch(p, BWD, bf16, s);
   if (e != hipSuccess || !sums || p.C == 0) return e;
   const int rows = p.B * ((p.pieces + kConvWaves - 1) / kConvWaves);
-  hipLaunchKernelGGL(sum_kernel, dim3((unsigned)(((long long)(p.K + 1) * p.C + 63) / 64)), dim3(256), 0, s, p, rows);
+  hipLaunchKernelGGL(sum_kernel, dim3((unsigned)(((long long)(p.K + 1) * p.C + 63) / 64)), dim3(64 * kSumWaves), 0, s, p, rows);
   return hipGetLastError();
 }

@@ -45,17 +45,19 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void fwd_kernel(const 
   const El<BF>* x = (const El<BF>*)p.x + at;
   const El<BF>* r = (const El<BF>*)p.residual + at;
   float v[P][VW], sum = 0.f;
+  RawPiece<BF, VW> rx[P], rr[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int c = (i * L + lane) * VW;
-    load_piece<BF, VW>(x + c, p.D - c, v[i]);
-  }
+  for (int i = 0; i < P; ++i) rx[i] = load_raw<BF, VW>(x + (i * L + lane) * VW, p.D - (i * L + lane) * VW);
+  if (p.residual)
+#pragma unroll
+    for (int i = 0; i < P; ++i) rr[i] = load_raw<BF, VW>(r + (i * L + lane) * VW, p.D - (i * L + lane) * VW);
+#pragma unroll
+  for (int i = 0; i < P; ++i) unpack<BF, VW>(rx[i], v[i]);
   if (p.residual) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int c = (i * L + lane) * VW;
       float b[VW];
-      load_piece<BF, VW>(r + c, p.D - c, b);
+      unpack<BF, VW>(rr[i], b);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         v[i][j] += b[j];
@@ -107,45 +109,46 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void fwd_kernel(const 
 }
 
 // dx = rstd (g - mean(g) - xh mean(g xh)) + dtotal, g = dy weight (without
-// mean(g) for RMS); the rows' sums of dy xh and dy go to `part`
-template <bool BF, int L, int P>
-__global__ __launch_bounds__(L < kThreads ? kThreads : L) void bwd_kernel(const NormParams p) {
-  constexpr int VW = piece_width<BF>(), ROWS = L < kThreads ? kThreads / L : 1;
+// mean(g) for RMS); the rows' sums of dy xh and (BIAS) dy go to `part`, a row of
+// them for each workgroup
+constexpr int back_threads(int L) { return L == 64 ? 512 : L; }
+template <bool BF, int L, int P, bool BIAS>
+__global__ __launch_bounds__(back_threads(L)) void bwd_kernel(const NormParams p) {
+  constexpr int VW = piece_width<BF>(), ROWS = back_threads(L) / L;
   __shared__ float lds[2 * (L / 64)];
+  __shared__ float both[ROWS > 1 ? 2 * P * L * VW : 1];
   int slot = 0;
   const int lane = threadIdx.x % L;
   const int group = blockIdx.x * ROWS + threadIdx.x / L, groups = gridDim.x * ROWS;
-  float w[P][VW], dw[P][VW], db[P][VW];
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int c = (i * L + lane) * VW;
-    if (p.weight) load_piece<false, VW>(p.weight + c, p.D - c, w[i]);
-#pragma unroll
-    for (int j = 0; j < VW; ++j) {
-      if (!p.weight) w[i][j] = 1.f;
-      dw[i][j] = db[i][j] = 0.f;
-    }
-  }
+  float dw[P][VW] = {}, db[BIAS ? P : 1][VW] = {};
   const float inv = 1.f / (float)p.D;
   for (long long row = group; row < p.M; row += groups) {
     const long long at = row * p.D;
     const float mean = p.stats[2 * row], rstd = p.stats[2 * row + 1];
+    RawPiece<BF, VW> rx[P], rg[P], rt[P];
     float x[P][VW], g[P][VW], s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c = (i * L + lane) * VW;
-      load_piece<BF, VW>((const El<BF>*)p.x + at + c, p.D - c, x[i]);
-      load_piece<BF, VW>((const El<BF>*)p.dy + at + c, p.D - c, g[i]);
+      rx[i] = load_raw<BF, VW>((const El<BF>*)p.x + at + c, p.D - c);
+      rg[i] = load_raw<BF, VW>((const El<BF>*)p.dy + at + c, p.D - c);
     }
+    if (p.dtotal)
+#pragma unroll
+      for (int i = 0; i < P; ++i) rt[i] = load_raw<BF, VW>((const El<BF>*)p.dtotal + at + (i * L + lane) * VW, p.D - (i * L + lane) * VW);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int left = p.D - (i * L + lane) * VW;
+      const int c = (i * L + lane) * VW, left = p.D - c;
+      float w[VW];
+      if (p.weight) load_piece<false, VW>(p.weight + c, left, w);
+      unpack<BF, VW>(rx[i], x[i]);
+      unpack<BF, VW>(rg[i], g[i]);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         x[i][j] = j < left ? (x[i][j] - mean) * rstd : 0.f;
         dw[i][j] = fmaf(g[i][j], x[i][j], dw[i][j]);
-        db[i][j] += g[i][j];
-        g[i][j] *= w[i][j];
+        if constexpr (BIAS) db[i][j] += g[i][j];
+        if (p.weight) g[i][j] *= w[j];
         s0 += g[i][j];
         s1 = fmaf(g[i][j], x[i][j], s1);
       }
@@ -157,7 +160,7 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void bwd_kernel(const 
     for (int i = 0; i < P; ++i) {
       const int c = (i * L + lane) * VW, left = p.D - c;
       float t[VW];
-      if (p.dtotal) load_piece<BF, VW>((const El<BF>*)p.dtotal + at + c, left, t);
+      if (p.dtotal) unpack<BF, VW>(rt[i], t);
 #pragma unroll
       for (int j = 0; j < VW; ++j) {
         const float d = rstd * (g[i][j] - fmaf(x[i][j], s1, s0));
@@ -167,12 +170,34 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void bwd_kernel(const 
     }
   }
   if (!p.part) return;
+  // the waves' sums, one wave after the other
+  if constexpr (ROWS > 1) {
+    for (int r = 0; r < ROWS; ++r) {
+      if ((int)threadIdx.x / L == r) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            float* to = both + (i * VW + j) * L + lane;
+            if (r > 0) dw[i][j] += *to;
+            *to = dw[i][j];
+            if constexpr (BIAS) {
+              to += P * L * VW;
+              if (r > 0) db[i][j] += *to;
+              *to = db[i][j];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    if ((int)threadIdx.x / L != ROWS - 1) return;
+  }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int c = (i * L + lane) * VW, left = p.D - c;
-    float* to = p.part + (long long)group * 2 * p.D + c;
+    float* to = p.part + (long long)blockIdx.x * (BIAS ? 2 : 1) * p.D + c;
     store_piece<false, VW>(to, left, dw[i]);
-    store_piece<false, VW>(to + p.D, left, db[i]);
+    if constexpr (BIAS) store_piece<false, VW>(to + p.D, left, db[i]);
   }
 }
 
@@ -288,80 +313,78 @@ __global__ __launch_bounds__(kThreads) void columns_kernel(const NormParams p) {
     dw = fmaf(g, (x - p.stats[2 * row]) * p.stats[2 * row + 1], dw);
     db += g;
   }
-  float* to = p.part + (long long)blockIdx.y * 2 * p.D + c;
+  float* to = p.part + (long long)blockIdx.y * (p.dbias ? 2 : 1) * p.D + c;
   to[0] = dw;
-  to[p.D] = db;
+  if (p.dbias) to[p.D] = db;
 }
 
-// columns of the partial sums: 64 columns a workgroup, its four waves a quarter of the rows each
-__global__ __launch_bounds__(256) void sum_kernel(const NormParams p) {
-  __shared__ float lds[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long long c = (long long)blockIdx.x * 64 + lane, n = 2LL * p.D;
-  float s = 0.f;
-  if (c < n)
-    for (int i = wave; i < p.parts; i += 4) s += p.part[i * n + c];
-  lds[wave][lane] = s;
-  __syncthreads();
-  if (wave || c >= n) return;
-  s = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
-  if (c < p.D) {
-    if (p.dweight) p.dweight[c] = s;
-  } else if (p.dbias) {
-    p.dbias[c - p.D] = s;
-  }
+__global__ __launch_bounds__(64 * kSumWaves) void sum_kernel(const NormParams p) {
+  __shared__ float lds[kSumWaves][64];
+  const long long c = (long long)blockIdx.x * 64 + (threadIdx.x & 63), n = (p.dbias ? 2LL : 1LL) * p.D;
+  const float s = column_sum(p.part, n, c, p.parts, lds);
+  if (threadIdx.x >= 64 || c >= n) return;
+  if (c >= p.D) p.dbias[c - p.D] = s;
+  else if (p.dweight) p.dweight[c] = s;
 }
 
 // Lanes and pieces of a row.
 struct Shape {
   int lanes, pieces;       // lanes 0: too long for registers
 };
-constexpr int kMost = 32;  // values of a row that a lane holds at most
-Shape shape(int M, int D, int vw) {
+constexpr int kMost = 32;  // values of a row that a lane holds at most (of 1024 lanes: half of it, a quarter of the registers)
+Shape shape(int D, int vw) {
   const int pieces = (D + vw - 1) / vw;
   Shape s;
-  // a wave a row needs no barrier; few rows spread over more lanes
-  s.lanes = pieces <= 64 || (pieces <= 64 * (kMost / vw) && M >= 1024) ? 64 : pieces <= 256 * (kMost / vw) ? 256 : 1024;
+  // a wave a row where it holds the row in one piece a lane; a workgroup with few
+  // pieces a lane hides more latency than a wave with many (16384 x 2048 bf16
+  // backward 47 us, with a wave a row 51)
+  s.lanes = pieces <= 64 ? 64 : pieces <= 256 * (kMost / vw) ? 256 : 1024;
   s.pieces = 1;
   while (s.pieces * s.lanes < pieces) s.pieces *= 2;
-  if (s.pieces * vw > kMost) s.lanes = 0;
+  if (s.pieces * vw > (s.lanes == 1024 ? kMost / 2 : kMost)) s.lanes = 0;
   return s;
 }
 
 template <bool BF, int L, int P>
 void start(const NormParams& p, bool back, int blocks, hipStream_t s) {
   constexpr int threads = L < kThreads ? kThreads : L, rows = threads / L;
-  if (back) hipLaunchKernelGGL((bwd_kernel<BF, L, P>), dim3(blocks), dim3(threads), 0, s, p);
+  if (back && p.dbias) hipLaunchKernelGGL((bwd_kernel<BF, L, P, true>), dim3(blocks), dim3(back_threads(L)), 0, s, p);
+  else if (back) hipLaunchKernelGGL((bwd_kernel<BF, L, P, false>), dim3(blocks), dim3(back_threads(L)), 0, s, p);
   else hipLaunchKernelGGL((fwd_kernel<BF, L, P>), dim3((unsigned)(((long long)p.M + rows - 1) / rows)), dim3(threads), 0, s, p);
 }
 
-template <bool BF, int L>
-void pick(const NormParams& p, bool back, int pieces, int blocks, hipStream_t s) {
-  if (pieces == 1) start<BF, L, 1>(p, back, blocks, s);
-  else if (pieces == 2) start<BF, L, 2>(p, back, blocks, s);
-  else if (pieces == 4) start<BF, L, 4>(p, back, blocks, s);
-  else if constexpr (!BF) start<BF, L, 8>(p, back, blocks, s);
+template <bool BF>
+void pick(const NormParams& p, bool back, const Shape& sh, int blocks, hipStream_t s) {
+  const int n = sh.pieces;
+  if (sh.lanes == 64) return start<BF, 64, 1>(p, back, blocks, s);
+  if (sh.lanes == 256) {
+    if (n == 1) return start<BF, 256, 1>(p, back, blocks, s);
+    if (n == 2) return start<BF, 256, 2>(p, back, blocks, s);
+    if (BF || n == 4) return start<BF, 256, 4>(p, back, blocks, s);
+    return start<BF, 256, BF ? 4 : 8>(p, back, blocks, s);
+  }
+  if (BF || n == 2) return start<BF, 1024, 2>(p, back, blocks, s);   // more than 8192 columns
+  start<BF, 1024, BF ? 2 : 4>(p, back, blocks, s);
 }
 
-// workgroups of the backward launch: 64-lane rows, four a workgroup
+// workgroups of the backward launch, and rows of partial sums
 int back_blocks(int M, int lanes) {
-  if (lanes == 64) return std::max(1, std::min((M + 3) / 4, 512));
-  return std::max(1, std::min(M, lanes == 256 ? 1024 : 256));
+  if (lanes == 64) return std::max(1, std::min((M + 7) / 8, 512));
+  return std::max(1, std::min(M, lanes == 1024 ? 256 : 1024));
 }
+int back_parts(int M, int lanes) { return lanes ? back_blocks(M, lanes) : std::min(M, 64); }
 
 template <bool BF>
 hipError_t launch(const NormParams& p, bool back, hipStream_t s) {
-  const Shape sh = shape(p.M, p.D, piece_width<BF>());
+  const Shape sh = shape(p.D, piece_width<BF>());
   if (sh.lanes) {
     const int blocks = back ? back_blocks(p.M, sh.lanes) : 0;
-    if (sh.lanes == 64) pick<BF, 64>(p, back, sh.pieces, blocks, s);
-    else if (sh.lanes == 256) pick<BF, 256>(p, back, sh.pieces, blocks, s);
-    else pick<BF, 1024>(p, back, sh.pieces, blocks, s);
+    pick<BF>(p, back, sh, blocks, s);
   } else if (!back) {
     hipLaunchKernelGGL(fwd_long_kernel<BF>, dim3(p.M), dim3(1024), 0, s, p);
   } else {
     if (p.dx) hipLaunchKernelGGL(bwd_long_kernel<BF>, dim3(p.M), dim3(1024), 0, s, p);
-    if (p.part) hipLaunchKernelGGL(columns_kernel<BF>, dim3((p.D + kThreads - 1) / kThreads, p.parts), dim3(kThreads), 0, s, p);
+    if (p.part) hipLaunchKernelGGL(columns_kernel<BF>, dim3((p.D + kThreads - 1) / kThreads, (unsigned)p.parts), dim3(kThreads), 0, s, p);
   }
   return hipGetLastError();
 }
@@ -372,8 +395,8 @@ hipError_t launch(const NormParams& p, bool back, hipStream_t s) {
 int rnnk::norm_parts(int M, int D) {
   int most = 1;
   for (int vw : {4, 8}) {
-    const Shape sh = shape(M, D, vw);
-    most = std::max(most, sh.lanes == 0 ? std::min(M, 64) : back_blocks(M, sh.lanes) * (sh.lanes == 64 ? 4 : 1));
+    const Shape sh = shape(D, vw);
+    most = std::max(most, back_parts(M, sh.lanes));
   }
   return most;
 }
@@ -388,12 +411,12 @@ hipError_t rnn_launch_norm_bwd(const NormParams& q, int bf16, hipStream_t s) {
   NormParams p = q;
   const bool sums = p.dweight || p.dbias;
   if (!sums) p.part = nullptr;
-  const Shape sh = shape(p.M, p.D, bf16 ? 8 : 4);
-  p.parts = p.M == 0 ? 0 : sh.lanes == 0 ? std::min(p.M, 64) : back_blocks(p.M, sh.lanes) * (sh.lanes == 64 ? 4 : 1);
+  const Shape sh = shape(p.D, bf16 ? 8 : 4);
+  p.parts = p.M == 0 ? 0 : back_parts(p.M, sh.lanes);
   if (p.M > 0 && (p.dx || sums)) {
     const hipError_t e = bf16 ? launch<true>(p, true, s) : launch<false>(p, true, s);
     if (e != hipSuccess) return e;
   }
-  if (sums) hipLaunchKernelGGL(sum_kernel, dim3((unsigned)((2LL * p.D + 63) / 64)), dim3(256), 0, s, p);
+  if (sums) hipLaunchKernelGGL(sum_kernel, dim3((unsigned)(((p.dbias ? 2LL : 1LL) * p.D + 63) / 64)), dim3(64 * kSumWaves), 0, s, p);
   return hipGetLastError();
 }

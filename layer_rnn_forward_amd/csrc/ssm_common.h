@@ -92,26 +92,43 @@ SsmPlan ssm_plan(int T, int B, int E, int N, int G, bool save);
 template <bool BF>
 constexpr int piece_width() { return BF ? 8 : 4; }
 
-// VW neighbouring elements (VW * size: 4, 8 or 16 bytes); those from `left` on are not there
+// VW neighbouring elements (VW * size: 8 or 16 bytes) as they are in memory;
+// those from `left` on are not there and read as 0.  (Unpacked where they are
+// used: a conversion next to the load would wait for it, and the loads would
+// come one after the other.)
 template <bool BF, int VW>
-__device__ __forceinline__ void load_piece(const El<BF>* p, int left, float (&o)[VW]) {
+using RawPiece = Bytes<VW*(BF ? 2 : 4)>;
+template <bool BF, int VW>
+__device__ __forceinline__ RawPiece<BF, VW> load_raw(const El<BF>* p, int left) {
+  RawPiece<BF, VW> w = {};
   if (left >= VW) {
-    constexpr int ES = BF ? 2 : 4;
-    const auto w = *reinterpret_cast<const Bytes<VW * ES>*>(p);
-    if constexpr (BF) {
+    w = *reinterpret_cast<const RawPiece<BF, VW>*>(p);
+  } else {
 #pragma unroll
-      for (int j = 0; j < VW / 2; ++j) {
-        o[2 * j] = __uint_as_float(w.w[j] << 16);
-        o[2 * j + 1] = __uint_as_float(w.w[j] & 0xffff0000u);
+    for (int j = 0; j < VW - 1; ++j)
+      if (j < left) {
+        if constexpr (BF) w.w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+        else w.w[j] = __float_as_uint(p[j]);
       }
-    } else {
+  }
+  return w;
+}
+template <bool BF, int VW>
+__device__ __forceinline__ void unpack(const RawPiece<BF, VW>& w, float (&o)[VW]) {
+  if constexpr (BF) {
 #pragma unroll
-      for (int j = 0; j < VW; ++j) o[j] = __uint_as_float(w.w[j]);
+    for (int j = 0; j < VW / 2; ++j) {
+      o[2 * j] = __uint_as_float(w.w[j] << 16);
+      o[2 * j + 1] = __uint_as_float(w.w[j] & 0xffff0000u);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < VW; ++j) o[j] = j < left ? el_load<BF>(p + j) : 0.f;
+    for (int j = 0; j < VW; ++j) o[j] = __uint_as_float(w.w[j]);
   }
+}
+template <bool BF, int VW>
+__device__ __forceinline__ void load_piece(const El<BF>* p, int left, float (&o)[VW]) {
+  unpack<BF, VW>(load_raw<BF, VW>(p, left), o);
 }
 template <bool BF, int VW>
 __device__ __forceinline__ void store_piece(El<BF>* p, int left, const float (&v)[VW]) {
@@ -169,6 +186,24 @@ __device__ __forceinline__ float sum_lanes(float v) {
   if constexpr (FROM <= 2) v += lane_xor<2>(v);
   if constexpr (FROM <= 1) v += lane_xor<1>(v);
   return v;
+}
+
+// Column i of `rows` rows of n partial sums: a workgroup of 16 waves takes 64
+// columns, every 16th row a wave; the sum is the first wave's.
+constexpr int kSumWaves = 16;
+__device__ __forceinline__ float column_sum(const float* part, long long n, long long i, int rows, float (*lds)[64]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float s = 0.f;
+  if (i < n)
+#pragma unroll 8
+    for (int r = wave; r < rows; r += kSumWaves) s += part[r * n + i];
+  lds[wave][lane] = s;
+  __syncthreads();
+  s = 0.f;
+  if (wave == 0)
+#pragma unroll
+    for (int w = 0; w < kSumWaves; ++w) s += lds[w][lane];
+  return s;
 }
 
 }  // namespace rnnk

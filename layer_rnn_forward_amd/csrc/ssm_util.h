@@ -197,7 +197,7 @@ __device__ __forceinline__ void store_own(SsmRows& r, const SsmPlace& q, int lef
 template <int G, int NP>
 constexpr int bc_pieces() { return (G * 2 * (NP / 4) + 63) / 64; }
 template <bool BF>
-using RawFour = Bytes<BF ? 8 : 16>;
+using RawFour = RawPiece<BF, 4>;
 template <bool BF, int G, int NP>
 __device__ __forceinline__ void load_bc(const SsmParams& p, const SsmPlace& q, int t0, RawFour<BF> (&v)[bc_pieces<G, NP>()]) {
   constexpr int PP = NP / 4;
@@ -208,19 +208,7 @@ __device__ __forceinline__ void load_bc(const SsmParams& p, const SsmPlace& q, i
     const bool c = x / PP % 2, on = t < q.len && x < G * 2 * PP;
     const long long row = (long long)(on ? t : q.len - 1) * p.B + q.b;
     const El<BF>* from = (const El<BF>*)(c ? p.Cm : p.Bm) + row * (c ? p.ldC : p.ldB) + q.g * p.N + n;
-    const int left = on ? p.N - n : 0;
-    v[i] = {};
-    if (left >= 4) {
-      v[i] = *reinterpret_cast<const RawFour<BF>*>(from);
-    } else if constexpr (BF) {
-      if (left > 0) v[i].w[0] = from[0];
-      if (left > 1) v[i].w[0] |= (uint32_t)from[1] << 16;
-      if (left > 2) v[i].w[1] = from[2];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (left > k) v[i].w[k] = __float_as_uint(from[k]);
-    }
+    v[i] = load_raw<BF, 4>(from, on ? p.N - n : 0);
   }
 }
 template <bool BF, int G, int NP>
