@@ -70,7 +70,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
     }
   } else {
     load_states(p.seg_first + at * NP + q.n, R, h);
-    for (int i = 0; i < q.seg; ++i) {
+    for (int i = 0; i < q.seg * p.sub; ++i) {
       float Q[R];
       const long long m = (long long)i * p.B * p.E + at;
       load_states(p.seg_q + m * NP + q.n, R, Q);
@@ -82,7 +82,8 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
 #pragma unroll
   for (int r = 0; r < R; ++r) A[r] *= kLog2e;
   const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
-  const int begin = q.seg * p.seg_steps, stop = min(begin + p.seg_steps, p.T), end = min(stop, q.len);
+  const int steps = LOCAL ? p.seg_steps / p.sub : p.seg_steps;
+  const int begin = min(q.seg * steps, p.T), stop = min(begin + steps, p.T), end = min(stop, q.len);
   SsmRows xu = ssm_rows<BF, Q>(p, q, p.u, p.ldu, begin), xd = ssm_rows<BF, Q>(p, q, p.delta, p.lddelta, begin),
           xz = ssm_rows<BF, Q>(p, q, p.z, p.ldz, begin), xy = ssm_rows<BF, Q>(p, q, p.y, p.ldy, begin);
   El<BF> ru[I], rd[I], rz[I] = {};
@@ -196,7 +197,7 @@ hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
     hipLaunchKernelGGL((step_kernel<BF, S>), dim3(tiles), block, 0, s, p);
     return hipGetLastError();
   }
-  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1)), block, 0, s, p);
+  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p);
   hipLaunchKernelGGL((fwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p);
   return hipGetLastError();
 }
@@ -227,12 +228,19 @@ SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
   SsmPlan r{};
   const int S = ssm_lanes(N), CH = 64 / S, step = ssm_chunk(S), NP = S * kSsmPer;
   const long long tiles = (long long)(E / G + CH - 1) / CH * G * B;
-  for (int back = 0; back < 2; ++back) {
-    const int segs = back ? segments(tiles, T, 1300, 2048) : segments(tiles, T, 800, 4096);
-    r.seg_steps[back] = std::max(step, ((T + segs - 1) / segs + step - 1) / step * step);
+  size_t segs = 1;
+  for (int back = 0; back < (save ? 2 : 1); ++back) {
+    const int n = back ? segments(tiles, T, 1300, 2048) : segments(tiles, T, 800, 4096);
+    // the first launch's waves need fewer registers: it cuts the segments into parts until it has 4096
+    int sub = 1;
+    while (n > 1 && tiles * (n - 1) * sub < 2048 && T / (n * sub) >= 64) sub *= 2;
+    const int whole = step * sub;
+    r.sub[back] = sub;
+    r.seg_steps[back] = std::max(whole, ((T + n - 1) / n + whole - 1) / whole * whole);
     r.segs[back] = std::max(1, (T + r.seg_steps[back] - 1) / r.seg_steps[back]);
+    if (r.segs[back] > 1) segs = std::max(segs, (size_t)r.segs[back] * sub);
   }
-  const size_t C = (size_t)B * E, segs = std::max(r.segs[0], save ? r.segs[1] : 1);
+  const size_t C = (size_t)B * E;
   size_t o = 0;
   auto take = [&o](size_t floats) {
     const size_t at = o;

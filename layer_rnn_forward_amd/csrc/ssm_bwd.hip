@@ -37,8 +37,10 @@ Parts parts_of(const SsmParams& p, int groups, int NP) {
 }
 
 // V values a lane, summed over the lanes whose indexes differ in the bits BIT
-// (32 first) down to S: while there are several values each fold halves them,
-// then every lane gets the sum.  Lane bit 32 holds the upper half of the values, ...
+// (32 first) down to S: while there are several values each fold halves them
+// (lanes with the bit set go on with the upper half), then every lane gets the
+// sum.  sums_left(), first_sum(): how many values a lane has left, and which;
+// has_sums(): whether the lane is the one of several with the same to keep them.
 template <int S, int BIT, int V>
 __device__ __forceinline__ void sum_channels(float (&v)[V]) {
   if constexpr (BIT >= S) {
@@ -56,32 +58,54 @@ __device__ __forceinline__ void sum_channels(float (&v)[V]) {
     }
   }
 }
+template <int S, int V>
+constexpr int sums_left() { return V * S > 64 ? V * S / 64 : 1; }
+template <int S, int V>
+__device__ __forceinline__ int first_sum(int lane) {
+  int first = 0;
+#pragma unroll
+  for (int bit = 32, half = V / 2; bit >= S && half >= 1; bit /= 2, half /= 2) first += lane & bit ? half : 0;
+  return first;
+}
+template <int S, int V>
+__device__ __forceinline__ bool has_sums(int lane) {
+  bool mine = true;
+#pragma unroll
+  for (int bit = 32, half = V / 2; bit >= S; bit /= 2, half /= 2)
+    if (half < 1) mine = mine && !(lane & bit);
+  return mine;
+}
 
 // LOCAL: the segments' maps of g (but the first one's), no outputs
 template <bool BF, int S, bool LOCAL>
 __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams p, const Parts out) {
   constexpr int R = kSsmPer, G = kSsmKeep, NP = S * R, Q = S < 4 ? S : 4, I = G / Q, CH = 64 / S, W = kSsmTiles;
   __shared__ __align__(16) float bc[W][G][2][NP];
+  __shared__ __align__(16) float zeros[LOCAL ? 1 : G][2][NP];
   __shared__ float sums[LOCAL ? 1 : 2][W][G][2][NP];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   SsmPlace q = ssm_place<S>(p, blockIdx.x, wave);
-  if (LOCAL) ++q.seg;
+  if (LOCAL) q.seg += p.sub;             // in parts of segments, of which the first segment's are not needed
   if (LOCAL && !__any(q.live)) return;
   const int left = q.live ? p.N - q.n : 0;
-  const bool whole = __all(q.live);
+  // Lanes of channels that are not there read zeros for B and C: an infinite one
+  // must not reach the sums over channels through them.  (Every wave writes them.)
+  if constexpr (!LOCAL)
+    for (int x = lane; x < G * 2 * NP; x += 64) (&zeros[0][0][0])[x] = 0.f;
+  const float* const bcs = (LOCAL || q.live ? &bc[wave][0][0][0] : &zeros[0][0][0]) + q.n;
   const long long at = (long long)q.b * p.E + q.e;
   float A[R], e[R] = {}, dA[R] = {}, dD = 0.f, dbias = 0.f, total = 0.f;
   load_states(p.A + (long long)q.e * p.N + q.n, left, A);
   if (p.segs == 1 || LOCAL) {
     if (p.dhy) load_states(p.dhy + at * p.N + q.n, left, e);
     if (LOCAL) {                       // dhy may be written over by the first segment
-      if (q.seg == p.segs - 1 && q.live) store_states(p.seg_first + at * NP + q.n, R, e);
+      if (q.seg == p.segs * p.sub - 1 && q.live) store_states(p.seg_first + at * NP + q.n, R, e);
 #pragma unroll
       for (int r = 0; r < R; ++r) e[r] = 0.f;
     }
   } else if (q.live) {
     load_states(p.seg_first + at * NP + q.n, R, e);
-    for (int i = p.segs - 1; i > q.seg; --i) {
+    for (int i = p.segs * p.sub - 1; i >= (q.seg + 1) * p.sub; --i) {
       float Q[R];
       const long long m = (long long)i * p.B * p.E + at;
       load_states(p.seg_q + m * NP + q.n, R, Q);
@@ -91,7 +115,8 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
     }
   }
   const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
-  const int begin = q.seg * p.seg_steps, stop = min(begin + p.seg_steps, p.T), end = min(stop, q.len);
+  const int steps = LOCAL ? p.seg_steps / p.sub : p.seg_steps;
+  const int begin = min(q.seg * steps, p.T), stop = min(begin + steps, p.T), end = min(stop, q.len);
   int t0 = begin + (end - begin + G - 1) / G * G - G;      // the last chunk with steps, if there is one
   SsmRows xu = ssm_rows<BF, Q>(p, q, p.u, p.ldu, t0), xd = ssm_rows<BF, Q>(p, q, p.delta, p.lddelta, t0),
           xz = ssm_rows<BF, Q>(p, q, p.z, p.ldz, t0), xdy = ssm_rows<BF, Q>(p, q, p.dy, p.lddy, t0);
@@ -127,30 +152,41 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
   // those then has no young stores to wait for.  The waves' sums of dB and dC
   // are added there, too; the other half of `sums` is written meanwhile.
   float rows[3][I] = {};
+  // the thread's place in the partial sums: value x of a step, of the chunk's step x / (2 NP)
+  const long long step = (long long)p.B * p.G * 2 * NP;
+  float* part = out.bc + (((long long)q.group * p.T + t0 + (int)threadIdx.x / (2 * NP)) * p.B + q.b) * p.G * 2 * NP + q.g * 2 * NP + threadIdx.x % (2 * NP);
   auto flush = [&](int t0) {
     if (p.du) store_own<BF, Q, true, I>(ydu, q, stop - t0, rows[0]);
     if (p.ddelta) store_own<BF, Q, true, I>(ydd, q, stop - t0, rows[1]);
     if (p.dz) store_own<BF, Q, true, I>(ydz, q, stop - t0, rows[2]);
     if (!p.dBm && !p.dCm) return;
     __syncthreads();
+    if (out.groups > 1) {
+#pragma unroll
+      for (int i = 0; i < (G * 2 * NP + 64 * W - 1) / (64 * W); ++i) {
+        const int x = threadIdx.x + i * 64 * W, s = x / (2 * NP);
+        if (G * 2 * NP % (64 * W) && x >= G * 2 * NP) break;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v += (&sums[LOCAL ? 0 : t0 / G & 1][w][0][0][0])[x];
+        if (t0 + s < end) part[i * (64 * W / (2 * NP)) * step] = v;
+      }
+      part -= G * step;
+      return;
+    }
     for (int x = threadIdx.x; x < G * 2 * NP; x += 64 * W) {
       const int s = x / (2 * NP), c = x / NP % 2, n = x % NP, t = t0 + s;
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) v += sums[LOCAL ? 0 : t0 / G & 1][w][s][c][n];
-      const long long row = (long long)t * p.B + q.b;
-      if (t >= end) continue;
-      if (out.groups > 1) {
-        out.bc[((((long long)q.group * p.T * p.B + row) * p.G + q.g) * 2 + c) * NP + n] = v;
-      } else if (n < p.N && (c ? p.dCm : p.dBm)) {
-        el_store<BF>((El<BF>*)(c ? p.dCm : p.dBm) + row * (c ? p.lddC : p.lddB) + q.g * p.N + n, v);
-      }
+      if (t < end && n < p.N && (c ? p.dCm : p.dBm))
+        el_store<BF>((El<BF>*)(c ? p.dCm : p.dBm) + ((long long)t * p.B + q.b) * (c ? p.lddC : p.lddB) + q.g * p.N + n, v);
     }
   };
   const int top = t0;
   if (begin < end)
     for (; t0 >= begin; t0 -= G) {
-      float u[I], d[I], du[I], z[I], dy[I], go[I], slope[I], h[R];
+      float u[I], d[I], du[I], go[I], gz[I], slope[I], h[R];
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         d[i] = el_load<BF>(&rd[i]) + bias;
@@ -167,25 +203,25 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
       for (int i = 0; i < I; ++i) {
         const bool on = t0 + i * Q + q.j < end && q.live;
         u[i] = on ? el_load<BF>(&ru[i]) : 0.f;
-        z[i] = on ? el_load<BF>(&rz[i]) : 0.f;
-        dy[i] = on ? el_load<BF>(&rdy[i]) : 0.f;
+        go[i] = on ? el_load<BF>(&rdy[i]) : 0.f;
         d[i] = on ? d[i] : 0.f;
         slope[i] = on ? slope[i] : 0.f;
         du[i] = d[i] * u[i];
-        go[i] = dy[i];
+        gz[i] = 0.f;
         total += d[i];
       }
       if (p.z)
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-          float g, unused;
-          act_pair<ACT_SILU>(z[i], g, unused);
+        for (int i = 0; i < I; ++i) {      // go: of what the gate multiplied, gz: dy times the gate's slope
+          const bool on = t0 + i * Q + q.j < end && q.live;
+          float g, dg;
+          act_pair<ACT_SILU>(on ? el_load<BF>(&rz[i]) : 0.f, g, dg);
+          gz[i] = go[i] * dg;
           go[i] *= g;
         }
 #pragma unroll
       for (int r = 0; r < R; ++r) h[r] = start[r];
-      float* own = &bc[wave][0][0][0];
-      put_bc<BF, G, NP>(own, rbc);
+      put_bc<BF, G, NP>(&bc[wave][0][0][0], rbc);
       if (!LOCAL && t0 < top) flush(t0 + G);
       if (t0 > begin) load(t0 - G);
       if constexpr (LOCAL) {
@@ -193,7 +229,7 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
         for (int s = G - 1; s >= 0; --s) {
           const float ds = from_lane<Q>(d[s / Q], s % Q), gs = from_lane<Q>(go[s / Q], s % Q);
           float C[R];
-          lds_get(own + s * 2 * NP + NP + q.n, C);
+          lds_get(bcs + s * 2 * NP + NP, C);
 #pragma unroll
           for (int r = 0; r < R; ++r) e[r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e)) * fmaf(C[r], gs, e[r]);
         }
@@ -209,8 +245,8 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
           const int s = i * Q + l;
           const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
           float B[R], C[R];
-          lds_get(own + s * 2 * NP + q.n, B);
-          lds_get(own + s * 2 * NP + NP + q.n, C);
+          lds_get(bcs + s * 2 * NP, B);
+          lds_get(bcs + s * 2 * NP + NP, C);
           part[l] = 0.f;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
@@ -224,7 +260,7 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
       }
       // backwards
       float (*const to)[2][NP] = sums[LOCAL ? 0 : t0 / G & 1][wave];
-      float gB[I], gA[I];
+      float gB[I], gA[I], v[2][2][R];
 #pragma unroll
       for (int i = I - 1; i >= 0; --i) {
         float pB[Q], pA[Q];
@@ -232,37 +268,34 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
         for (int l = Q - 1; l >= 0; --l) {
           const int s = i * Q + l;
           const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l), gs = from_lane<Q>(go[i], l);
-          float B[R], C[R], v[2 * R];
-          lds_get(own + s * 2 * NP + q.n, B);
-          lds_get(own + s * 2 * NP + NP + q.n, C);
+          float B[R], C[R];
+          lds_get(bcs + s * 2 * NP, B);
+          lds_get(bcs + s * 2 * NP + NP, C);
           pB[l] = pA[l] = 0.f;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const float g = fmaf(C[r], gs, e[r]);
-            v[r] = g * dus;
-            v[R + r] = gs * (s == G - 1 ? h[r] : hb[s == G - 1 ? s : s + 1][r]);
+            v[s & 1][0][r] = g * dus;
+            v[s & 1][1][r] = gs * (s == G - 1 ? h[r] : hb[s == G - 1 ? s : s + 1][r]);
             pB[l] = fmaf(g, B[r], pB[l]);
             e[r] = g * a[s][r];
             const float x = e[r] * hb[s][r];
             pA[l] = fmaf(x, A[r], pA[l]);
             dA[r] = fmaf(x, ds, dA[r]);
           }
-          if (!whole)                    // an infinite B or C must not reach the sums through channels that are not there
+          if (s & 1) continue;
+          // two steps' dB and dC: [2][2][R] values
+          constexpr int V = 4 * R;
+          float f[V];
 #pragma unroll
-            for (int x = 0; x < 2 * R; ++x) v[x] = q.live ? v[x] : 0.f;
-          sum_channels<S, 32, 2 * R>(v);
-          // the values that a lane has left: folds of the bits 32, 16, ... chose them
-          constexpr int LEFT = 2 * R > CH ? 2 * R / CH : 1;
-          int first = 0;
-          bool mine = true;
+          for (int x = 0; x < V; ++x) f[x] = v[x / (2 * R)][x / R % 2][x % R];
+          sum_channels<S, 32, V>(f);
+          if (has_sums<S, V>(lane))
 #pragma unroll
-          for (int bit = 32, half = R; bit >= S; bit /= 2, half /= 2) {
-            if (half >= 1) first += lane & bit ? half : 0;
-            else mine = mine && !(lane & bit);
-          }
-          if (mine)
-#pragma unroll
-            for (int x = 0; x < LEFT; ++x) to[s][(first + x) / R][q.n + (first + x) % R] = v[x];
+            for (int x = 0; x < sums_left<S, V>(); ++x) {
+              const int y = first_sum<S, V>(lane) + x;
+              to[s + y / (2 * R)][y / R % 2][q.n + y % R] = f[x];
+            }
         }
         gB[i] = sum_to_lane<S, Q>(pB);
         gA[i] = sum_to_lane<S, Q>(pA);
@@ -275,9 +308,7 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
         dbias += on ? dd : 0.f;
         rows[0][i] = on ? fmaf(D, go[i], d[i] * gB[i]) : 0.f;
         rows[1][i] = on ? dd : 0.f;
-        float g, dg;
-        act_pair<ACT_SILU>(z[i], g, dg);
-        rows[2][i] = on ? dy[i] * o[i] * dg : 0.f;
+        rows[2][i] = on ? o[i] * gz[i] : 0.f;
       }
     }
   if (!LOCAL && begin < end) flush(begin);
@@ -359,7 +390,7 @@ hipError_t start(const SsmParams& p, hipStream_t s) {
   const unsigned tiles = (unsigned)groups * p.G * p.B;
   const dim3 block(64 * kSsmTiles);
   if (p.B > 0) {
-    if (p.segs > 1) hipLaunchKernelGGL((bwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1)), block, 0, s, p, parts);
+    if (p.segs > 1) hipLaunchKernelGGL((bwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p, parts);
     hipLaunchKernelGGL((bwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p, parts);
   }
   const long long all = (long long)p.T * p.B * p.G * 2 * NP;

@@ -67,12 +67,13 @@ struct SsmParams {
   long long ldy;
   float* hy;
   float* starts;         // the state before every chunk of steps, or null
-  // segments of the time axis and their steps (a whole number of chunks); with
-  // more than one: the state that the first one starts from, the segments' maps
-  int segs, seg_steps;
+  // segments of the time axis, the parts of a segment that the first launch
+  // walks, a segment's steps (whole chunks in each part); with more than one
+  // segment: the state that the first one starts from, the parts' maps
+  int segs, sub, seg_steps;
   float* seg_first;      // [B][E][NP]
-  float* seg_q;          // [segs][B][E][NP]
-  float* seg_d;          // [segs][B][E]
+  float* seg_q;          // [segs * sub][B][E][NP]
+  float* seg_d;          // [segs * sub][B][E]
   const void* dy;        // backward, as what follows
   long long lddy;
   const float* dhy;
@@ -83,7 +84,7 @@ struct SsmParams {
 };
 // A call's segments (forward's or backward's) and the parts of the workspace, in floats
 struct SsmPlan {
-  int segs[2], seg_steps[2];
+  int segs[2], sub[2], seg_steps[2];
   size_t starts, first, q, d, part, all;   // offsets; all: the size
 };
 SsmPlan ssm_plan(int T, int B, int E, int N, int G, bool save);
