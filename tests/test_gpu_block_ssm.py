@@ -148,3 +148,76 @@ def test_no_rows():
     got = ssm_run("softplus", c)
     for k in ("dA", "dD", "ddelta_bias"):
         assert not got[k].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,lengths", [(16, None), (16, [700, 300]), (3, [5, 700]), (40, [700, 0])])
+def test_segments(dtype, N, lengths):
+    """Few channels and many steps: the time axis in segments, rows that end in the first ones."""
+    compare("softplus", ssm_case(700, 2, 20, N, 1, dtype, lengths, seed=3), dtype)
+
+
+@pytest.mark.parametrize("N", [2, 16])
+def test_parts_of_segments(N):
+    """So many channels that backward's segments are cut into parts for the first launch."""
+    compare("softplus", ssm_case(200, 2, 500, N, 500, "f32", [200, 150], seed=4), "f32")
+
+
+def test_segments_in_place():
+    """hy over h0 and dh0 over dhy where the first segment reads what the last one writes, and the other way round."""
+    c = ssm_case(600, 1, 24, 16, 1, "f32", seed=8)
+    want = ssm_run("softplus", c)
+    g = {k: gpu(v) for k, v in c.items()}
+    h, y, ws = g["h0"].clone(), torch.empty_like(g["u"]), room(R.rnn_ssm_workspace_size(600, 1, 24, 16, 1, "full"))
+    R.rnn_ssm_forward("softplus", *(g[k] for k in INPUTS), h, None, y, h, ws, "full")
+    assert torch.equal(h, want["hy"]) and torch.equal(y, want["y"])
+    d = g["dhy"].clone()
+    R.rnn_ssm_backward("softplus", *(g[k] for k in INPUTS), g["h0"], None, g["dy"], d, *[None] * 8, d, ws)
+    assert torch.equal(d, want["dh0"])
+
+
+def test_strong_decay_over_segments():
+    """A state of 1e30 carried through segments whose decay is far below fp32's range."""
+    c = ssm_case(640, 1, 16, 4, 1, "f32", seed=5, mode="linear", gated=False, extras=False)
+    c["A"][:] = torch.tensor([-0.2, -1.0, -1e-3, 0.0])
+    c["delta"][:] = 1.0
+    c["u"] *= 1e-20
+    c["h0"][:] = 1e30
+    c["dhy"][:] = 1e-30
+    compare("linear", c, "f32")
+
+
+def test_growing_states():
+    """Positive A: states that grow by e^40, and one that starts at zero beside them."""
+    c = ssm_case(400, 1, 8, 4, 1, "f32", seed=9, mode="linear", gated=False, extras=False)
+    c["A"][:] = torch.tensor([0.1, 0.05, 0.0, -0.1])
+    c["delta"][:] = 1.0
+    c["h0"][:, ::2] = 0.0
+    c["u"][:, :, ::2] = 0.0
+    compare("linear", c, "f32")
+
+
+def test_infinite_values_stay_in_their_row():
+    """An infinite input or a NaN state touches its own row and channel only."""
+    c = ssm_case(70, 3, 20, 16, 1, "f32", seed=10)
+    want = ssm_run("softplus", c)
+    c["u"][30, 1, 4] = float("inf")
+    c["h0"][2, 7, 3] = float("nan")
+    got = ssm_run("softplus", c)
+    assert torch.equal(got["y"][:, 0], want["y"][:, 0]) and torch.equal(got["hy"][0], want["hy"][0])
+    assert torch.equal(got["y"][:30, 1], want["y"][:30, 1]) and not got["y"][31:, 1, 4].isfinite().any()
+    others = [e for e in range(20) if e != 7]
+    assert torch.equal(got["y"][:, 2][:, others], want["y"][:, 2][:, others]) and got["hy"][2, 7].isnan()[3]
+    for k in ("du", "ddelta", "dz"):
+        assert torch.equal(got[k][:, 0], want[k][:, 0])
+
+
+def test_infinite_coefficient_reaches_only_its_own_sums():
+    """A tile with lanes to spare: an infinite C must not make the sums over channels NaN through them."""
+    c = ssm_case(20, 1, 5, 16, 1, "f32", seed=11, gated=False)
+    c["Cm"][7, 0, 3] = float("inf")
+    c["dy"][7] = c["dy"][7].abs() + 0.1
+    c["u"] = c["u"].abs() + 0.1
+    got = ssm_run("softplus", c)
+    assert (got["dBm"][:8, 0, 3] == float("inf")).all() and got["dBm"][8:, 0, 3].isfinite().all()
+    assert got["dBm"][:, 0, [n for n in range(16) if n != 3]].isfinite().all() and got["dCm"].isfinite().all()
