@@ -9,6 +9,8 @@
 // K of them, and sums the weights' gradients over its own steps; pieces' sums
 // are added in a second launch, in a fixed order.
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 #include "ssm_common.h"
 
@@ -16,7 +18,11 @@ using namespace rnnk;
 
 namespace {
 
-constexpr int kAhead = 8;     // steps whose loads are asked for at once
+// Steps whose loads are asked for at once, forward and backward.  Where all of
+// them and the channels of all lanes are there (most of a long piece) they are
+// walked without a branch, so that a wait for the next steps' loads counts past
+// the stores between.
+constexpr int kAhead = 8, kBackAhead = 4;
 
 constexpr int kWidth = 4;     // channels of a lane
 
@@ -29,6 +35,7 @@ __device__ __forceinline__ float silu(float v) {
 
 struct Place {
   int c, left;               // first channel, channels from there on
+  bool whole;                // every lane has all of its channels
   int b, len;
   int t0, t1;                // steps of the piece
 };
@@ -40,12 +47,15 @@ __device__ __forceinline__ Place place(const ConvParams& p) {
   const int tile = i % tiles;
   i /= tiles;
   r.b = i % p.B;
-  const int piece = i / p.B * kConvWaves + (int)(threadIdx.x >> 6);
+  const int piece = i / p.B * kConvWaves + (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // uniform, as what follows from it
   r.c = (tile * 64 + (int)(threadIdx.x & 63)) * VW;
   r.left = p.C - r.c;
-  r.t0 = piece * p.piece;
-  r.t1 = min(r.t0 + p.piece, p.T);
-  if (piece >= p.pieces) r.t0 = r.t1 = -1;
+  r.whole = (tile + 1) * 64 * VW <= p.C;
+  r.t0 = r.t1 = -1;
+  if (piece < p.pieces) {
+    r.t0 = piece * p.piece;
+    r.t1 = min(r.t0 + p.piece, p.T);
+  }
   r.len = p.lengths ? min(max(p.lengths[r.b], 0), p.T) : p.T;
   return r;
 }
@@ -67,9 +77,10 @@ __device__ __forceinline__ void load_weights(const ConvParams& p, const Place& a
 // input of step t >= -(K - 1); steps past the row's length are not used
 template <bool BF, int K, int VW>
 __device__ __forceinline__ RawPiece<BF, VW> input(const ConvParams& p, const Place& at, int t) {
+  if (t >= at.len || (t < 0 && !p.s0)) return {};
   const El<BF>* from = t >= 0 ? (const El<BF>*)p.x + ((long long)t * p.B + at.b) * p.ldx + at.c
                               : (const El<BF>*)p.s0 + ((long long)(t + K - 1) * p.B + at.b) * p.C + at.c;
-  return load_raw<BF, VW>(from, (t >= 0 ? t < at.len : p.s0 != nullptr) ? at.left : 0);
+  return load_raw<BF, VW>(from, at.left);
 }
 template <bool BF, int K, int VW>
 __device__ __forceinline__ void input(const ConvParams& p, const Place& at, int t, float (&v)[VW]) {
@@ -88,7 +99,7 @@ __device__ __forceinline__ void last_inputs(const ConvParams& p, const Place& at
   }
 }
 
-template <bool BF, int K>
+template <bool BF, int K, bool SILU>
 __global__ __launch_bounds__(64 * kConvWaves) void fwd_kernel(const ConvParams p) {
   constexpr int VW = kWidth;
   const Place at = place<VW>(p);
@@ -98,18 +109,20 @@ __global__ __launch_bounds__(64 * kConvWaves) void fwd_kernel(const ConvParams p
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) input<BF, K, VW>(p, at, at.t0 - (K - 1) + k, x[k + 1]);
   RawPiece<BF, VW> raw[kAhead], next[kAhead];
-  auto load = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) next[i] = input<BF, K, VW>(p, at, min(t + i, at.t1 - 1));
-  };
-  if (at.t0 < at.t1) load(at.t0);
-  for (int t = at.t0; t < at.t1; t += kAhead) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
-    if (t + kAhead < at.t1) load(t + kAhead);
+  auto load = [&](int t, auto fast) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (t + i >= at.t1) break;
+      if constexpr (decltype(fast)::value)
+        next[i] = *reinterpret_cast<const RawPiece<BF, VW>*>((const El<BF>*)p.x + ((long long)(t + i) * p.B + at.b) * p.ldx + at.c);
+      else
+        next[i] = input<BF, K, VW>(p, at, min(t + i, at.t1 - 1));
+    }
+  };
+  auto walk = [&](int t, auto fast) {
+    constexpr bool FAST = decltype(fast)::value;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!FAST && t + i >= at.t1) break;
       float v[VW], in[VW];
       unpack<BF, VW>(raw[i], in);
 #pragma unroll
@@ -120,17 +133,35 @@ __global__ __launch_bounds__(64 * kConvWaves) void fwd_kernel(const ConvParams p
         v[j] = bias[j];
 #pragma unroll
         for (int k = 0; k < K; ++k) v[j] = fmaf(w[k][j], x[k][j], v[j]);
-        if (p.silu) v[j] = silu(v[j]);
-        if (t + i >= at.len) v[j] = 0.f;
+        if (SILU) v[j] = silu(v[j]);
+        if (!FAST && t + i >= at.len) v[j] = 0.f;
       }
-      store_piece<BF, VW>((El<BF>*)p.y + ((long long)(t + i) * p.B + at.b) * p.ldy + at.c, at.left, v);
+      store_piece<BF, VW>((El<BF>*)p.y + ((long long)(t + i) * p.B + at.b) * p.ldy + at.c, FAST ? VW : at.left, v);
     }
+  };
+  // whole groups of steps of the piece and the row
+  const int fast = at.whole ? max(0, min(at.t1, at.len) - at.t0) / kAhead * kAhead : 0;
+  int t = at.t0;
+  if (fast) {
+    load(t, std::true_type{});
+    for (; t < at.t0 + fast; t += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
+      load(min(t + kAhead, at.t0 + fast - kAhead), std::true_type{});   // the last time: the same once more
+      walk(t, std::true_type{});
+    }
+  }
+  for (; t < at.t1; t += kAhead) {
+    load(t, std::false_type{});
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
+    walk(t, std::false_type{});
   }
   // s0 is read by the first piece alone, so sy may take its place
   if (p.sy && at.t0 == 0) last_inputs<BF, K, VW>(p, at);
 }
 
-template <bool BF, int K>
+template <bool BF, int K, bool SILU>
 __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p) {
   constexpr int VW = kWidth;
   const Place at = place<VW>(p);
@@ -154,25 +185,45 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
     for (int k = 0; k < K - 1; ++k) input<BF, K, VW>(p, at, at.t0 - (K - 1) + k, x[k + 1]);
     // after step t the gradient of input t - K + 1 is whole
     const int end = at.t1 + K - 1;
-    for (int t = at.t0; t < end; t += kAhead) {
-      RawPiece<BF, VW> rx[kAhead], rdy[kAhead];
+    RawPiece<BF, VW> rx[kBackAhead], rdy[kBackAhead], nx[kBackAhead], ndy[kBackAhead];
+    auto load = [&](int t, auto fast) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int s = min(t + i, end - 1);
-        const int left = s < at.len ? at.left : 0;
-        rx[i] = load_raw<BF, VW>((const El<BF>*)p.x + ((long long)s * p.B + at.b) * p.ldx + at.c, left);
-        rdy[i] = load_raw<BF, VW>((const El<BF>*)p.dy + ((long long)s * p.B + at.b) * p.lddy + at.c, left);
+      for (int i = 0; i < kBackAhead; ++i) {
+        constexpr bool FAST = decltype(fast)::value;
+        const int s = FAST ? t + i : min(t + i, end - 1);
+        const El<BF>* x = (const El<BF>*)p.x + ((long long)s * p.B + at.b) * p.ldx + at.c;
+        const El<BF>* dy = (const El<BF>*)p.dy + ((long long)s * p.B + at.b) * p.lddy + at.c;
+        if constexpr (FAST) {
+          nx[i] = *reinterpret_cast<const RawPiece<BF, VW>*>(x);
+          ndy[i] = *reinterpret_cast<const RawPiece<BF, VW>*>(dy);
+        } else {
+          nx[i] = ndy[i] = {};
+          if (s < at.len) {
+            nx[i] = load_raw<BF, VW>(x, at.left);
+            ndy[i] = load_raw<BF, VW>(dy, at.left);
+          }
+        }
       }
+    };
+    auto turn = [&] {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= end) break;
+      for (int i = 0; i < kBackAhead; ++i) {
+        rx[i] = nx[i];
+        rdy[i] = ndy[i];
+      }
+    };
+    auto walk = [&](int t, auto fast) {
+      constexpr bool FAST = decltype(fast)::value;
+#pragma unroll
+      for (int i = 0; i < kBackAhead; ++i) {
+        if (!FAST && t + i >= end) break;
         const int s = t + i - (K - 1);      // the input whose gradient is whole
-        const bool mine = t + i < at.t1;
+        const bool mine = FAST || t + i < at.t1;
         float dx[VW], more[VW], in[VW], dy[VW];
         unpack<BF, VW>(rx[i], in);
         unpack<BF, VW>(rdy[i], dy);
         const int j0 = s - at.len + K - 1;
-        const bool last = p.dsy && j0 >= 0 && j0 < K - 1 && (s >= at.t0 || at.t0 == 0);
+        const bool last = !FAST && p.dsy && j0 >= 0 && j0 < K - 1 && (s >= at.t0 || at.t0 == 0);
         if (last) load_piece<BF, VW>((const El<BF>*)p.dsy + ((long long)j0 * p.B + at.b) * p.C + at.c, at.left, more);
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
@@ -180,12 +231,12 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
           for (int k = 0; k < K - 1; ++k) x[k][j] = x[k + 1][j];
           x[K - 1][j] = in[j];
           float d = dy[j];
-          if (p.silu) {
+          if (SILU) {
             float v = bias[j], a, da;
 #pragma unroll
             for (int k = 0; k < K; ++k) v = fmaf(w[k][j], x[k][j], v);
             act_pair<ACT_SILU>(v, a, da);
-            d = t + i < at.len ? d * da : 0.f;
+            d = FAST || t + i < at.len ? d * da : 0.f;
           }
 #pragma unroll
           for (int k = K - 1; k > 0; --k) dv[k][j] = dv[k - 1][j];
@@ -199,12 +250,31 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
 #pragma unroll
           for (int k = 0; k < K; ++k) dx[j] = fmaf(w[k][j], dv[k][j], dx[j]);
         }
-        if (s >= at.t0) {
-          if (p.dx) store_piece<BF, VW>((El<BF>*)p.dx + ((long long)s * p.B + at.b) * p.lddx + at.c, at.left, dx);
+        if (FAST || s >= at.t0) {
+          if (FAST || p.dx) store_piece<BF, VW>((El<BF>*)p.dx + ((long long)s * p.B + at.b) * p.lddx + at.c, FAST ? VW : at.left, dx);
         } else if (at.t0 == 0 && p.ds0) {
           store_piece<BF, VW>((El<BF>*)p.ds0 + ((long long)(s + K - 1) * p.B + at.b) * p.C + at.c, at.left, dx);
         }
       }
+    };
+    // the first steps complete inputs before the piece, the last ones are past it
+    // or the row; between them whole groups
+    constexpr int HEAD = (K - 1 + kBackAhead - 1) / kBackAhead * kBackAhead;
+    int t = at.t0;
+    const int fast = at.whole && p.dx ? max(0, min(at.t1, at.len) - t - HEAD) / kBackAhead * kBackAhead : 0;
+    const int to = fast ? t + HEAD + fast : 0;
+    for (; t < end; t += kBackAhead) {
+      if (t + fast == to && fast) {          // HEAD steps are done
+        load(t, std::true_type{});
+        for (; t < to; t += kBackAhead) {
+          turn();
+          load(min(t + kBackAhead, to - kBackAhead), std::true_type{});   // the last time: the same once more
+          walk(t, std::true_type{});
+        }
+      }
+      load(t, std::false_type{});
+      turn();
+      walk(t, std::false_type{});
     }
   }
   if (!p.part) return;
@@ -268,8 +338,10 @@ void start(const ConvParams& p, Pass what, hipStream_t s) {
   }
   const long long width = 64 * kWidth, tiles = (p.C + width - 1) / width;
   const dim3 grid((unsigned)(tiles * p.B * ((p.pieces + kConvWaves - 1) / kConvWaves))), block(64 * kConvWaves);
-  if (what == FWD) hipLaunchKernelGGL((fwd_kernel<BF, K>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((bwd_kernel<BF, K>), grid, block, 0, s, p);
+  if (what == FWD && p.silu) hipLaunchKernelGGL((fwd_kernel<BF, K, true>), grid, block, 0, s, p);
+  else if (what == FWD) hipLaunchKernelGGL((fwd_kernel<BF, K, false>), grid, block, 0, s, p);
+  else if (p.silu) hipLaunchKernelGGL((bwd_kernel<BF, K, true>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((bwd_kernel<BF, K, false>), grid, block, 0, s, p);
 }
 
 template <bool BF>
@@ -295,12 +367,11 @@ hipError_t launch(const ConvParams& p, Pass what, int bf16, hipStream_t s) {
 
 }  // namespace
 
-// steps of a wave's piece (at least K - 1 of them)
-int rnnk::conv_piece(int T, int B, int C, bool) {
-  const long long waves = (long long)B * ((C + 64 * kWidth - 1) / (64 * kWidth));
-  int piece = 32;
-  while (piece > 8 && waves * ((T + piece - 1) / piece) < 2048) piece /= 2;
-  return piece;
+// Steps of a wave's piece (at least K - 1 of them): as many as give each SIMD the
+// waves that its registers hold (4 forward, 3 backward), so that all run at once.
+int rnnk::conv_piece(int T, int B, int C, bool back) {
+  const double steps = (double)B * ((C + 64 * kWidth - 1) / (64 * kWidth)) * T / (back ? 3072 : 4096);
+  return (int)std::min(std::max(1.0, std::ceil(steps / 8)), std::ceil(std::max(T, 1) / 8.0)) * 8;
 }
 
 hipError_t rnn_launch_conv_fwd(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, FWD, bf16, s); }

@@ -28,6 +28,13 @@ def test_sequences(act, dtype, T, B, C, K):
     compare(act, conv_case(T, B, C, K, dtype), dtype)
 
 
+@pytest.mark.parametrize("dtype,K,act", [("f32", 3, "none"), ("bf16", 2, "silu")])
+def test_long_pieces(dtype, K, act):
+    """So many rows that a wave walks pieces of more than 8 steps; rows that end inside, at and before their ends."""
+    lengths = [300, 0, 1, 16, 17, 8, 24, 299] + [300 - i for i in range(84)]
+    compare(act, conv_case(300, 92, 257, K, dtype, lengths), dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,K,lengths", [(40, 4, [40, 0, 1, 2, 3, 17]), (9, 8, [9, 8, 7, 1, 0, 3]), (70, 3, [-5, 99, 64, 32, 33, 31])])
 def test_ragged_rows(dtype, T, K, lengths):
