@@ -527,7 +527,8 @@ rnn_status_t rnn_norm_backward(void* stream, rnn_norm_t kind, rnn_wtype_t wtype,
  * NULL: zeros): the inputs before the first step, the last of them x_(-1).
  * sy as s0, or NULL: the inputs before the step that follows the row's last;
  * it may be s0 itself.  `lengths` as for the scan.  act: RNN_ACT_NONE or
- * RNN_ACT_SILU.  UNSUPPORTED: B * C >= 2^30 or T >= 2^30. */
+ * RNN_ACT_SILU.  UNSUPPORTED: B * C >= 2^30, T >= 2^30, or 2^24 workgroups (of
+ * 256 channels of a row, and some steps). */
 #define RNN_ACT_NONE ((rnn_act_t)3)
 
 rnn_status_t rnn_conv_forward(void* stream, rnn_act_t act, rnn_wtype_t wtype, int T, int B, int C, int K,
@@ -555,9 +556,11 @@ rnn_status_t rnn_conv_backward(void* stream, rnn_act_t act, rnn_wtype_t wtype, i
  * neighbouring channels of a group; A [E, N]; D, delta_bias [E].  D, z and
  * delta_bias may be NULL (the term or factor is left out).  States h0, hy
  * [B, E, N]; h0 NULL: zeros, hy NULL: not wanted; hy may be h0 itself.
- * INVALID_ARG where groups < 1 or does not divide E; UNSUPPORTED: N > 64,
- * B * E >= 2^24, T >= 2^30, groups * N >= 2^20 or B * ld > 2^26.  A state's decay over any
- * number of steps may leave fp32's range; the states themselves may not. */
+ * INVALID_ARG where N or groups < 1 or groups does not divide E; UNSUPPORTED:
+ * N > 64, E >= 2^22, B * E >= 2^30, T >= 2^30, over several steps B * ld >
+ * 2^28, or 2^24 workgroups (of up to 4 * 64 channels of a row and group).  A is
+ * finite.  A state's decay over any number of steps may leave fp32's range;
+ * the states themselves may not. */
 typedef enum RNN_ENUM_BASE { RNN_DELTA_SOFTPLUS = 0, RNN_DELTA_LINEAR = 1 } rnn_delta_t;
 
 typedef struct rnn_ssm_inputs {

@@ -374,6 +374,11 @@ int rnnk::conv_piece(int T, int B, int C, bool back) {
   return (int)std::min(std::max(1.0, std::ceil(steps / 8)), std::ceil(std::max(T, 1) / 8.0)) * 8;
 }
 
+long long rnnk::conv_blocks(int T, int B, int C, bool back) {
+  const long long tiles = (C + 64 * kWidth - 1) / (64 * kWidth), steps = (long long)conv_piece(T, B, C, back) * kConvWaves;
+  return tiles * B * std::max(1LL, (T + steps - 1) / steps);
+}
+
 hipError_t rnn_launch_conv_fwd(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, FWD, bf16, s); }
 hipError_t rnn_launch_conv_step(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, STEP, bf16, s); }
 hipError_t rnn_launch_conv_bwd(const ConvParams& q, int bf16, hipStream_t s) {

@@ -16,6 +16,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Workgroups by rows: a launch has fewer than 2^32 threads in a dimension.
+dim3 row_grid(long long blocks) {
+  const long long x = std::min(blocks, 1LL << 21);
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ long long row_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // sum over L lanes (64: a wave, else the workgroup); `slot` alternates between calls
 template <int L>
 __device__ __forceinline__ float row_sum(float v, float* lds, int& slot) {
@@ -39,8 +46,8 @@ __global__ __launch_bounds__(L < kThreads ? kThreads : L) void fwd_kernel(const 
   __shared__ float lds[2 * (L / 64)];
   int slot = 0;
   const int lane = threadIdx.x % L;
-  const long long row = (long long)blockIdx.x * ROWS + threadIdx.x / L;
-  if (ROWS > 1 && row >= p.M) return;            // (whole waves; no barrier follows)
+  const long long row = row_block() * ROWS + threadIdx.x / L;
+  if (row >= p.M) return;                        // (a whole workgroup, or a wave of those without barriers)
   const long long at = row * p.D;
   const El<BF>* x = (const El<BF>*)p.x + at;
   const El<BF>* r = (const El<BF>*)p.residual + at;
@@ -207,7 +214,8 @@ __global__ __launch_bounds__(1024) void fwd_long_kernel(const NormParams p) {
   constexpr int VW = piece_width<BF>();
   __shared__ float lds[32];
   int slot = 0;
-  const long long at = (long long)blockIdx.x * p.D;
+  const long long row = row_block(), at = row * p.D;
+  if (row >= p.M) return;
   const float inv = 1.f / (float)p.D;
   // the row's values: what an earlier walk has left in `total`, else x (+ residual)
   auto value = [&](int c, bool again, float(&v)[VW]) {
@@ -254,8 +262,8 @@ __global__ __launch_bounds__(1024) void fwd_long_kernel(const NormParams p) {
     store_piece<BF, VW>((El<BF>*)p.y + at + c, p.D - c, v);
   }
   if (p.stats && threadIdx.x == 0) {
-    p.stats[2LL * blockIdx.x] = mean;
-    p.stats[2LL * blockIdx.x + 1] = rstd;
+    p.stats[2 * row] = mean;
+    p.stats[2 * row + 1] = rstd;
   }
 }
 
@@ -264,8 +272,9 @@ __global__ __launch_bounds__(1024) void bwd_long_kernel(const NormParams p) {
   constexpr int VW = piece_width<BF>();
   __shared__ float lds[32];
   int slot = 0;
-  const long long at = (long long)blockIdx.x * p.D;
-  const float inv = 1.f / (float)p.D, mean = p.stats[2LL * blockIdx.x], rstd = p.stats[2LL * blockIdx.x + 1];
+  const long long row = row_block(), at = row * p.D;
+  if (row >= p.M) return;
+  const float inv = 1.f / (float)p.D, mean = p.stats[2 * row], rstd = p.stats[2 * row + 1];
   float x[VW], g[VW], w[VW], s0 = 0.f, s1 = 0.f;
   auto values = [&](int c) {
     const int left = p.D - c;
@@ -350,7 +359,7 @@ void start(const NormParams& p, bool back, int blocks, hipStream_t s) {
   constexpr int threads = L < kThreads ? kThreads : L, rows = threads / L;
   if (back && p.dbias) hipLaunchKernelGGL((bwd_kernel<BF, L, P, true>), dim3(blocks), dim3(back_threads(L)), 0, s, p);
   else if (back) hipLaunchKernelGGL((bwd_kernel<BF, L, P, false>), dim3(blocks), dim3(back_threads(L)), 0, s, p);
-  else hipLaunchKernelGGL((fwd_kernel<BF, L, P>), dim3((unsigned)(((long long)p.M + rows - 1) / rows)), dim3(threads), 0, s, p);
+  else hipLaunchKernelGGL((fwd_kernel<BF, L, P>), row_grid(((long long)p.M + rows - 1) / rows), dim3(threads), 0, s, p);
 }
 
 template <bool BF>
@@ -381,9 +390,9 @@ hipError_t launch(const NormParams& p, bool back, hipStream_t s) {
     const int blocks = back ? back_blocks(p.M, sh.lanes) : 0;
     pick<BF>(p, back, sh, blocks, s);
   } else if (!back) {
-    hipLaunchKernelGGL(fwd_long_kernel<BF>, dim3(p.M), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL(fwd_long_kernel<BF>, row_grid(p.M), dim3(1024), 0, s, p);
   } else {
-    if (p.dx) hipLaunchKernelGGL(bwd_long_kernel<BF>, dim3(p.M), dim3(1024), 0, s, p);
+    if (p.dx) hipLaunchKernelGGL(bwd_long_kernel<BF>, row_grid(p.M), dim3(1024), 0, s, p);
     if (p.part) hipLaunchKernelGGL(columns_kernel<BF>, dim3((p.D + kThreads - 1) / kThreads, (unsigned)p.parts), dim3(kThreads), 0, s, p);
   }
   return hipGetLastError();

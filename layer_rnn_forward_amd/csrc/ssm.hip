@@ -191,7 +191,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
 
 template <bool BF, int S>
 hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
-  const unsigned tiles = (unsigned)ssm_groups(p, S) * p.G * p.B;   // at most B * E
+  const unsigned tiles = (unsigned)ssm_blocks(p.B, p.E, p.N, p.G);
   const dim3 block(64 * kSsmTiles);
   if (step) {
     hipLaunchKernelGGL((step_kernel<BF, S>), dim3(tiles), block, 0, s, p);
@@ -224,6 +224,8 @@ static int segments(long long tiles, int T, int alone, int fill) {
   return (int)std::max(1LL, std::min<long long>(fill / tiles, T / 32));
 }
 
+long long rnnk::ssm_blocks(int B, int E, int N, int G) { return (long long)ssm_groups(E, G, ssm_lanes(N)) * G * B; }
+
 SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
   SsmPlan r{};
   const int S = ssm_lanes(N), CH = 64 / S, step = ssm_chunk(S), NP = S * kSsmPer;
@@ -254,7 +256,7 @@ SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
     r.d = take(segs * C);
   }
   if (save) {
-    const size_t groups = (size_t)(E / G + CH * kSsmTiles - 1) / (CH * kSsmTiles);
+    const size_t groups = ssm_groups(E, G, S);
     r.part = take((groups > 1 ? groups * T * B * G * 2 * NP : 0) + r.segs[1] * C * (NP + 2));
   }
   r.all = o;

@@ -45,9 +45,8 @@ size_t norm_bytes(int M, int D) { return std::max(kAlign, align_up((size_t)norm_
 rnn_status_t conv_sizes(int T, int B, int C, int K) {
   if (T < 0 || B < 0 || C < 0 || K < 1) return RNN_STATUS_INVALID_ARG;
   if (K > kConvMost || (long long)B * C >= (1LL << 30) || T >= (1 << 30)) return RNN_STATUS_UNSUPPORTED;
-  // workgroups of a launch, and rows of partial sums
-  if ((long long)B * (C / 64 + 1) * (T / 32 + 1) >= (1LL << 31)) return RNN_STATUS_UNSUPPORTED;
-  return RNN_STATUS_SUCCESS;
+  // threads of a launch, 256 a workgroup
+  return std::max(conv_blocks(T, B, C, false), conv_blocks(T, B, C, true)) >= (1 << 24) ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
 }
 bool conv_ok(int act, int wtype) { return (act == RNN_ACT_NONE || act == RNN_ACT_SILU) && wtype_ok(wtype); }
 
@@ -67,9 +66,9 @@ size_t conv_bytes(int T, int B, int C, int K) {
 // -------------------------------------------------------------------- ssm
 rnn_status_t ssm_sizes(int T, int B, int E, int N, int groups) {
   if (T < 0 || B < 0 || E < 0 || N < 1 || groups < 1 || E % groups) return RNN_STATUS_INVALID_ARG;
-  if (N > kSsmStates || (long long)B * E >= (1 << 24) || T >= (1 << 30) || (long long)groups * N >= (1 << 20)) return RNN_STATUS_UNSUPPORTED;
-  // the launch over dB and dC, and its partial sums
-  return (double)T * B * groups * N >= 0x1p37 ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
+  if (N > kSsmStates || E >= (1 << 22) || (long long)B * E >= (1LL << 30) || T >= (1 << 30)) return RNN_STATUS_UNSUPPORTED;
+  // threads of a launch, 256 a workgroup
+  return ssm_blocks(B, E, N, groups) >= (1 << 24) ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
 }
 bool ssm_ok(int mode, int wtype) { return (mode == RNN_DELTA_SOFTPLUS || mode == RNN_DELTA_LINEAR) && wtype_ok(wtype); }
 
@@ -88,11 +87,11 @@ void ssm_room(SsmParams& p, const SsmPlan& q, bool back, void* ws) {
   p.part = f + q.part;
 }
 
-// rows `ld` elements apart; a step's lie within 32 bits of each other
-rnn_status_t ssm_rows(int B, const void* x, long long ld, long long width) {
+// rows `ld` elements apart; over several steps, four of them lie within 32 bits of each other
+rnn_status_t ssm_rows(int T, int B, const void* x, long long ld, long long width) {
   if (!x) return RNN_STATUS_SUCCESS;
   if (ld < width) return RNN_STATUS_INVALID_ARG;
-  return ld > (1 << 26) / std::max(B, 1) ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
+  return T > 1 && ld > (1 << 28) / std::max(B, 1) ? RNN_STATUS_UNSUPPORTED : RNN_STATUS_SUCCESS;
 }
 
 // the inputs' checks; they are needed where there are steps
@@ -100,11 +99,11 @@ rnn_status_t ssm_inputs(SsmParams& p, const rnn_ssm_inputs_t* in, int mode, int 
   if (!in || !in->A) return RNN_STATUS_INVALID_ARG;
   if (T > 0 && (!in->u || !in->delta || !in->Bm || !in->Cm)) return RNN_STATUS_INVALID_ARG;
   const long long GN = (long long)groups * N;
-  LM_TRY(ssm_rows(B, in->u, in->ldu, E));
-  LM_TRY(ssm_rows(B, in->delta, in->lddelta, E));
-  LM_TRY(ssm_rows(B, in->z, in->ldz, E));
-  LM_TRY(ssm_rows(B, in->Bm, in->ldB, GN));
-  LM_TRY(ssm_rows(B, in->Cm, in->ldC, GN));
+  LM_TRY(ssm_rows(T, B, in->u, in->ldu, E));
+  LM_TRY(ssm_rows(T, B, in->delta, in->lddelta, E));
+  LM_TRY(ssm_rows(T, B, in->z, in->ldz, E));
+  LM_TRY(ssm_rows(T, B, in->Bm, in->ldB, GN));
+  LM_TRY(ssm_rows(T, B, in->Cm, in->ldC, GN));
   p.T = T; p.B = B; p.E = E; p.N = N; p.G = groups;
   p.softplus = mode == RNN_DELTA_SOFTPLUS;
   p.u = in->u; p.delta = in->delta; p.z = in->z; p.Bm = in->Bm; p.Cm = in->Cm;
@@ -215,7 +214,7 @@ rnn_status_t rnn_ssm_step(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, int
   SsmParams p{};
   LM_TRY(ssm_inputs(p, in, mode, 1, B, E, N, groups));
   if (!y) return RNN_STATUS_INVALID_ARG;
-  LM_TRY(ssm_rows(B, y, ldy, E));
+  LM_TRY(ssm_rows(1, B, y, ldy, E));
   p.h0 = h; p.y = y; p.ldy = ldy; p.hy = hy;
   return dev(rnn_launch_ssm_step(p, wtype == RNN_W_BF16, hs(stream)));
 }
@@ -238,7 +237,7 @@ rnn_status_t rnn_ssm_forward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype, 
   SsmParams p{};
   LM_TRY(ssm_inputs(p, in, mode, T, B, E, N, groups));
   if (T > 0 && !y) return RNN_STATUS_INVALID_ARG;
-  LM_TRY(ssm_rows(B, y, ldy, E));
+  LM_TRY(ssm_rows(T, B, y, ldy, E));
   p.h0 = h0; p.lengths = lengths; p.y = y; p.ldy = ldy; p.hy = hy;
   ssm_room(p, plan, false, ws);
   if (save == RNN_SAVE_NONE) p.starts = nullptr;
@@ -259,12 +258,12 @@ rnn_status_t rnn_ssm_backward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype,
   const long long GN = (long long)groups * N;
   const rnn_ssm_grads_t& g = *grads;
   if ((B > 0 && T > 0 && !dy) || (g.dz && !in->z)) return RNN_STATUS_INVALID_ARG;
-  LM_TRY(ssm_rows(B, dy, lddy, E));
-  LM_TRY(ssm_rows(B, g.du, g.lddu, E));
-  LM_TRY(ssm_rows(B, g.ddelta, g.ldddelta, E));
-  LM_TRY(ssm_rows(B, g.dz, g.lddz, E));
-  LM_TRY(ssm_rows(B, g.dBm, g.lddB, GN));
-  LM_TRY(ssm_rows(B, g.dCm, g.lddC, GN));
+  LM_TRY(ssm_rows(T, B, dy, lddy, E));
+  LM_TRY(ssm_rows(T, B, g.du, g.lddu, E));
+  LM_TRY(ssm_rows(T, B, g.ddelta, g.ldddelta, E));
+  LM_TRY(ssm_rows(T, B, g.dz, g.lddz, E));
+  LM_TRY(ssm_rows(T, B, g.dBm, g.lddB, GN));
+  LM_TRY(ssm_rows(T, B, g.dCm, g.lddC, GN));
   p.lengths = lengths; p.dy = dy; p.lddy = lddy; p.dhy = dhy;
   p.du = g.du; p.ddelta = g.ddelta; p.dz = g.dz; p.dBm = g.dBm; p.dCm = g.dCm;
   p.lddu = g.lddu; p.ldddelta = g.ldddelta; p.lddz = g.lddz; p.lddB = g.lddB; p.lddC = g.lddC;

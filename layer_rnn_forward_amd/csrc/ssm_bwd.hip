@@ -342,18 +342,18 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
 // dB and dC: the workgroups' sums
 template <bool BF>
 __global__ __launch_bounds__(256) void channels_kernel(const SsmParams p, const Parts in, int NP) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, all = (long long)p.T * p.B * p.G * 2 * NP;
-  if (i >= all) return;
-  const int n = (int)(i % NP), c = (int)(i / NP % 2), g = (int)(i / (2 * NP) % p.G);
-  const long long row = i / (2LL * NP * p.G);
-  if (n >= p.N) return;
-  const int b = (int)(row % p.B), len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-  void* to = c ? p.dCm : p.dBm;
-  if (!to) return;
-  float s = 0.f;
-  if (row / p.B < len)
-    for (int x = 0; x < in.groups; ++x) s += in.bc[x * all + i];
-  el_store<BF>((El<BF>*)to + row * (c ? p.lddC : p.lddB) + g * p.N + n, s);
+  const long long all = (long long)p.T * p.B * p.G * 2 * NP;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const int n = (int)(i % NP), c = (int)(i / NP % 2), g = (int)(i / (2 * NP) % p.G);
+    const long long row = i / (2LL * NP * p.G);
+    void* to = c ? p.dCm : p.dBm;
+    if (n >= p.N || !to) continue;
+    const int b = (int)(row % p.B), len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+    float s = 0.f;
+    if (row / p.B < len)
+      for (int x = 0; x < in.groups; ++x) s += in.bc[x * all + i];
+    el_store<BF>((El<BF>*)to + row * (c ? p.lddC : p.lddB) + g * p.N + n, s);
+  }
 }
 
 // dA, dD, ddelta_bias: the sums over rows and segments; 64 values a workgroup, every fourth row a wave
@@ -395,7 +395,7 @@ hipError_t start(const SsmParams& p, hipStream_t s) {
   }
   const long long all = (long long)p.T * p.B * p.G * 2 * NP;
   if ((p.dBm || p.dCm) && all && groups > 1)
-    hipLaunchKernelGGL(channels_kernel<BF>, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, p, parts, NP);
+    hipLaunchKernelGGL(channels_kernel<BF>, dim3((unsigned)std::min<long long>((all + 255) / 256, 1 << 20)), dim3(256), 0, s, p, parts, NP);
   if (p.dA || p.dD || p.ddelta_bias)
     hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(((long long)p.E * (NP + 2) + 63) / 64)), dim3(256), 0, s, p, parts, NP);
   return hipGetLastError();

@@ -55,6 +55,7 @@ struct ConvParams {
 };
 constexpr int kConvWaves = 4;   // consecutive pieces of a workgroup
 int conv_piece(int T, int B, int C, bool back);
+long long conv_blocks(int T, int B, int C, bool back);   // workgroups of a launch
 
 constexpr int kSsmStates = 64;  // most states of a channel
 struct SsmParams {
@@ -87,6 +88,7 @@ struct SsmPlan {
   int segs[2], sub[2], seg_steps[2];
   size_t starts, first, q, d, part, all;   // offsets; all: the size
 };
+long long ssm_blocks(int B, int E, int N, int G);   // workgroups of a segment
 SsmPlan ssm_plan(int T, int B, int E, int N, int G, bool save);
 
 // 16 bytes of a row at any alignment

@@ -104,10 +104,11 @@ struct SsmPlace {
   int len;               // the row's steps
 };
 // workgroups of a group's tiles
-__host__ __device__ inline int ssm_groups(const SsmParams& p, int S) {
+__host__ __device__ inline int ssm_groups(int E, int G, int S) {
   const int channels = 64 / S * kSsmTiles;
-  return (p.E / p.G + channels - 1) / channels;
+  return (E / G + channels - 1) / channels;
 }
+__host__ __device__ inline int ssm_groups(const SsmParams& p, int S) { return ssm_groups(p.E, p.G, S); }
 template <int S>
 __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, unsigned at, int wave) {
   constexpr int CH = 64 / S, Q = S < 4 ? S : 4;
@@ -130,7 +131,8 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, unsigned at, i
 }
 
 // The rows of a time-major tensor as a wave walks them, chunk after chunk: a
-// uniform address and the lane's part of it in 32 bits (B * ld <= 2^26).
+// uniform address and the lane's part of it, of up to three steps and a row, in
+// 32 bits (B * ld <= 2^28).
 // (Pointers say that they are to global memory: the compiler does not look
 // through the asm statements below for it.)
 using GlobalBytes = __attribute__((address_space(1))) char*;

@@ -48,7 +48,7 @@ def test_conv(lib):
     n = ctypes.c_size_t()
     for args, want in (((4, 2, 8, 4), 0), ((0, 0, 0, 1), 0), ((-1, 2, 8, 4), INVALID), ((4, -2, 8, 4), INVALID), ((4, 2, -8, 4), INVALID),
                        ((4, 2, 8, 0), INVALID), ((4, 2, 8, 9), UNSUPPORTED), ((4, 1 << 15, 1 << 15, 4), UNSUPPORTED),
-                       ((1 << 30, 1, 1, 4), UNSUPPORTED), ((1 << 29, 1 << 10, 1, 4), UNSUPPORTED)):
+                       ((1 << 30, 1, 1, 4), UNSUPPORTED), ((1, 1 << 24, 1, 4), UNSUPPORTED), ((1 << 29, 1 << 10, 1, 4), 0)):
         assert lib.rnn_conv_workspace_size(*args, ctypes.byref(n)) == want, args
     assert lib.rnn_conv_workspace_size(4, 2, 8, 4, None) == INVALID
 
@@ -86,8 +86,8 @@ def test_ssm(lib):
     for args, want in (((4, 2, 8, 4, 1, 0), 0), ((4, 2, 8, 4, 2, 1), 0), ((0, 0, 0, 1, 1, 1), 0), ((-1, 2, 8, 4, 1, 0), INVALID),
                        ((4, -2, 8, 4, 1, 0), INVALID), ((4, 2, -8, 4, 1, 0), INVALID), ((4, 2, 8, 0, 1, 0), INVALID), ((4, 2, 8, 4, 0, 0), INVALID),
                        ((4, 2, 8, 4, 3, 0), INVALID), ((4, 2, 8, 4, 1, 2), INVALID), ((4, 2, 8, 4, 1, -1), INVALID), ((4, 2, 8, 65, 1, 0), UNSUPPORTED),
-                       ((4, 1 << 12, 1 << 12, 4, 1, 0), UNSUPPORTED), ((1 << 30, 1, 8, 4, 1, 0), UNSUPPORTED),
-                       ((1 << 29, 1 << 10, 8, 4, 1, 0), UNSUPPORTED)):
+                       ((4, 1 << 15, 1 << 15, 4, 1, 0), UNSUPPORTED), ((1 << 30, 1, 8, 4, 1, 0), UNSUPPORTED), ((4, 1, 1 << 22, 4, 1, 0), UNSUPPORTED),
+                       ((1, 1 << 24, 8, 4, 1, 0), UNSUPPORTED), ((1, 1 << 20, 64, 4, 64, 0), UNSUPPORTED), ((4, 1 << 14, 1 << 12, 16, 1, 1), 0)):
         assert lib.rnn_ssm_workspace_size(*args, ctypes.byref(n)) == want, args
     assert lib.rnn_ssm_workspace_size(4, 2, 8, 4, 1, 0, None) == INVALID
     # the states before every 8th step, 16 of them a channel
@@ -104,14 +104,15 @@ def test_ssm(lib):
         return lib.rnn_ssm_backward(None, mode, wt, T, B, E, N, G, ins and ctypes.byref(ins), None, dy, lddy, None,
                                     grads and ctypes.byref(grads), ws, n)
 
-    big = 1 << 26
+    big = 1 << 28
+    for call in (fwd, bwd):
+        assert call(ins=inputs(ldu=big)) == UNSUPPORTED and call(ins=inputs(ldC=big)) == UNSUPPORTED      # B * ld > 2^28
     for call in (fwd, step, bwd):
         for bad in (dict(mode=2), dict(mode=-1), dict(wt=2), dict(B=-1), dict(E=-1), dict(N=0), dict(G=3), dict(G=0), dict(ins=None),
                     *[dict(ins=inputs(**{k: None})) for k in ("u", "delta", "Bm", "Cm", "A")],
                     *[dict(ins=inputs(**{k: v})) for k, v in (("ldu", 7), ("lddelta", 0), ("ldz", -8), ("ldB", 3), ("ldC", 3))]):
             assert call(**bad) == INVALID, (call, bad)
-        assert call(N=65) == UNSUPPORTED and call(B=1 << 12, E=1 << 12) == UNSUPPORTED
-        assert call(ins=inputs(ldu=big)) == UNSUPPORTED and call(ins=inputs(ldC=big)) == UNSUPPORTED      # B * ld > 2^26
+        assert call(N=65) == UNSUPPORTED and call(B=1 << 24) == UNSUPPORTED and call(E=1 << 22) == UNSUPPORTED
     for bad in (dict(T=-1), dict(save=2), dict(y=None), dict(ldy=7), dict(ws=None), dict(ws=SOME + 64)):
         assert fwd(**bad) == INVALID, bad
     assert fwd(n=size - 1) == SMALL and fwd(save=1, n=full - 1) == SMALL and fwd(B=0) == 0 and step(B=0) == 0
