@@ -8,6 +8,13 @@
 // than its piece, which makes the v' that its last inputs need, keeps the last
 // K of them, and sums the weights' gradients over its own steps; pieces' sums
 // are added in a second launch, in a fixed order.
+//
+// Bound: memory (two values a step and channel forward, three backward).  2048
+// steps of 8 rows of 2048 channels, bf16, K = 4: forward 31 us, backward 50 us,
+// the sums 5 us (4.3 and 4.0 TB/s).  With a branch for every step and lane, which
+// makes each wait for loads one for the stores before them, too, 37 and 67 us;
+// with pieces of 32 steps (1.3 rounds of the waves that fit, backward) 67 us;
+// 8 channels a lane forward 38 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

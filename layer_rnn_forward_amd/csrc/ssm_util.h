@@ -139,8 +139,8 @@ using GlobalBytes = __attribute__((address_space(1))) char*;
 template <bool BF>
 using GlobalEl = __attribute__((address_space(1))) El<BF>*;
 // What a load brings stays as it is until it is used: were it widened or made a
-// float at once, the wave would wait for it there (a training pass of 2048
-// steps waited half its time).
+// float at once, the wave would wait for it there (the forward training pass of
+// 2048 x 8 x 2048 in bf16 414 us instead of 240).
 struct SsmRows {
   GlobalBytes row;        // of the chunk's first step
   long long hop;          // bytes from one of a lane's own steps to the next
