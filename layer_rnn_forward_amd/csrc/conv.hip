@@ -2,7 +2,7 @@
 // sum_k w[c, k] x_(t - K + 1 + k), y = v or silu(v), its gradients, and its
 // form for single steps.
 //
-// A lane holds VW neighbouring channels and walks a piece of the time axis with
+// A lane holds 4 neighbouring channels (kWidth) and walks a piece of the time axis with
 // the last K inputs in registers, so an input is read once, and again only by
 // the piece that follows (K - 1 steps).  Backward walks K - 1 steps further
 // than its piece, which makes the v' that its last inputs need, keeps the last
@@ -11,10 +11,11 @@
 //
 // Bound: memory (two values a step and channel forward, three backward).  2048
 // steps of 8 rows of 2048 channels, bf16, K = 4: forward 31 us, backward 50 us,
-// the sums 5 us (4.3 and 4.0 TB/s).  With a branch for every step and lane, which
-// makes each wait for loads one for the stores before them, too, 37 and 67 us;
-// with pieces of 32 steps (1.3 rounds of the waves that fit, backward) 67 us;
-// 8 channels a lane forward 38 us.
+// the sums 5 us (4.3 and 4.0 TB/s).  With a branch for every step and lane,
+// which makes each wait for loads one for the stores before them, too, 36 us
+// forward (32 without); with pieces of 32 steps backward (1.3 rounds of the waves
+// that fit) 67 us instead of 50.
+
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -377,7 +378,7 @@ hipError_t launch(const ConvParams& p, Pass what, int bf16, hipStream_t s) {
 // Steps of a wave's piece (at least K - 1 of them): as many as give each SIMD the
 // waves that its registers hold (4 forward, 3 backward), so that all run at once.
 int rnnk::conv_piece(int T, int B, int C, bool back) {
-  const double steps = (double)B * ((C + 64 * kWidth - 1) / (64 * kWidth)) * T / (back ? 3072 : 4096);
+  const double steps = (double)B * ((C + 64 * kWidth - 1) / (64 * kWidth)) * T / (1024 * (back ? 3 : 4));
   return (int)std::min(std::max(1.0, std::ceil(steps / 8)), std::ceil(std::max(T, 1) / 8.0)) * 8;
 }
 

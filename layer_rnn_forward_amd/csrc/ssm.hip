@@ -4,18 +4,19 @@
 // A wave walks the steps of 16 channels (16 states each) one after the other,
 // the states in registers.  Bound: vector instructions.  Each step and state
 // takes a product, an exponential (half the rate), a product and two fused
-// ones, 6 issue slots of the 10 that a pass takes in all; the memory's time is a
-// third of that (8 bytes a step and channel in bf16).  2048 steps of 8 rows of
-// 2048 channels, bf16, training: 0.23 ms, 2.3 times the slots' own time (0.136
-// ms at 2.4 GHz) since this is one wave a SIMD, which waits for its own results;
-// cut into 4 segments the same walk takes 0.17 ms but the segments' first
-// launch 0.10.  A prompt of 8192 steps of 3520 channels (220 waves a segment, 18
-// segments): 0.11 + 0.15 ms.
+// ones, 6 issue slots of the 10 that a pass takes in all.  The memory's time is
+// less than half of the pass's (in bf16 8 bytes a step and channel, 16 in
+// training with the states kept).  2048 steps of 8 rows of 2048 channels, bf16,
+// training: 0.23 ms, 1.7 times the slots' own time (0.136 ms at 2.4 GHz), since
+// this is one wave a SIMD, which waits for its own results; cut into 4 segments
+// the same walk takes 0.19 ms but the segments' first launch 0.10.  A prompt of
+// 8192 steps of 3520 channels (220 waves a segment, 18 segments): 0.11 + 0.15 ms.
 //
 // Measured against it (the same training pass): the exponentials kept over
 // pieces of a block that the waves of a workgroup exchange, so that states are
-// walked twice but exponentials computed once, 0.55 ms; 2 states a lane (twice
-// the waves) 0.28; the state of every 16th step kept instead of every 8th 0.24.
+// walked twice but exponentials computed once, 0.56 ms; 2 states a lane (twice
+// the waves) 0.28 where 4 took 0.24.
+
 #include <algorithm>
 
 #include "ssm_util.h"
@@ -229,7 +230,7 @@ hipError_t launch(const SsmParams& p, bool step, hipStream_t s) {
 
 // Segments of a pass with `tiles` waves a segment: one from `alone` waves on
 // (the first launch then costs more than the waiting of few waves: forward 0.25
-// against 0.29 ms with 1024 waves, backward 0.87 against 0.70), else as many as
+// against 0.29 ms with 1024 waves, backward 0.87 against 0.72), else as many as
 // fill the device with `fill` waves (forward 4 a SIMD: 264 us for the prompt
 // above, 281 with 2; backward 2, what its registers allow), of 32 steps at least.
 static int segments(long long tiles, int T, int alone, int fill) {

@@ -12,13 +12,12 @@
 // adds the parameters' gradients of the rows and segments, too.  All in a fixed
 // order.
 //
-// Bound: vector instructions, 105 of them a step and wave (256 states): forward
-// walk and exponentials 24, back 32, sums over channels 17, over the lanes of a
-// channel 7, the rest what belongs to a channel and step alone.  2048 steps of 8
-// rows of 2048 channels, bf16: 0.49 ms in two segments (their issue slots alone
-// 0.40 at 2.4 GHz), the segments' first launch 0.07, the second 0.02.  Two waves
-// a SIMD (195 registers); with three (168 and some spilled) 0.73 ms; one segment
-// of one wave a SIMD 0.87.  Chunks of 16 steps spill: 1.6 ms.
+// Bound: vector instructions, 105 of them a step and wave (256 states).  2048
+// steps of 8 rows of 2048 channels, bf16: 0.49 ms in two segments (their issue
+// slots alone 0.40 at 2.4 GHz), the segments' first launch 0.07, the sums of dB
+// and dC 0.02.  Two waves a SIMD (195 registers): with three (168 registers and
+// 108 bytes spilled) 0.73 ms where two took 0.57, with one segment of one wave a
+// SIMD 0.87 where two took 0.61 + 0.11.  Chunks of 16 steps spill: 1.6 ms.
 #include <algorithm>
 
 #include "ssm_util.h"
