@@ -132,7 +132,8 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, unsigned at, i
 
 // The rows of a time-major tensor as a wave walks them, chunk after chunk: a
 // uniform address and the lane's part of it, of up to three steps and a row, in
-// 32 bits (B * ld <= 2^28).
+// 32 bits (B * ld <= 2^28 over several steps; a single step may lie in rows
+// farther apart, and what its lanes own past it is not read).
 // (Pointers say that they are to global memory: the compiler does not look
 // through the asm statements below for it.)
 using GlobalBytes = __attribute__((address_space(1))) char*;
@@ -149,7 +150,7 @@ struct SsmRows {
 template <bool BF, int Q>
 __device__ __forceinline__ SsmRows ssm_rows(const SsmParams& p, const SsmPlace& q, const void* x, long long ld, int t0) {
   constexpr int ES = BF ? 2 : 4;
-  const long long step = p.B * ld * ES;
+  const long long step = p.T > 1 ? p.B * ld * ES : 0;
   SsmRows r;
   r.row = (GlobalBytes)(uintptr_t)x + q.b * ld * ES + t0 * step;
   r.hop = Q * step;

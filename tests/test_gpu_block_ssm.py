@@ -63,6 +63,32 @@ def test_slices_of_wider_tensors(dtype, B):
             assert torch.equal(got[k], want[k]), k
 
 
+@pytest.mark.parametrize("N", [2, 16, 40])
+def test_one_step_in_rows_far_apart(N):
+    """A step's rows 2^27 elements apart (the last step of sequences that lie one after the other): B * ld is past what
+    several steps may have, and a lane's offset of three steps past 32 bits."""
+    c = ssm_case(1, 4, 21, N, 1, "f32")
+    want = ssm_run("softplus", c)
+    ld, at = 1 << 27, 0
+    store = torch.empty(3 * ld + 1024, device="cuda")
+
+    def far(t):
+        nonlocal at
+        v = store[at:].as_strided(t.shape, (4 * ld, ld, 1))
+        at += t.shape[-1]
+        return v.copy_(t)
+    g = {k: far(v) if k in ("u", "delta", "Bm", "Cm", "z", "dy") else gpu(v) for k, v in c.items()}
+    got = {k: far(torch.full(v.shape, 7.0)) if k in ("y", "du", "ddelta", "dBm", "dCm", "dz") else torch.full_like(v, 7.0)
+           for k, v in want.items()}
+    assert at <= 1024
+    ws = room(R.rnn_ssm_workspace_size(1, 4, 21, N, 1, "full"))
+    R.rnn_ssm_forward("softplus", *(g[k] for k in INPUTS), g["h0"], None, got["y"], got["hy"], ws, "full")
+    R.rnn_ssm_backward("softplus", *(g[k] for k in INPUTS), g["h0"], None, g["dy"], g["dhy"], got["du"], got["ddelta"],
+                       got["dA"], got["dBm"], got["dCm"], got["dD"], got["dz"], got["ddelta_bias"], got["dh0"], ws)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+
+
 def test_no_steps():
     c = ssm_case(0, 2, 10, 16, 1, "f32")
     got = compare("softplus", c, "f32")
