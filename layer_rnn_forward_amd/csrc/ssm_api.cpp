@@ -252,12 +252,15 @@ rnn_status_t rnn_ssm_backward(void* stream, rnn_delta_t mode, rnn_wtype_t wtype,
   LM_TRY(ssm_sizes(T, B, E, N, groups));
   const SsmPlan plan = ssm_plan(T, B, E, N, groups, true);
   LM_TRY(room(ws, ws_bytes, ssm_bytes(plan)));
-  if (E == 0) return RNN_STATUS_SUCCESS;
   SsmParams p{};
-  LM_TRY(ssm_inputs(p, in, mode, B > 0 ? T : 0, B, E, N, groups));
   const long long GN = (long long)groups * N;
   const rnn_ssm_grads_t& g = *grads;
-  if ((B > 0 && T > 0 && !dy) || (g.dz && !in->z)) return RNN_STATUS_INVALID_ARG;
+  if (E > 0) {
+    LM_TRY(ssm_inputs(p, in, mode, B > 0 ? T : 0, B, E, N, groups));
+    if ((B > 0 && T > 0 && !dy) || (g.dz && !in->z)) return RNN_STATUS_INVALID_ARG;
+  } else {                               // dB and dC, sums over no channels, are 0
+    p.T = T; p.B = B; p.N = N; p.G = groups;
+  }
   LM_TRY(ssm_rows(T, B, dy, lddy, E));
   LM_TRY(ssm_rows(T, B, g.du, g.lddu, E));
   LM_TRY(ssm_rows(T, B, g.ddelta, g.ldddelta, E));

@@ -392,18 +392,18 @@ __global__ __launch_bounds__(256) void rows_kernel(const SsmParams p, const Part
 template <bool BF, int S>
 hipError_t start(const SsmParams& p, hipStream_t s) {
   constexpr int NP = S * kSsmPer;
-  const int groups = ssm_groups(p, S);
+  const int groups = ssm_groups(p, S);   // 0: no channels
   const Parts parts = parts_of(p, groups, NP);
   const unsigned tiles = (unsigned)groups * p.G * p.B;
   const dim3 block(64 * kSsmTiles);
-  if (p.B > 0) {
+  if (tiles > 0) {
     if (p.segs > 1) hipLaunchKernelGGL((bwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p, parts);
     hipLaunchKernelGGL((bwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p, parts);
   }
   const long long all = (long long)p.T * p.B * p.G * 2 * NP;
-  if ((p.dBm || p.dCm) && all && groups > 1)
+  if ((p.dBm || p.dCm) && all && groups != 1)
     hipLaunchKernelGGL(channels_kernel<BF>, dim3((unsigned)std::min<long long>((all + 255) / 256, 1 << 20)), dim3(256), 0, s, p, parts, NP);
-  if (p.dA || p.dD || p.ddelta_bias)
+  if (p.E > 0 && (p.dA || p.dD || p.ddelta_bias))
     hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(((long long)p.E * (NP + 2) + 63) / 64)), dim3(256), 0, s, p, parts, NP);
   return hipGetLastError();
 }
@@ -422,6 +422,5 @@ hipError_t launch(const SsmParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t rnn_launch_ssm_bwd(const SsmParams& p, int bf16, hipStream_t s) {
-  if (p.E == 0) return hipSuccess;
   return bf16 ? launch<true>(p, s) : launch<false>(p, s);
 }

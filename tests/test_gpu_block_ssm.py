@@ -89,6 +89,18 @@ def test_one_step_in_rows_far_apart(N):
         assert torch.equal(got[k], want[k]), k
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_channels(dtype):
+    """B and C of no channels: their gradients are 0."""
+    c = ssm_case(9, 2, 6, 8, 2, dtype)
+    for k in ("u", "delta", "z", "dy"):
+        c[k] = c[k][..., :0].contiguous()
+    c |= {"A": c["A"][:0], "D": c["D"][:0], "delta_bias": c["delta_bias"][:0], "h0": c["h0"][:, :0].contiguous(),
+          "dhy": c["dhy"][:, :0].contiguous()}
+    got = ssm_run("softplus", c)
+    assert (got["dBm"] == 0).all() and (got["dCm"] == 0).all() and got["dBm"].shape == (9, 2, 16)
+
+
 def test_no_steps():
     c = ssm_case(0, 2, 10, 16, 1, "f32")
     got = compare("softplus", c, "f32")
