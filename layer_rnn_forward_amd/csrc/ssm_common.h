@@ -25,7 +25,7 @@ struct NormParams {
   void* dx;              // or null
   float* dweight;        // or null
   float* dbias;          // or null
-  float* part;           // [parts][2][D]
+  float* part;           // [parts][2][D], without dbias [parts][1][D]
   int parts;
 };
 int norm_parts(int M, int D);   // rows of partial sums of the parameters' gradients
