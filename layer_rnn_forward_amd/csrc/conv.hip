@@ -68,13 +68,19 @@ __device__ __forceinline__ Place place(const ConvParams& p) {
   return r;
 }
 
+// values of a lane's weights from the i-th 16 bytes on, where `left` channels are
+// there (all of them may be 2^30: times K they are past 32 bits)
+template <int K, int VW>
+__host__ __device__ constexpr int weights_left(int left, int i) { return (left < VW ? left : VW) * K - 4 * i; }
+static_assert(weights_left<kConvMost, kWidth>((1 << 30) - 1, 1) == kConvMost * kWidth - 4, "no overflow with the most channels");
+
 template <int K, int VW>
 __device__ __forceinline__ void load_weights(const ConvParams& p, const Place& at, float (&w)[K][VW], float (&bias)[VW]) {
   // the lane's weights are neighbours: 16 bytes a load
   const float* from = p.w + (long long)at.c * K;
   RawPiece<false, 4> raw[VW * K / 4];
 #pragma unroll
-  for (int i = 0; i < VW * K / 4; ++i) raw[i] = load_raw<false, 4>(from + 4 * i, at.left * K - 4 * i);
+  for (int i = 0; i < VW * K / 4; ++i) raw[i] = load_raw<false, 4>(from + 4 * i, weights_left<K, VW>(at.left, i));
   load_piece<false, VW>(p.bias + at.c, p.bias ? at.left : 0, bias);
 #pragma unroll
   for (int j = 0; j < VW; ++j)

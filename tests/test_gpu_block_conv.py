@@ -115,3 +115,12 @@ def test_no_rows():
     dw, db = torch.full_like(w, 3.0), torch.full((6,), 3.0, device="cuda")
     R.rnn_conv_backward("silu", x, w, None, None, None, x, None, None, dw, db, None, room(R.rnn_conv_workspace_size(4, 0, 6, 3)))
     assert not dw.any() and not db.any()
+
+
+def test_more_channels_than_32_bits_of_weights():
+    """C * K past 2^31: a step without state or bias is the product with the newest input's weight, exactly."""
+    C, K = (1 << 28) + 5, 8
+    x, w = torch.empty(1, 1, C, device="cuda").uniform_(-1, 1), torch.empty(C, K, device="cuda").uniform_(-1, 1)
+    y = torch.full_like(x, 7.0)
+    R.rnn_conv_forward("none", x, w, None, None, None, y, None)
+    assert torch.equal(y.view(C), w[:, K - 1] * x.view(C))
