@@ -312,7 +312,7 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
 
 __global__ __launch_bounds__(64 * kSumWaves) void sum_kernel(const ConvParams p, int rows) {
   __shared__ float lds[kSumWaves][64];
-  const long long n = (long long)(p.K + 1) * p.C, i = (long long)blockIdx.x * 64 + (threadIdx.x & 63);
+  const long long n = (long long)(p.K + 1) * p.C, i = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 64 + (threadIdx.x & 63);
   const float s = column_sum(p.part, n, i, rows, lds);
   if (threadIdx.x >= 64 || i >= n) return;
   const int k = (int)(i / p.C), c = (int)(i - (long long)k * p.C);
@@ -403,6 +403,6 @@ hipError_t rnn_launch_conv_bwd(const ConvParams& q, int bf16, hipStream_t s) {
   const hipError_t e = launch(p, BWD, bf16, s);
   if (e != hipSuccess || !sums || p.C == 0) return e;
   const int rows = p.B * ((p.pieces + kConvWaves - 1) / kConvWaves);
-  hipLaunchKernelGGL(sum_kernel, dim3((unsigned)(((long long)(p.K + 1) * p.C + 63) / 64)), dim3(64 * kSumWaves), 0, s, p, rows);
+  hipLaunchKernelGGL(sum_kernel, wide_grid(((long long)(p.K + 1) * p.C + 63) / 64), dim3(64 * kSumWaves), 0, s, p, rows);
   return hipGetLastError();
 }

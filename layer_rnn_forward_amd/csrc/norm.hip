@@ -20,11 +20,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Workgroups by rows: a launch has fewer than 2^32 threads in a dimension.
-dim3 row_grid(long long blocks) {
-  const long long x = std::min(blocks, 1LL << 21);
-  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
-}
 __device__ __forceinline__ long long row_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // sum over L lanes (64: a wave, else the workgroup); `slot` alternates between calls
@@ -363,7 +358,7 @@ void start(const NormParams& p, bool back, int blocks, hipStream_t s) {
   constexpr int threads = L < kThreads ? kThreads : L, rows = threads / L;
   if (back && p.dbias) hipLaunchKernelGGL((bwd_kernel<BF, L, P, true>), dim3(blocks), dim3(back_threads(L)), 0, s, p);
   else if (back) hipLaunchKernelGGL((bwd_kernel<BF, L, P, false>), dim3(blocks), dim3(back_threads(L)), 0, s, p);
-  else hipLaunchKernelGGL((fwd_kernel<BF, L, P>), row_grid(((long long)p.M + rows - 1) / rows), dim3(threads), 0, s, p);
+  else hipLaunchKernelGGL((fwd_kernel<BF, L, P>), wide_grid(((long long)p.M + rows - 1) / rows), dim3(threads), 0, s, p);
 }
 
 template <bool BF>
@@ -394,9 +389,9 @@ hipError_t launch(const NormParams& p, bool back, hipStream_t s) {
     const int blocks = back ? back_blocks(p.M, sh.lanes) : 0;
     pick<BF>(p, back, sh, blocks, s);
   } else if (!back) {
-    hipLaunchKernelGGL(fwd_long_kernel<BF>, row_grid(p.M), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL(fwd_long_kernel<BF>, wide_grid(p.M), dim3(1024), 0, s, p);
   } else {
-    if (p.dx) hipLaunchKernelGGL(bwd_long_kernel<BF>, row_grid(p.M), dim3(1024), 0, s, p);
+    if (p.dx) hipLaunchKernelGGL(bwd_long_kernel<BF>, wide_grid(p.M), dim3(1024), 0, s, p);
     if (p.part) hipLaunchKernelGGL(columns_kernel<BF>, dim3((p.D + kThreads - 1) / kThreads, (unsigned)p.parts), dim3(kThreads), 0, s, p);
   }
   return hipGetLastError();

@@ -191,6 +191,13 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
+// Workgroups (of up to 1024 threads) in two dimensions, the last row of them partly
+// past the end: a launch has fewer than 2^32 threads in a dimension.
+inline dim3 wide_grid(long long blocks) {
+  const long long x = blocks < (1LL << 21) ? blocks : 1LL << 21;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+
 // Column i of `rows` rows of n partial sums: a workgroup of 16 waves takes 64
 // columns, every 16th row a wave; the sum is the first wave's.
 constexpr int kSumWaves = 16;

@@ -124,3 +124,16 @@ def test_more_channels_than_32_bits_of_weights():
     y = torch.full_like(x, 7.0)
     R.rnn_conv_forward("none", x, w, None, None, None, y, None)
     assert torch.equal(y.view(C), w[:, K - 1] * x.view(C))
+
+
+def test_more_threads_of_sums_than_a_dimension_takes():
+    """(K + 1) C past 2^28: the sums of dw and dbias have more than 2^32 threads."""
+    T, C, K = 2, 1 << 26, 4
+    x, dy = (torch.empty(T, 1, C, device="cuda").uniform_(-1, 1) for _ in range(2))
+    w, dw, db = torch.ones(C, K, device="cuda"), torch.full((C, K), 7.0, device="cuda"), torch.full((C,), 7.0, device="cuda")
+    R.rnn_conv_backward("none", x, w, None, None, None, dy, None, None, dw, db, None, room(R.rnn_conv_workspace_size(T, 1, C, K)))
+    x, dy = x.view(T, C), dy.view(T, C)
+    assert torch.equal(db, dy[0] + dy[1]) and not dw[:, :2].any() and torch.equal(dw[:, 2], dy[1] * x[0])
+    a, b = dy[0].double() * x[0], dy[1].double() * x[1]
+    # one product rounded, then their sum: half a step (2^-24) of each
+    assert ((dw[:, 3] - (a + b)).abs() <= 2.0 ** -24 * (2 * a.abs() + b.abs()) * (1 + 2.0 ** -20)).all()
