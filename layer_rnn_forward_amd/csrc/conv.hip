@@ -232,7 +232,7 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
       for (int i = 0; i < kBackAhead; ++i) {
         if (!FAST && t + i >= end) break;
         const int s = t + i - (K - 1);      // the input whose gradient is whole
-        const bool mine = FAST || t + i < at.t1;
+        const bool mine = FAST || t + i < min(at.t1, at.len);   // (past the row's length: 0 times an infinite input)
         float dx[VW], more[VW], in[VW], dy[VW];
         unpack<BF, VW>(rx[i], in);
         unpack<BF, VW>(rdy[i], dy);
@@ -263,6 +263,7 @@ __global__ __launch_bounds__(64 * kConvWaves) void bwd_kernel(const ConvParams p
           dx[j] = last ? more[j] : 0.f;
 #pragma unroll
           for (int k = 0; k < K; ++k) dx[j] = fmaf(w[k][j], dv[k][j], dx[j]);
+          if (!FAST && s >= at.len) dx[j] = 0.f;                // whatever the weights
         }
         if (FAST || s >= at.t0) {
           if (FAST || p.dx) store_piece<BF, VW>((El<BF>*)p.dx + ((long long)s * p.B + at.b) * p.lddx + at.c, FAST ? VW : at.left, dx);

@@ -137,3 +137,23 @@ def test_more_threads_of_sums_than_a_dimension_takes():
     a, b = dy[0].double() * x[0], dy[1].double() * x[1]
     # one product rounded, then their sum: half a step (2^-24) of each
     assert ((dw[:, 3] - (a + b)).abs() <= 2.0 ** -24 * (2 * a.abs() + b.abs()) * (1 + 2.0 ** -20)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [40, 256])
+def test_steps_past_a_row_take_no_part_in_gradients(dtype, C):
+    """An infinite last input of a row meets the newest tap only; an infinite weight leaves dx past the row's length 0."""
+    c = conv_case(45, 3, C, 4, dtype, [45, 21, 1], bias=False)
+    c["dy"] = c["dy"].abs() + 0.1
+    c["x"][20, 1] = c["s0"][1, 2] = 0
+    want = conv_run("none", c)
+    c["x"][20, 1] = c["s0"][1, 2] = float("inf")      # the second row's last; the third's x_-2, which its one step meets with tap 1
+    got = conv_run("none", c)
+    assert torch.equal(got["dw"][:, [0, 2]], want["dw"][:, [0, 2]])
+    assert (got["dw"][:, [1, 3]] == float("inf")).all()
+    for k in ("dx", "ds0", "dbias"):
+        assert torch.equal(got[k], want[k]), k
+    c["w"][:, 2] = float("inf")
+    got = conv_run("none", c)
+    for b, n in enumerate((45, 21, 1)):
+        assert not got["dx"][n:, b].any() and not got["y"][n:, b].any()
