@@ -52,7 +52,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void step_kernel(const SsmParams p)
   if (p.hy) store_states(p.hy + st, left, h);
   o = sum_channel<1, S>(o);
   if (q.n) return;
-  o = fmaf(D, u, o);
+  if (p.D) o = fmaf(D, u, o);            // (an infinite u times 0 would be NaN)
   if (p.z) {
     float a, da;
     act_pair<ACT_SILU>(z, a, da);
@@ -178,7 +178,8 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
         }
       }
       if constexpr (!LOCAL) {
-        y[i] = fmaf(D, u[i], sum_to_lane<S, Q>(part)) * gate[i];
+        const float o = sum_to_lane<S, Q>(part);
+        y[i] = (p.D ? fmaf(D, u[i], o) : o) * gate[i];
         if (t0 + i * Q + q.j >= end) y[i] = 0.f;
       }
     }

@@ -263,7 +263,8 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
             part[l] = fmaf(C[r], h[r], part[l]);
           }
         }
-        o[i] = fmaf(D, u[i], sum_to_lane<S, Q>(part));
+        o[i] = sum_to_lane<S, Q>(part);
+        o[i] = p.D ? fmaf(D, u[i], o[i]) : o[i];   // (an infinite u times 0 would be NaN)
       }
       // backwards
       float (*const to)[2][NP] = sums[LOCAL ? 0 : t0 / G & 1][wave];
@@ -313,7 +314,8 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
         const bool on = t0 + i * Q + q.j < end;
         dD = fmaf(go[i], u[i], dD);
         dbias += on ? dd : 0.f;
-        rows[0][i] = on ? fmaf(D, go[i], d[i] * gB[i]) : 0.f;
+        const float du = d[i] * gB[i];
+        rows[0][i] = on ? (p.D ? fmaf(D, go[i], du) : du) : 0.f;
         rows[1][i] = on ? dd : 0.f;
         rows[2][i] = on ? o[i] * gz[i] : 0.f;
       }

@@ -1,11 +1,12 @@
 """Selective state-space scan on the GPU against the definition in 64 bits; tolerances are the oracle's bounds on an
 evaluation in fp32 and half a step of the output's type."""
 
+import numpy as np
 import pytest
 import torch
 
 import layer_rnn_forward_amd as R
-from oracle.bounds import check
+from oracle.bounds import Bound, check
 from tests.block_gpu import INPUTS, gpu, room, ssm_case, ssm_run, ssm_want
 
 pytestmark = pytest.mark.gpu
@@ -259,3 +260,42 @@ def test_infinite_coefficient_reaches_only_its_own_sums():
     got = ssm_run("softplus", c)
     assert (got["dBm"][:8, 0, 3] == float("inf")).all() and got["dBm"][8:, 0, 3].isfinite().all()
     assert got["dBm"][:, 0, [n for n in range(16) if n != 3]].isfinite().all() and got["dCm"].isfinite().all()
+
+
+def positive(T, N, dtype, seed):
+    """Inputs whose products and sums cannot cancel: what is infinite stays so, with its sign."""
+    c = ssm_case(T, 3, 20, N, 1, dtype, seed=seed, mode="linear", gated=False, extras=False)
+    for k in ("u", "Bm", "Cm", "h0", "dy", "dhy"):
+        c[k] = c[k].abs() + 0.25
+    c["A"] = -torch.rand(20, N, generator=torch.Generator().manual_seed(seed)) - 0.1
+    return c
+
+
+def compare_infinite(c, dtype):
+    """As compare, where the definition's values may be infinite or NaN: the same ones are."""
+    got = ssm_run("linear", c)
+    with np.errstate(all="ignore"):
+        want = ssm_want("linear", c)
+    for k, w in want.items():
+        g, there = got[k].double().cpu().numpy(), np.isfinite(w.v)
+        assert np.array_equal(g[~there], w.v[~there], equal_nan=True), (k, g[~there][:4], w.v[~there][:4])
+        finite = torch.tensor(np.where(there, g, 0.0))
+        check(k, finite, Bound(np.where(there, w.v, 0.0), np.where(there, w.e, 0.0)), "f32" if k in FP32 else dtype)
+    return got, want
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_skip_that_is_left_out_takes_no_part(dtype):
+    """Without D an infinite u or dy is no product with 0."""
+    c = positive(72, 16, dtype, seed=12)
+    c["u"][30, 1, 4] = float("inf")
+    got, _ = compare_infinite(c, dtype)
+    assert got["y"][30:, 1, 4].isinf().all() and not got["y"].isnan().any() and not got["hy"].isnan().any()
+    g = {k: gpu(v) for k, v in c.items()}
+    h, y = g["h0"].clone(), torch.empty_like(g["u"][0])
+    R.rnn_ssm_step("linear", *(g[k] if k in ("A", "D", "delta_bias") or g[k] is None else g[k][30] for k in INPUTS), h, y, h)
+    assert y[1, 4].isinf() and not y.isnan().any()
+    c = positive(72, 16, dtype, seed=12)
+    c["dy"][30, 1, 4] = float("inf")
+    got = ssm_run("linear", c)
+    assert got["du"][:31, 1, 4].isinf().all() and not got["du"].isnan().any()
