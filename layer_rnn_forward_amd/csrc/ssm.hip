@@ -47,6 +47,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void step_kernel(const SsmParams p)
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     h[r] = fmaf(__builtin_amdgcn_exp2f(d * (A[r] * kLog2e)), h[r], du * B[r]);
+    if (r >= left) h[r] = 0.f;           // not there (an infinite d or du times 0)
     o = fmaf(C[r], h[r], o);
   }
   if (p.hy) store_states(p.hy + st, left, h);
@@ -61,8 +62,9 @@ __global__ __launch_bounds__(64 * kSsmTiles) void step_kernel(const SsmParams p)
   el_store<BF>((El<BF>*)p.y + q.b * p.ldy + q.e, o);
 }
 
-// LOCAL: the segments' maps (but the last one's), no outputs
-template <bool BF, int S, bool LOCAL>
+// LOCAL: the segments' maps (but the last one's), no outputs.  PAD: some lanes'
+// states are not there.
+template <bool BF, int S, bool LOCAL, bool PAD>
 __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) {
   constexpr int R = kSsmPer, G = ssm_chunk(S), NP = S * R, Q = S < 4 ? S : 4, I = G / Q;
   __shared__ __align__(16) float bc[kSsmTiles][G][2][NP];
@@ -159,28 +161,41 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
       }
     };
     read(0);
+    // GUARD: states that are not there are held at 0 (an infinite d or du would
+    // make them NaN, 0 times it, and through them the sum over the states).  The
+    // empty asm statement keeps the compiler from sharing the ways' values.
+    const bool usual = !PAD || all_finite(d, du);
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      if (i + 1 < I) read(i + 1);
-      if (G > kSsmKeep && i * Q == kSsmKeep)
+    for (int way = 0; way < (PAD ? 2 : 1); ++way) {
+      const bool GUARD = way == 1;
+      if (PAD && usual == GUARD) continue;
+      if (GUARD)
 #pragma unroll
-        for (int r = 0; r < R; ++r) mid[r] = h[r];
-      asm volatile("" ::: "memory");
-      float part[Q];
+        for (int i = 0; i < I; ++i) asm volatile("" : "+v"(d[i]), "+v"(du[i]));
 #pragma unroll
-      for (int l = 0; l < Q; ++l) {
-        const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
-        part[l] = 0.f;
+      for (int i = 0; i < I; ++i) {
+        if (i + 1 < I) read(i + 1);
+        if (G > kSsmKeep && i * Q == kSsmKeep)
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          h[r] = fmaf(__builtin_amdgcn_exp2f(ds * A[r]), h[r], dus * B[i & 1][l][r]);
-          if constexpr (!LOCAL) part[l] = fmaf(C[i & 1][l][r], h[r], part[l]);
+          for (int r = 0; r < R; ++r) mid[r] = h[r];
+        asm volatile("" ::: "memory");
+        float part[Q];
+#pragma unroll
+        for (int l = 0; l < Q; ++l) {
+          const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
+          part[l] = 0.f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            h[r] = fmaf(__builtin_amdgcn_exp2f(ds * A[r]), h[r], dus * B[i & 1][l][r]);
+            if (GUARD && r >= left) h[r] = 0.f;
+            if constexpr (!LOCAL) part[l] = fmaf(C[i & 1][l][r], h[r], part[l]);
+          }
         }
-      }
-      if constexpr (!LOCAL) {
-        const float o = sum_to_lane<S, Q>(part);
-        y[i] = (p.D ? fmaf(D, u[i], o) : o) * gate[i];
-        if (t0 + i * Q + q.j >= end) y[i] = 0.f;
+        if constexpr (!LOCAL) {
+          const float o = sum_to_lane<S, Q>(part);
+          y[i] = (p.D ? fmaf(D, u[i], o) : o) * gate[i];
+          if (t0 + i * Q + q.j >= end) y[i] = 0.f;
+        }
       }
     }
   }
@@ -202,7 +217,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
   }
 }
 
-template <bool BF, int S>
+template <bool BF, int S, bool PAD>
 hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
   const unsigned tiles = (unsigned)ssm_blocks(p.B, p.E, p.N, p.G);
   const dim3 block(64 * kSsmTiles);
@@ -210,9 +225,14 @@ hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
     hipLaunchKernelGGL((step_kernel<BF, S>), dim3(tiles), block, 0, s, p);
     return hipGetLastError();
   }
-  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p);
-  hipLaunchKernelGGL((fwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p);
+  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true, PAD>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p);
+  hipLaunchKernelGGL((fwd_kernel<BF, S, false, PAD>), dim3(tiles * p.segs), block, 0, s, p);
   return hipGetLastError();
+}
+
+template <bool BF, int S>
+hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
+  return p.N < S * kSsmPer ? start<BF, S, true>(p, step, s) : start<BF, S, false>(p, step, s);
 }
 
 template <bool BF>

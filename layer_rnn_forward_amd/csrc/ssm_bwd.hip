@@ -83,8 +83,10 @@ __device__ __forceinline__ bool has_sums(int lane) {
   return mine;
 }
 
-// LOCAL: the segments' maps of g (but the first one's), no outputs
-template <bool BF, int S, bool LOCAL>
+// LOCAL: the segments' maps of g (but the first one's), no outputs.  PAD: some
+// lanes' states are not there; they and their gradients are held at 0, whatever
+// d, du and do.
+template <bool BF, int S, bool LOCAL, bool PAD>
 __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams p, const Parts out) {
   constexpr int R = kSsmPer, G = kSsmKeep, NP = S * R, Q = S < 4 ? S : 4, I = G / Q, CH = 64 / S, W = kSsmTiles;
   __shared__ __align__(16) float bc[W][G][2][NP];
@@ -231,83 +233,100 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
       put_bc<BF, G, NP>(&bc[wave][0][0][0], rbc);
       if (!LOCAL && t0 < top) flush(t0 + G);
       if (t0 > begin) load(t0 - G);
-      if constexpr (LOCAL) {
+      // GUARD: states that are not there and their gradients are held at 0 (an
+      // infinite d, du or do would make them NaN, 0 times it)
+      float o[I], gB[I], gA[I];
+      const bool usual = !PAD || (all_finite(d, du) && all_finite(go, go));
 #pragma unroll
-        for (int s = G - 1; s >= 0; --s) {
-          const float ds = from_lane<Q>(d[s / Q], s % Q), gs = from_lane<Q>(go[s / Q], s % Q);
-          float C[R];
-          lds_get(bcs + s * 2 * NP + NP, C);
+      for (int way = 0; way < (PAD ? 2 : 1); ++way) {
+        const bool GUARD = way == 1;
+        if (PAD && usual == GUARD) continue;
+        if (GUARD)
 #pragma unroll
-          for (int r = 0; r < R; ++r) e[r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e)) * fmaf(C[r], gs, e[r]);
-        }
-        continue;
-      }
-      // forwards: the exponentials, the state before every step, what the gate multiplied
-      float a[G][R], hb[G][R], o[I];
+          for (int i = 0; i < I; ++i) asm volatile("" : "+v"(d[i]), "+v"(du[i]), "+v"(go[i]));
+        if constexpr (LOCAL) {
 #pragma unroll
-      for (int i = 0; i < I; ++i) {
-        float part[Q];
+          for (int s = G - 1; s >= 0; --s) {
+            const float ds = from_lane<Q>(d[s / Q], s % Q), gs = from_lane<Q>(go[s / Q], s % Q);
+            float C[R];
+            lds_get(bcs + s * 2 * NP + NP, C);
 #pragma unroll
-        for (int l = 0; l < Q; ++l) {
-          const int s = i * Q + l;
-          const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
-          float B[R], C[R];
-          lds_get(bcs + s * 2 * NP, B);
-          lds_get(bcs + s * 2 * NP + NP, C);
-          part[l] = 0.f;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            a[s][r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e));
-            hb[s][r] = h[r];
-            h[r] = fmaf(a[s][r], h[r], dus * B[r]);
-            part[l] = fmaf(C[r], h[r], part[l]);
-          }
-        }
-        o[i] = sum_to_lane<S, Q>(part);
-        o[i] = p.D ? fmaf(D, u[i], o[i]) : o[i];   // (an infinite u times 0 would be NaN)
-      }
-      // backwards
-      float (*const to)[2][NP] = sums[LOCAL ? 0 : t0 / G & 1][wave];
-      float gB[I], gA[I], v[2][2][R];
-#pragma unroll
-      for (int i = I - 1; i >= 0; --i) {
-        float pB[Q], pA[Q];
-#pragma unroll
-        for (int l = Q - 1; l >= 0; --l) {
-          const int s = i * Q + l;
-          const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l), gs = from_lane<Q>(go[i], l);
-          float B[R], C[R];
-          lds_get(bcs + s * 2 * NP, B);
-          lds_get(bcs + s * 2 * NP + NP, C);
-          pB[l] = pA[l] = 0.f;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float g = fmaf(C[r], gs, e[r]);
-            v[s & 1][0][r] = g * dus;
-            v[s & 1][1][r] = gs * (s == G - 1 ? h[r] : hb[s == G - 1 ? s : s + 1][r]);
-            pB[l] = fmaf(g, B[r], pB[l]);
-            e[r] = g * a[s][r];
-            const float x = e[r] * hb[s][r];
-            pA[l] = fmaf(x, A[r], pA[l]);
-            dA[r] = fmaf(x, ds, dA[r]);
-          }
-          if (s & 1) continue;
-          // two steps' dB and dC: [2][2][R] values
-          constexpr int V = 4 * R;
-          float f[V];
-#pragma unroll
-          for (int x = 0; x < V; ++x) f[x] = v[x / (2 * R)][x / R % 2][x % R];
-          sum_channels<S, 32, V>(f);
-          if (has_sums<S, V>(lane))
-#pragma unroll
-            for (int x = 0; x < sums_left<S, V>(); ++x) {
-              const int y = first_sum<S, V>(lane) + x;
-              to[s + y / (2 * R)][y / R % 2][q.n + y % R] = f[x];
+            for (int r = 0; r < R; ++r) {
+              e[r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e)) * fmaf(C[r], gs, e[r]);
+              if (GUARD && r >= left) e[r] = 0.f;
             }
+          }
+          continue;
         }
-        gB[i] = sum_to_lane<S, Q>(pB);
-        gA[i] = sum_to_lane<S, Q>(pA);
+        // forwards: the exponentials, the state before every step, what the gate multiplied
+        float a[G][R], hb[G][R];
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          float part[Q];
+#pragma unroll
+          for (int l = 0; l < Q; ++l) {
+            const int s = i * Q + l;
+            const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l);
+            float B[R], C[R];
+            lds_get(bcs + s * 2 * NP, B);
+            lds_get(bcs + s * 2 * NP + NP, C);
+            part[l] = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              a[s][r] = __builtin_amdgcn_exp2f(ds * (A[r] * kLog2e));
+              hb[s][r] = h[r];
+              h[r] = fmaf(a[s][r], h[r], dus * B[r]);
+              if (GUARD && r >= left) a[s][r] = h[r] = 0.f;
+              part[l] = fmaf(C[r], h[r], part[l]);
+            }
+          }
+          o[i] = sum_to_lane<S, Q>(part);
+          o[i] = p.D ? fmaf(D, u[i], o[i]) : o[i];   // (an infinite u times 0 would be NaN)
+        }
+        // backwards
+        float (*const to)[2][NP] = sums[LOCAL ? 0 : t0 / G & 1][wave];
+        float v[2][2][R];
+#pragma unroll
+        for (int i = I - 1; i >= 0; --i) {
+          float pB[Q], pA[Q];
+#pragma unroll
+          for (int l = Q - 1; l >= 0; --l) {
+            const int s = i * Q + l;
+            const float ds = from_lane<Q>(d[i], l), dus = from_lane<Q>(du[i], l), gs = from_lane<Q>(go[i], l);
+            float B[R], C[R];
+            lds_get(bcs + s * 2 * NP, B);
+            lds_get(bcs + s * 2 * NP + NP, C);
+            pB[l] = pA[l] = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const float g = GUARD && r >= left ? 0.f : fmaf(C[r], gs, e[r]);
+              v[s & 1][0][r] = g * dus;
+              v[s & 1][1][r] = gs * (s == G - 1 ? h[r] : hb[s == G - 1 ? s : s + 1][r]);
+              pB[l] = fmaf(g, B[r], pB[l]);
+              e[r] = g * a[s][r];
+              const float x = e[r] * hb[s][r];
+              pA[l] = fmaf(x, A[r], pA[l]);
+              dA[r] = fmaf(x, ds, dA[r]);
+            }
+            if (s & 1) continue;
+            // two steps' dB and dC: [2][2][R] values
+            constexpr int V = 4 * R;
+            float f[V];
+#pragma unroll
+            for (int x = 0; x < V; ++x) f[x] = v[x / (2 * R)][x / R % 2][x % R];
+            sum_channels<S, 32, V>(f);
+            if (has_sums<S, V>(lane))
+#pragma unroll
+              for (int x = 0; x < sums_left<S, V>(); ++x) {
+                const int y = first_sum<S, V>(lane) + x;
+                to[s + y / (2 * R)][y / R % 2][q.n + y % R] = f[x];
+              }
+          }
+          gB[i] = sum_to_lane<S, Q>(pB);
+          gA[i] = sum_to_lane<S, Q>(pA);
+        }
       }
+      if constexpr (LOCAL) continue;
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const float dd = slope[i] * fmaf(u[i], gB[i], gA[i]);
@@ -391,7 +410,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const SsmParams p, const Part
   }
 }
 
-template <bool BF, int S>
+template <bool BF, int S, bool PAD>
 hipError_t start(const SsmParams& p, hipStream_t s) {
   constexpr int NP = S * kSsmPer;
   const int groups = ssm_groups(p, S);   // 0: no channels
@@ -399,8 +418,8 @@ hipError_t start(const SsmParams& p, hipStream_t s) {
   const unsigned tiles = (unsigned)groups * p.G * p.B;
   const dim3 block(64 * kSsmTiles);
   if (tiles > 0) {
-    if (p.segs > 1) hipLaunchKernelGGL((bwd_kernel<BF, S, true>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p, parts);
-    hipLaunchKernelGGL((bwd_kernel<BF, S, false>), dim3(tiles * p.segs), block, 0, s, p, parts);
+    if (p.segs > 1) hipLaunchKernelGGL((bwd_kernel<BF, S, true, PAD>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p, parts);
+    hipLaunchKernelGGL((bwd_kernel<BF, S, false, PAD>), dim3(tiles * p.segs), block, 0, s, p, parts);
   }
   const long long all = (long long)p.T * p.B * p.G * 2 * NP;
   if ((p.dBm || p.dCm) && all && groups != 1)
@@ -408,6 +427,11 @@ hipError_t start(const SsmParams& p, hipStream_t s) {
   if (p.E > 0 && (p.dA || p.dD || p.ddelta_bias))
     hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(((long long)p.E * (NP + 2) + 63) / 64)), dim3(256), 0, s, p, parts, NP);
   return hipGetLastError();
+}
+
+template <bool BF, int S>
+hipError_t start(const SsmParams& p, hipStream_t s) {
+  return p.N < S * kSsmPer ? start<BF, S, true>(p, s) : start<BF, S, false>(p, s);
 }
 
 template <bool BF>

@@ -86,6 +86,15 @@ __device__ __forceinline__ float sum_to_lane(float (&v)[Q]) {
   return sum_channel<4, S>(v[0]);
 }
 
+// whether all lanes' values are finite
+template <int I>
+__device__ __forceinline__ bool all_finite(const float (&v)[I], const float (&w)[I]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < I; ++i) s = fmaf(0.f, w[i], fmaf(0.f, v[i], s));
+  return !__any(s != 0.f);               // an infinity or NaN times 0 is NaN
+}
+
 // a lane's states, `left` of which are there
 __device__ __forceinline__ void load_states(const float* p, int left, float (&v)[kSsmPer]) { load_piece<false, kSsmPer>(p, left, v); }
 __device__ __forceinline__ void store_states(float* p, int left, const float (&v)[kSsmPer]) { store_piece<false, kSsmPer>(p, left, v); }

@@ -299,3 +299,32 @@ def test_a_skip_that_is_left_out_takes_no_part(dtype):
     c["dy"][30, 1, 4] = float("inf")
     got = ssm_run("linear", c)
     assert got["du"][:31, 1, 4].isinf().all() and not got["du"].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 13, 16, 24, 41, 64])
+def test_infinite_inputs_are_infinite_results(dtype, N):
+    """Also where the states are fewer than the lanes hold: those that are not there take no part."""
+    c = positive(72, N, dtype, seed=12)
+    c["u"][30, 1, 4] = float("inf")
+    got, want = compare_infinite(c, dtype)
+    for k in ("y", "hy", "ddelta", "dBm", "dCm", "dA"):
+        assert got[k].isinf().any() and not got[k].isnan().any(), k
+    assert got["y"][30:, 1, 4].isinf().all() and np.isinf(want["dA"].v[4]).all()
+    c["delta"][40, 2, 7] = float("inf")
+    got = ssm_run("linear", c)
+    assert got["y"][40:, 2, 7].isinf().all() and got["hy"][2, 7].isinf().all()
+
+
+@pytest.mark.parametrize("N", [1, 3, 13, 24])
+def test_infinite_inputs_of_single_steps(N):
+    c = positive(4, N, "f32", seed=13)
+    c["u"][2, 1, 4], c["delta"][2, 2, 7] = float("inf"), float("inf")
+    want = ssm_run("linear", c, backward=False)
+    g = {k: gpu(v) for k, v in c.items()}
+    h, y = g["h0"].clone(), torch.empty_like(g["u"])
+    for t in range(4):
+        R.rnn_ssm_step("linear", *(g[k] if k in ("A", "D", "delta_bias") or g[k] is None else g[k][t] for k in INPUTS), h, y[t], h)
+    for b, e in ((1, 4), (2, 7)):
+        assert y[2:, b, e].isinf().all() and h[b, e].isinf().all()
+    assert torch.equal(y.isinf(), want["y"].isinf()) and not y.isnan().any() and int(y.isinf().sum()) == 4
