@@ -328,3 +328,20 @@ def test_infinite_inputs_of_single_steps(N):
     for b, e in ((1, 4), (2, 7)):
         assert y[2:, b, e].isinf().all() and h[b, e].isinf().all()
     assert torch.equal(y.isinf(), want["y"].isinf()) and not y.isnan().any() and int(y.isinf().sum()) == 4
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 4, 13, 16, 64])
+@pytest.mark.parametrize("T,lengths", [(70, None), (70, [70, 39, 1]), (300, [300, 203, 35])])
+def test_infinite_states_past_a_rows_end(dtype, N, T, lengths):
+    """A state that an infinite input has left infinite adds nothing past the row's last step, wherever that lies in a
+    chunk of steps."""
+    c = positive(T, N, dtype, seed=14)
+    if lengths:
+        c["lengths"] = torch.tensor(lengths, dtype=torch.int32)
+    c["u"][30, 1, 4] = float("inf")
+    got, want = compare_infinite(c, dtype)
+    assert np.isinf(want["dA"].v[4]).all() and not got["dA"].isnan().any()
+    c["u"][30, 1, 4], c["u"][-1 if not lengths else lengths[1] - 1, 1, 5] = 0.5, float("inf")     # the last step: dA is finite
+    got, _ = compare_infinite(c, dtype)
+    assert got["dA"].isfinite().all()
