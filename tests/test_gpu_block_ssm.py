@@ -345,3 +345,29 @@ def test_infinite_states_past_a_rows_end(dtype, N, T, lengths):
     c["u"][30, 1, 4], c["u"][-1 if not lengths else lengths[1] - 1, 1, 5] = 0.5, float("inf")     # the last step: dA is finite
     got, _ = compare_infinite(c, dtype)
     assert got["dA"].isfinite().all()
+
+
+# (T, B, E, N, G): more channels a group than a workgroup takes, 256 with up to 4 states, 128 with 8, 64 with 16, 32 with 32
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,E,N,G,lengths", [(21, 2, 260, 4, 1, [21, 13]), (19, 1, 530, 3, 2, None), (33, 2, 130, 8, 1, [33, 6]),
+                                               (40, 1, 300, 7, 1, None), (41, 2, 70, 16, 1, [41, 17]), (37, 2, 140, 16, 2, None),
+                                               (50, 2, 200, 13, 1, [0, 50]), (26, 2, 33, 30, 1, [26, 9]), (35, 1, 140, 32, 2, None),
+                                               (30, 2, 40, 64, 1, [30, 23])])
+def test_sums_over_several_workgroups(dtype, T, B, E, N, G, lengths):
+    """dB and dC of a group that several workgroups share, for every number of lanes a channel."""
+    print("CASE ssm sums", dtype, T, B, E, N, G, flush=True)
+    compare("softplus", ssm_case(T, B, E, N, G, dtype, lengths, seed=15), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,E,N,G,lengths", [(520, 2, 90, 16, 1, [520, 301]), (300, 1, 300, 4, 1, None), (200, 1, 150, 8, 1, [130])])
+def test_sums_over_several_workgroups_and_segments(dtype, T, B, E, N, G, lengths):
+    compare("softplus", ssm_case(T, B, E, N, G, dtype, lengths, seed=16), dtype)
+
+
+@pytest.mark.parametrize("dtype,E,N,G", [("f32", 11040, 16, 10), ("bf16", 44160, 3, 1)])
+def test_sums_over_several_workgroups_and_parts(dtype, E, N, G):
+    """690 waves a segment: backward has two segments, cut into two parts each for its first launch, as in wide training
+    batches, and several workgroups a group."""
+    print("CASE ssm parts", dtype, E, N, G, flush=True)
+    compare("softplus", ssm_case(130, 1, E, N, G, dtype, [117], seed=17), dtype)
