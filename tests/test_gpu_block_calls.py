@@ -237,3 +237,40 @@ def test_binding_refuses_other_layouts_and_types():
         R.rnn_ssm_forward("softplus", x, x, A, bc, bc, None, None, None, None, None, x.clone(), None, ws[1:])
     with pytest.raises(R.RNNError):
         R.rnn_ssm_forward("softplus", x, x, A, bc, bc, None, None, None, None, None, x.clone(), None, ws[:512], "full")
+
+
+def test_calls_keep_their_place_on_the_stream():
+    """Inputs that arrive on a stream behind a long product, calls behind them, copies of the results behind those, and
+    nothing of the host between: every call waits for what comes before it and is done for what follows."""
+    c, n, v = ssm_case(500, 2, 70, 16, 1, "f32", seed=4), norm_case(300, 700, "f32", seed=4), conv_case(200, 3, 300, 4, "f32", seed=4)
+    want = {f"ssm.{k}": t for k, t in ssm_run("softplus", c).items()}
+    want |= {f"norm.{k}": t for k, t in norm_run("layer", n).items()}
+    want |= {f"conv.{k}": t for k, t in conv_run("silu", v).items()}
+    sources = {f"{p}.{k}": gpu(t) for p, d in (("ssm", c), ("norm", n), ("conv", v)) for k, t in d.items() if t is not None}
+    g = {k: torch.full_like(t, float("nan")) for k, t in sources.items()}
+    out = {k: torch.full_like(t, 7.0) for k, t in want.items()}
+    stats, big = torch.full((300, 2), 7.0, device="cuda"), torch.randn(4096, 4096, device="cuda")
+    sizes = (R.rnn_ssm_workspace_size(500, 2, 70, 16, 1, "full"), R.rnn_norm_workspace_size(300, 700), R.rnn_conv_workspace_size(200, 3, 300, 4))
+    ws, wn, wc = (room(s) for s in sizes)
+    copies = {k: torch.empty_like(t) for k, t in want.items()}
+    args = [g.get(f"ssm.{k}") for k in INPUTS]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(8):
+            big @ big
+        for k, t in sources.items():
+            g[k].copy_(t)
+        R.rnn_ssm_forward("softplus", *args, g["ssm.h0"], None, out["ssm.y"], out["ssm.hy"], ws, "full")
+        R.rnn_ssm_backward("softplus", *args, g["ssm.h0"], None, g["ssm.dy"], g["ssm.dhy"],
+                           *(out[f"ssm.{k}"] for k in ("du", "ddelta", "dA", "dBm", "dCm", "dD", "dz", "ddelta_bias", "dh0")), ws)
+        R.rnn_norm_forward("layer", g["norm.x"], g["norm.residual"], g["norm.weight"], g["norm.bias"], out["norm.y"], out["norm.total"], stats)
+        R.rnn_norm_backward("layer", out["norm.total"], g["norm.weight"], stats, g["norm.dy"], g["norm.dtotal"], out["norm.dx"],
+                            out["norm.dweight"], out["norm.dbias"], wn)
+        x = (g["conv.x"], g["conv.w"], g["conv.bias"], g["conv.s0"], None)
+        R.rnn_conv_forward("silu", *x, out["conv.y"], out["conv.sy"])
+        R.rnn_conv_backward("silu", *x, g["conv.dy"], g["conv.dsy"], *(out[f"conv.{k}"] for k in ("dx", "dw", "dbias", "ds0")), wc)
+        for k, t in out.items():
+            copies[k].copy_(t)
+    s.synchronize()
+    same(copies, want)

@@ -157,3 +157,10 @@ def test_steps_past_a_row_take_no_part_in_gradients(dtype, C):
     got = conv_run("none", c)
     for b, n in enumerate((45, 21, 1)):
         assert not got["dx"][n:, b].any() and not got["y"][n:, b].any()
+
+
+@pytest.mark.parametrize("dtype,K,act", [("f32", 6, "silu"), ("bf16", 7, "none"), ("f32", 8, "silu"), ("bf16", 8, "silu")])
+def test_long_pieces_of_wide_filters(dtype, K, act):
+    """Whole groups of steps without branches, whose first ones wait for K - 1 steps, for the widest filters."""
+    lengths = [300, 0, 1, 16, 17, 8, 24, 299] + [300 - i for i in range(84)]
+    compare(act, conv_case(300, 92, 257, K, dtype, lengths, seed=2), dtype)

@@ -106,3 +106,12 @@ def test_misaligned_rows():
         R.rnn_norm_forward("rms", x.clone(), None, None, None, want)
         R.rnn_norm_forward("rms", x, None, None, None, y)
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,D", [(600, 8195), (300, 16384), (150, 16400)])
+def test_several_long_rows_a_workgroup(kind, dtype, M, D):
+    """Workgroups of 1024 lanes that walk several rows, and sums by columns over every 64th row."""
+    print("CASE norm", kind, dtype, M, D, flush=True)
+    compare(kind, norm_case(M, D, dtype, seed=3), dtype)
