@@ -371,8 +371,7 @@ void pick(const NormParams& p, bool back, const Shape& sh, int blocks, hipStream
     if (BF || n == 4) return start<BF, 256, 4>(p, back, blocks, s);
     return start<BF, 256, BF ? 4 : 8>(p, back, blocks, s);
   }
-  if (BF || n == 2) return start<BF, 1024, 2>(p, back, blocks, s);   // more than 8192 columns
-  start<BF, 1024, BF ? 2 : 4>(p, back, blocks, s);
+  start<BF, 1024, BF ? 2 : 4>(p, back, blocks, s);                   // more than 8192 columns
 }
 
 // workgroups of the backward launch, and rows of partial sums

@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
     }
   } else {
     load_states(p.seg_first + at * NP + q.n, R, h);
-    for (int i = 0; i < q.seg * p.sub; ++i) {
+    for (int i = 0; i < q.seg; ++i) {
       float Q[R];
       const long long m = (long long)i * p.B * p.E + at;
       load_states(p.seg_q + m * NP + q.n, R, Q);
@@ -96,8 +96,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
 #pragma unroll
   for (int r = 0; r < R; ++r) A[r] *= kLog2e;
   const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
-  const int steps = LOCAL ? p.seg_steps / p.sub : p.seg_steps;
-  const int begin = min(q.seg * steps, p.T), stop = min(begin + steps, p.T), end = min(stop, q.len);
+  const int begin = min(q.seg * p.seg_steps, p.T), stop = min(begin + p.seg_steps, p.T), end = min(stop, q.len);
   SsmRows xu = ssm_rows<BF, Q>(p, q, p.u, p.ldu, begin), xd = ssm_rows<BF, Q>(p, q, p.delta, p.lddelta, begin),
           xz = ssm_rows<BF, Q>(p, q, p.z, p.ldz, begin), xy = ssm_rows<BF, Q>(p, q, p.y, p.ldy, begin);
   El<BF> ru[I], rd[I], rz[I] = {};
@@ -225,7 +224,7 @@ hipError_t start(const SsmParams& p, bool step, hipStream_t s) {
     hipLaunchKernelGGL((step_kernel<BF, S>), dim3(tiles), block, 0, s, p);
     return hipGetLastError();
   }
-  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true, PAD>), dim3(tiles * (p.segs - 1) * p.sub), block, 0, s, p);
+  if (p.segs > 1) hipLaunchKernelGGL((fwd_kernel<BF, S, true, PAD>), dim3(tiles * (p.segs - 1)), block, 0, s, p);
   hipLaunchKernelGGL((fwd_kernel<BF, S, false, PAD>), dim3(tiles * p.segs), block, 0, s, p);
   return hipGetLastError();
 }
@@ -249,14 +248,14 @@ hipError_t launch(const SsmParams& p, bool step, hipStream_t s) {
 
 }  // namespace
 
-// Segments of a pass with `tiles` waves a segment: one from `alone` waves on
-// (the first launch then costs more than the waiting of few waves: forward 0.25
-// against 0.29 ms with 1024 waves, backward 0.87 against 0.72), else as many as
-// fill the device with `fill` waves (forward 4 a SIMD: 264 us for the prompt
-// above, 281 with 2; backward 2, what its registers allow), of 32 steps at least.
-static int segments(long long tiles, int T, int alone, int fill) {
-  if (tiles == 0 || tiles >= alone) return 1;
-  return (int)std::max(1LL, std::min<long long>(fill / tiles, T / 32));
+// Segments of a pass with `tiles` waves a segment: as many as fill the device
+// (forward with 4 waves a SIMD: 264 us for the prompt above, 281 with 2; backward
+// with 2, what its registers allow: 0.72 ms for 1024 waves, 0.87 in one segment),
+// of 32 steps at least.  Forward one from 800 waves on: the first launch then
+// costs more than the waiting of few waves (0.25 against 0.29 ms with 1024).
+static int segments(long long tiles, int T, bool back) {
+  if (tiles == 0 || (!back && tiles >= 800)) return 1;
+  return (int)std::max(1LL, std::min<long long>((back ? 2048 : 4096) / tiles, T / 32));
 }
 
 long long rnnk::ssm_blocks(int B, int E, int N, int G) { return (long long)ssm_groups(E, G, ssm_lanes(N)) * G * B; }
@@ -267,13 +266,13 @@ SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
   const long long tiles = (long long)(E / G + CH - 1) / CH * G * B;
   size_t segs = 1;
   for (int back = 0; back < (save ? 2 : 1); ++back) {
-    const int n = back ? segments(tiles, T, 1300, 2048) : segments(tiles, T, 800, 4096);
-    // the first launch's waves hold less: it cuts the segments into parts until it
-    // has 2048 waves or more (backward of 1024 waves 110 -> 84 us)
+    const int n = segments(tiles, T, back);
+    // backward's first launch holds less in a wave: it cuts the segments into parts
+    // until it has 2048 waves or more (1024 waves 110 -> 84 us)
     int sub = 1;
-    while (n > 1 && tiles * (n - 1) * sub < 2048 && T / (n * sub) >= 64) sub *= 2;
+    while (back && n > 1 && tiles * (n - 1) * sub < 2048 && T / (n * sub) >= 64) sub *= 2;
     const int whole = step * sub;
-    r.sub[back] = sub;
+    if (back) r.sub = sub;
     r.seg_steps[back] = std::max(whole, ((T + n - 1) / n + whole - 1) / whole * whole);
     r.segs[back] = std::max(1, (T + r.seg_steps[back] - 1) / r.seg_steps[back]);
     if (r.segs[back] > 1) segs = std::max(segs, (size_t)r.segs[back] * sub);

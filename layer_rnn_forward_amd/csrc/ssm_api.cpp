@@ -78,7 +78,7 @@ size_t ssm_bytes(const SsmPlan& q) { return std::max(kAlign, q.all * 4); }
 void ssm_room(SsmParams& p, const SsmPlan& q, bool back, void* ws) {
   float* f = (float*)ws;
   p.segs = q.segs[back];
-  p.sub = q.sub[back];
+  p.sub = q.sub;
   p.seg_steps = q.seg_steps[back];
   p.seg_first = f + q.first;
   p.seg_q = f + q.q;

@@ -68,13 +68,14 @@ struct SsmParams {
   long long ldy;
   float* hy;
   float* starts;         // the state before every chunk of steps, or null
-  // segments of the time axis, the parts of a segment that the first launch
-  // walks, a segment's steps (whole chunks in each part); with more than one
-  // segment: the state that the first one starts from, the parts' maps
+  // segments of the time axis, the parts of a segment that backward's first
+  // launch walks, a segment's steps (whole chunks in each part); with more than
+  // one segment: the state that the first one starts from, the segments' or
+  // parts' maps
   int segs, sub, seg_steps;
   float* seg_first;      // [B][E][NP]
-  float* seg_q;          // [segs * sub][B][E][NP]
-  float* seg_d;          // [segs * sub][B][E]
+  float* seg_q;          // [segs (* sub)][B][E][NP]
+  float* seg_d;          // [segs (* sub)][B][E]
   const void* dy;        // backward, as what follows
   long long lddy;
   const float* dhy;
@@ -85,7 +86,7 @@ struct SsmParams {
 };
 // A call's segments (forward's or backward's) and the parts of the workspace, in floats
 struct SsmPlan {
-  int segs[2], sub[2], seg_steps[2];
+  int segs[2], seg_steps[2], sub;
   size_t starts, first, q, d, part, all;   // offsets; all: the size
 };
 long long ssm_blocks(int B, int E, int N, int G);   // workgroups of a segment
