@@ -96,6 +96,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
 #pragma unroll
   for (int r = 0; r < R; ++r) A[r] *= kLog2e;
   const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
+  const uint32_t skip = p.D ? ~0u : 0u;  // without D, no product of 0 and what may be infinite
   const int begin = min(q.seg * p.seg_steps, p.T), stop = min(begin + p.seg_steps, p.T), end = min(stop, q.len);
   SsmRows xu = ssm_rows<BF, Q>(p, q, p.u, p.ldu, begin), xd = ssm_rows<BF, Q>(p, q, p.delta, p.lddelta, begin),
           xz = ssm_rows<BF, Q>(p, q, p.z, p.ldz, begin), xy = ssm_rows<BF, Q>(p, q, p.y, p.ldy, begin);
@@ -191,8 +192,7 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
           }
         }
         if constexpr (!LOCAL) {
-          const float o = sum_to_lane<S, Q>(part);
-          y[i] = (p.D ? fmaf(D, u[i], o) : o) * gate[i];
+          y[i] = fmaf(D, masked(u[i], skip), sum_to_lane<S, Q>(part)) * gate[i];
           if (t0 + i * Q + q.j >= end) y[i] = 0.f;
         }
       }

@@ -124,6 +124,7 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
     }
   }
   const float bias = p.delta_bias ? p.delta_bias[q.e] : 0.f, D = p.D ? p.D[q.e] : 0.f;
+  const uint32_t skip = p.D ? ~0u : 0u;  // without D, no product of 0 and what may be infinite
   const int steps = LOCAL ? p.seg_steps / p.sub : p.seg_steps;
   const int begin = min(q.seg * steps, p.T), stop = min(begin + steps, p.T), end = min(stop, q.len);
   int t0 = begin + (end - begin + G - 1) / G * G - G;      // the last chunk with steps, if there is one
@@ -286,7 +287,7 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
             }
           }
           o[i] = sum_to_lane<S, Q>(part);
-          o[i] = p.D ? fmaf(D, u[i], o[i]) : o[i];   // (an infinite u times 0 would be NaN)
+          o[i] = fmaf(D, masked(u[i], skip), o[i]);
         }
         // backwards
         float (*const to)[2][NP] = sums[LOCAL ? 0 : t0 / G & 1][wave];
@@ -338,8 +339,7 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
         const bool on = t0 + i * Q + q.j < end;
         dD = fmaf(go[i], u[i], dD);
         dbias += on ? dd : 0.f;
-        const float du = d[i] * gB[i];
-        rows[0][i] = on ? (p.D ? fmaf(D, go[i], du) : du) : 0.f;
+        rows[0][i] = on ? fmaf(D, masked(go[i], skip), d[i] * gB[i]) : 0.f;
         rows[1][i] = on ? dd : 0.f;
         rows[2][i] = on ? o[i] * gz[i] : 0.f;
       }

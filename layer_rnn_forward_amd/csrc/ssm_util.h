@@ -86,6 +86,9 @@ __device__ __forceinline__ float sum_to_lane(float (&v)[Q]) {
   return sum_channel<4, S>(v[0]);
 }
 
+// v or, where the mask is 0, 0
+__device__ __forceinline__ float masked(float v, uint32_t mask) { return __uint_as_float(__float_as_uint(v) & mask); }
+
 // whether all lanes' values are finite
 template <int I>
 __device__ __forceinline__ bool all_finite(const float (&v)[I], const float (&w)[I]) {
