@@ -495,7 +495,8 @@ rnn_status_t rnn_checkpoint_load(void* stream, rnn_wtype_t wtype, int rows, int 
  * `ld` is given, the rows of a time-major tensor [T, B, width] (row t * B + b)
  * lie ld elements apart, so that it may be a slice of a wider one (ld >=
  * width, else INVALID_ARG).  Sums are fp32 with a fixed order.  Outputs past a
- * row's length are 0 and inputs there are not used, whatever they hold. */
+ * row's length are 0 and inputs there are not used, whatever they hold.  A
+ * workspace's size does for fewer rows and steps, too. */
 
 /* y = (s - m) * rstd * weight + bias  for each of M rows of D values, with
  *   RNN_NORM_LAYER  m = mean(s), rstd = 1 / sqrt(mean((s - m)^2) + eps)

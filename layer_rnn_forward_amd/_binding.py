@@ -671,7 +671,7 @@ def _rows(t, name, dev, dtype, shape, optional=False):
 
 
 def rnn_norm_workspace_size(M: int, D: int) -> int:
-    """Bytes of the workspace of rnn_norm_backward."""
+    """Bytes of the workspace of rnn_norm_backward (which does for fewer rows, too)."""
     _ints(M, D)
     n = ctypes.c_size_t()
     _check(load_library().rnn_norm_workspace_size(M, D, ctypes.byref(n)), "rnn_norm_workspace_size")
@@ -774,7 +774,7 @@ def rnn_conv_step(act, x, w, bias, s, y, sy):
 
 
 def rnn_conv_workspace_size(T: int, B: int, C: int, K: int) -> int:
-    """Bytes of the workspace of rnn_conv_backward."""
+    """Bytes of the workspace of rnn_conv_backward (which does for fewer steps and rows, too)."""
     _ints(T, B, C, K)
     n = ctypes.c_size_t()
     _check(load_library().rnn_conv_workspace_size(T, B, C, K, ctypes.byref(n)), "rnn_conv_workspace_size")
@@ -829,7 +829,7 @@ def _ssm_call(mode, u, delta, A, Bm, Cm, D, z, delta_bias, dims):
 
 def rnn_ssm_workspace_size(T: int, B: int, E: int, N: int, groups: int = 1, save: str = "none") -> int:
     """Bytes of the workspace of rnn_ssm_forward and, with save "full", of the
-    rnn_ssm_backward calls after it."""
+    rnn_ssm_backward calls after it (which does for fewer steps and rows, too)."""
     _ints(T, B, E, N, groups)
     n = ctypes.c_size_t()
     _check(load_library().rnn_ssm_workspace_size(T, B, E, N, groups, _choice(SSM_SAVES, save, "save"), ctypes.byref(n)),

@@ -394,6 +394,14 @@ long long rnnk::conv_blocks(int T, int B, int C, bool back) {
   return tiles * B * std::max(1LL, (T + steps - 1) / steps);
 }
 
+// At least the B * groups of pieces of a backward pass, and no fewer with more
+// steps or rows, so that a workspace does for fewer of both: a piece has at
+// least 8 steps and its share of 1024 * 3 waves.
+long long rnnk::conv_parts(int T, int B, int C) {
+  const long long tiles = std::max(1, (C + 64 * kWidth - 1) / (64 * kWidth)), waves = 1024 * 3 / kConvWaves;
+  return std::min((waves + tiles - 1) / tiles + 2LL * B, B * std::max(1LL, (T + 8LL * kConvWaves - 1) / (8 * kConvWaves)));
+}
+
 hipError_t rnn_launch_conv_fwd(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, FWD, bf16, s); }
 hipError_t rnn_launch_conv_step(const ConvParams& p, int bf16, hipStream_t s) { return launch(p, STEP, bf16, s); }
 hipError_t rnn_launch_conv_bwd(const ConvParams& q, int bf16, hipStream_t s) {

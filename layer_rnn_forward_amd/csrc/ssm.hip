@@ -263,8 +263,7 @@ long long rnnk::ssm_blocks(int B, int E, int N, int G) { return (long long)ssm_g
 SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
   SsmPlan r{};
   const int S = ssm_lanes(N), CH = 64 / S, step = ssm_chunk(S), NP = S * kSsmPer;
-  const long long tiles = (long long)(E / G + CH - 1) / CH * G * B;
-  size_t segs = 1;
+  const long long row = (long long)(E / G + CH - 1) / CH * G, tiles = row * B;   // waves of a row, of a segment
   for (int back = 0; back < (save ? 2 : 1); ++back) {
     const int n = segments(tiles, T, back);
     // backward's first launch holds less in a wave: it cuts the segments into parts
@@ -275,8 +274,13 @@ SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
     if (back) r.sub = sub;
     r.seg_steps[back] = std::max(whole, ((T + n - 1) / n + whole - 1) / whole * whole);
     r.segs[back] = std::max(1, (T + r.seg_steps[back] - 1) / r.seg_steps[back]);
-    if (r.segs[back] > 1) segs = std::max(segs, (size_t)r.segs[back] * sub);
   }
+  // The sizes follow from bounds of the above that do not fall with more steps or
+  // rows, so that a workspace does for fewer of both: there are several segments
+  // with up to 1024 waves a segment and 64 steps or more; n B <= 4096 / row
+  // forward, 2048 / row backward, and n sub B <= 8192 / row (the last doubling
+  // found less than 2048 waves in n - 1 segments), all at most B T / 32.
+  auto most = [&](long long waves) { return row ? std::min(waves / row, (long long)B * (T / 32)) : 0; };
   const size_t C = (size_t)B * E;
   size_t o = 0;
   auto take = [&o](size_t floats) {
@@ -285,14 +289,15 @@ SsmPlan rnnk::ssm_plan(int T, int B, int E, int N, int G, bool save) {
     return at;
   };
   if (save) r.starts = take(((size_t)T + kSsmKeep - 1) / kSsmKeep * C * NP);
-  if (segs > 1) {
-    r.first = take(C * NP);
-    r.q = take(segs * C * NP);
-    r.d = take(segs * C);
+  if (row > 0 && row <= 1024 && T >= 64) {
+    const size_t maps = most(save ? 8192 : 4096) * (size_t)E;
+    r.first = take(std::min<size_t>(B, 1024 / row) * E * NP);
+    r.q = take(maps * NP);
+    r.d = take(maps);
   }
   if (save) {
     const size_t groups = ssm_groups(E, G, S);
-    r.part = take((groups > 1 ? groups * T * B * G * 2 * NP : 0) + r.segs[1] * C * (NP + 2));
+    r.part = take((groups > 1 ? groups * T * B * G * 2 * NP : 0) + std::max((size_t)B, (size_t)most(2048)) * E * (NP + 2));
   }
   r.all = o;
   return r;

@@ -59,8 +59,7 @@ ConvParams conv_params(int act, int T, int B, int C, int K, bool back) {
   return p;
 }
 size_t conv_bytes(int T, int B, int C, int K) {
-  const ConvParams p = conv_params(RNN_ACT_NONE, T, B, C, K, true);
-  return std::max(kAlign, align_up((size_t)((p.pieces + kConvWaves - 1) / kConvWaves) * B * (K + 1) * C * 4));
+  return std::max(kAlign, align_up((size_t)conv_parts(T, B, C) * (K + 1) * C * 4));
 }
 
 // -------------------------------------------------------------------- ssm

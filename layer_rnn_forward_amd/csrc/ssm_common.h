@@ -56,6 +56,7 @@ struct ConvParams {
 constexpr int kConvWaves = 4;   // consecutive pieces of a workgroup
 int conv_piece(int T, int B, int C, bool back);
 long long conv_blocks(int T, int B, int C, bool back);   // workgroups of a launch
+long long conv_parts(int T, int B, int C);               // rows of partial sums that a workspace has room for
 
 constexpr int kSsmStates = 64;  // most states of a channel
 struct SsmParams {

@@ -274,3 +274,22 @@ def test_calls_keep_their_place_on_the_stream():
             copies[k].copy_(t)
     s.synchronize()
     same(copies, want)
+
+
+def test_workspaces_do_for_fewer_steps_and_rows():
+    """One workspace each, sized for the longest sequences of the largest batch, for all calls of a server."""
+    T, B, E, N, K = 700, 4, 90, 16, 4
+    ws, wc = room(R.rnn_ssm_workspace_size(T, B, E, N, 1, "full")), room(R.rnn_conv_workspace_size(T, B, E, K))
+    for t, b in ((700, 4), (545, 4), (33, 4), (65, 3), (699, 1), (1, 2), (512, 2)):
+        c, v = ssm_case(t, b, E, N, 1, "f32", seed=t), conv_case(t, b, E, K, "f32", seed=t)
+        want, g = ssm_run("softplus", c), {k: gpu(x) for k, x in c.items()}
+        got = {k: torch.full_like(x, 7.0) for k, x in want.items()}
+        args = [g[k] for k in INPUTS]
+        R.rnn_ssm_forward("softplus", *args, g["h0"], None, got["y"], got["hy"], ws, "full")
+        R.rnn_ssm_backward("softplus", *args, g["h0"], None, g["dy"], g["dhy"],
+                           *(got[k] for k in ("du", "ddelta", "dA", "dBm", "dCm", "dD", "dz", "ddelta_bias", "dh0")), ws)
+        same(got, want)
+        want, g = conv_run("silu", v), {k: gpu(x) for k, x in v.items()}
+        dw, db = torch.full_like(want["dw"], 7.0), torch.full_like(want["dbias"], 7.0)
+        R.rnn_conv_backward("silu", g["x"], g["w"], g["bias"], g["s0"], None, g["dy"], g["dsy"], None, dw, db, None, wc)
+        assert torch.equal(dw, want["dw"]) and torch.equal(db, want["dbias"])
