@@ -10,11 +10,12 @@
 // are added in a second launch, in a fixed order.
 //
 // Bound: memory (two values a step and channel forward, three backward).  2048
-// steps of 8 rows of 2048 channels, bf16, K = 4: forward 31 us, backward 50 us,
-// the sums 5 us (4.3 and 4.0 TB/s).  With a branch for every step and lane,
+// steps of 8 rows of 2048 channels, bf16, K = 4: forward 31 us, backward 51 us,
+// the sums 5 us (4.3 and 3.9 TB/s).  With a branch for every step and lane,
 // which makes each wait for loads one for the stores before them, too, 36 us
 // forward (32 without); with pieces of 32 steps backward (1.3 rounds of the waves
-// that fit) 67 us instead of 50.
+// that fit) 67 us instead of 50.  Channels past the last whole 256 take the walk
+// with the branches: 1237 x 7 packed x 357, fp32, K = 3: 7 and 12 us, the sums 4.
 
 #include <algorithm>
 #include <cmath>
@@ -382,8 +383,12 @@ hipError_t launch(const ConvParams& p, Pass what, int bf16, hipStream_t s) {
 
 }  // namespace
 
-// Steps of a wave's piece (at least K - 1 of them): as many as give each SIMD the
-// waves that its registers hold (4 forward, 3 backward), so that all run at once.
+// Steps of a wave's piece (at least K - 1 of them): as many as give each SIMD 4
+// waves forward and 3 backward, so that all run at once where its registers hold as
+// many: with K up to 4, and mostly with 5 and 6 forward, 5 backward.  Of wider filters
+// they hold 3 forward (K = 8; in fp32 7, too, and 5 with silu) and 2 backward (K = 7
+// and 8; 6 but for bf16 without silu; in fp32 5 with silu), so that a launch is up to
+// 1.5 rounds of what fits.
 int rnnk::conv_piece(int T, int B, int C, bool back) {
   const double steps = (double)B * ((C + 64 * kWidth - 1) / (64 * kWidth)) * T / (1024 * (back ? 3 : 4));
   return (int)std::min(std::max(1.0, std::ceil(steps / 8)), std::ceil(std::max(T, 1) / 8.0)) * 8;

@@ -9,7 +9,9 @@
 //
 // Bound: memory.  16384 rows of 2048, bf16, with residual: forward 47 us (5.7
 // TB/s: what it writes stays in the last cache level), backward 48 us, the sums 6
-// us; 4291 rows of 1357 in fp32: 12, 16 and 6 us.  16 rows: one launch of 3 us.
+// us; 4291 rows of 1357 in fp32: 12, 17 and 6 us.  16 rows: one launch of 3 us.
+// Backward with a bias gradient spills on rows of 8193 to 16384 columns (1024
+// lanes, 128 registers each): 74 registers in fp32, 6 in bf16.
 #include <algorithm>
 
 #include "ssm_common.h"

@@ -7,7 +7,7 @@
 // ones, 6 issue slots of the 10 that a pass takes in all.  The memory's time is
 // less than half of the pass's (in bf16 8 bytes a step and channel, 16 in
 // training with the states kept).  2048 steps of 8 rows of 2048 channels, bf16,
-// training: 0.23 ms, 1.7 times the slots' own time (0.136 ms at 2.4 GHz), since
+// training: 0.23 ms, 1.7 times the slots' own time (0.137 ms at 2.4 GHz), since
 // this is one wave a SIMD, which waits for its own results; cut into 4 segments
 // the same walk takes 0.19 ms but the segments' first launch 0.10.  A prompt of
 // 8192 steps of 3520 channels (220 waves a segment, 18 segments): 0.11 + 0.15 ms.
@@ -16,6 +16,10 @@
 // pieces of a block that the waves of a workgroup exchange, so that states are
 // walked twice but exponentials computed once, 0.56 ms; 2 states a lane (twice
 // the waves) 0.28 where 4 took 0.24.
+//
+// The last segment composes the maps of all before it, one after the other, each
+// with a round trip to memory: 16384 steps of 16 channels (512 segments) take 6 us
+// in the first launch and 142 in the second.
 
 #include <algorithm>
 
@@ -162,8 +166,11 @@ __global__ __launch_bounds__(64 * kSsmTiles) void fwd_kernel(const SsmParams p) 
     };
     read(0);
     // GUARD: states that are not there are held at 0 (an infinite d or du would
-    // make them NaN, 0 times it, and through them the sum over the states).  The
-    // empty asm statement keeps the compiler from sharing the ways' values.
+    // make them NaN, 0 times it, and through them the sum over the states), in a
+    // way of its own: 13 states of the training pass above 0.25 ms instead of 0.27
+    // with selects in every chunk.  The empty asm statement keeps the compiler from
+    // sharing the ways' values (with what they share computed before the branch
+    // 199 registers instead of 144).
     const bool usual = !PAD || all_finite(d, du);
 #pragma unroll
     for (int way = 0; way < (PAD ? 2 : 1); ++way) {

@@ -12,12 +12,19 @@
 // adds the parameters' gradients of the rows and segments, too.  All in a fixed
 // order.
 //
-// Bound: vector instructions, 105 of them a step and wave (256 states).  2048
-// steps of 8 rows of 2048 channels, bf16: 0.49 ms in two segments (their issue
+// Bound: vector instructions, 107 of them a step and wave (256 states).  2048
+// steps of 8 rows of 2048 channels, bf16: 0.51 ms in two segments (their issue
 // slots alone 0.40 at 2.4 GHz), the segments' first launch 0.07, the sums of dB
-// and dC 0.02.  Two waves a SIMD (195 registers): with three (168 registers and
+// and dC 0.02.  Two waves a SIMD (204 registers): with three (168 registers and
 // 108 bytes spilled) 0.73 ms where two took 0.57, with one segment of one wave a
 // SIMD 0.87 where two took 0.61 + 0.11.  Chunks of 16 steps spill: 1.6 ms.
+//
+// What spills all the same: 79 (16 states) to 149 scalar registers, most of them
+// the addresses and strides of the seven tensors that are walked, into lanes of
+// vector registers, which every chunk reads back; and with one lane a
+// channel (up to 4 states), where a lane owns all 8 steps of a chunk, 76 to 98 of
+// 256 vector registers (160 to 204 bytes of scratch): 4 states a channel take as
+// long as 16 (0.82 ms for the same pass).
 #include <algorithm>
 
 #include "ssm_util.h"
@@ -237,9 +244,9 @@ __global__ __launch_bounds__(64 * kSsmTiles, 2) void bwd_kernel(const SsmParams 
       // GUARD: states that are not there and their gradients are held at 0 (an
       // infinite d, du or do would make them NaN, 0 times it), and steps past the
       // end add nothing to dA (an infinite state would, 0 times it): a way of its
-      // own, since selects in every chunk cost more (16 states 840 us instead of 827
-      // for a training pass of 2048 x 8 x 2048; with one lane a channel, where the
-      // second way spills more registers, 808 instead of 937).
+      // own, since selects in every chunk cost more (a training pass of 2048 x 8 x
+      // 2048 with 16 states 840 us instead of 832; with one lane a channel, where
+      // the second way spills more registers, 808 instead of 937).
       float o[I], gB[I], gA[I];
       constexpr bool ENDS = !LOCAL && S > 1;
       const bool usual = (!ENDS || t0 + G <= end) && (!PAD || (all_finite(d, du) && all_finite(go, go)));
