@@ -239,9 +239,10 @@ __device__ __forceinline__ void put_bc(float* to, const RawFour<BF> (&v)[bc_piec
     }
 }
 
-// a state through a map: P from the sum of d, twice its root
+// a state through a map: P from the sum of d, twice its root (which is held above
+// 0, so that an infinite state stays so; of finite ones its square leaves nothing)
 __device__ __forceinline__ float through(float A, float sum, float Q, float h) {
-  const float P = __builtin_amdgcn_exp2f(fminf(0.5f * kLog2e * A * sum, 127.f));
+  const float P = fmaxf(__builtin_amdgcn_exp2f(fminf(0.5f * kLog2e * A * sum, 127.f)), 0x1p-149f);
   return fmaf(P, P * h, Q);
 }
 

@@ -371,3 +371,19 @@ def test_sums_over_several_workgroups_and_parts(dtype, E, N, G):
     batches, and several workgroups a group."""
     print("CASE ssm parts", dtype, E, N, G, flush=True)
     compare("softplus", ssm_case(130, 1, E, N, G, dtype, [117], seed=17), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [4, 13, 16])
+def test_infinite_states_stay_infinite_over_segments(dtype, N):
+    """Segments whose decay is far below fp32's range, after an infinite input or before an infinite gradient: infinity
+    times a decay, not times 0."""
+    c = positive(400, N, dtype, seed=18)
+    c["A"] *= 20.0
+    c["delta"][:] = 0.5
+    c["u"][30, 1, 4] = float("inf")
+    got, _ = compare_infinite(c, dtype)
+    assert got["y"][30:, 1, 4].isinf().all() and got["hy"][1, 4].isinf().all()
+    c["u"][30, 1, 4], c["dhy"][1, 5] = 0.5, float("inf")
+    got = ssm_run("linear", c)
+    assert got["dh0"][1, 5].isinf().all() and got["du"][:, 1, 5].isinf().all()
